@@ -63,6 +63,11 @@ extern "C" {
                                          affected tile are undefined                       */
 #define MLA_STATUS_SLOT_RANGE     0x4 /* mla_prolog_run_cached: some slot_mapping[t] was
                                          >= num_slots; that token's cache row was skipped  */
+#define MLA_STATUS_SEQ_RANGE      0x8 /* a sequence offset, length or index was outside its
+                                         buffer (see each call for what it does then)      */
+#define MLA_STATUS_PAGE_RANGE    0x10 /* a page index was outside [0, num_pages)           */
+#define MLA_STATUS_POOL_FULL     0x20 /* mla_prolog_pages_*: the free pages, or the columns
+                                         of the page table, did not suffice                */
 
 /* ---- dims flags --------------------------------------------------------- */
 #define MLA_PROLOG_QUANT_Q 0x1u /* q path emits INT8 codes + FP32 per-token scales.
@@ -529,6 +534,235 @@ int mla_prolog_plan(const mla_prolog_dims* dims, int32_t sms, mla_prolog_plan_in
  * cost).
  */
 int mla_prolog_lpt(const int64_t* cost, int32_t n, int32_t groups, int32_t* table, int64_t* busiest);
+
+/* ---- attention over the prolog's outputs -------------------------------- */
+
+/*
+ * Attention over whole prompts: each query of a packed batch of sequences
+ * attends to its own sequence's keys, head by head, on the per-head K and V
+ * that mla_prolog_run() writes.
+ *
+ *   s_ij  = scale * q_scale_i * <q_i, k_j>
+ *   out_i = sum_j softmax_j(s_ij) v_j,    lse_i = log sum_j exp(s_ij)
+ *
+ * over the allowed keys j: those of i's sequence and, with
+ * MLA_PROMPT_CAUSAL, j <= i + (Lk - Lq) (i, j counted within the sequence;
+ * Lq, Lk its query and key rows: the queries are the LAST Lq of the Lk
+ * tokens, so a chunk of a prompt attends to the tokens before it).  A query
+ * without an allowed key gets out = 0 and lse = -inf.  Keys that are not
+ * allowed never reach a result, whatever they hold (NaN and infinities
+ * included).  Grouped heads: query head h reads key head
+ * h / (num_heads / kv_heads).
+ *
+ * The products run on BF16 operands with FP32 sums; softmax statistics and
+ * the output sums are FP32; the probabilities are rounded to BF16 for the
+ * product with v, and out once at the end.
+ *
+ * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): Tq, Tk, sequences >= 0;
+ * kv_heads >= 1 divides num_heads; qk_dim and v_dim positive multiples of 16,
+ * qk_dim <= 256, v_dim <= 128; num_heads <= 65535; scale finite and > 0.
+ */
+#define MLA_PROMPT_CAUSAL           0x1u /* the causal rule above; without it every key of
+                                            the sequence is allowed                         */
+#define MLA_PROMPT_Q_INT8           0x2u /* q holds INT8 codes and q_scale their scales, as
+                                            out_q_int8 and out_scale of mla_prolog_run()    */
+#define MLA_PROMPT_Q_SCALE_PER_HEAD 0x4u /* q_scale is [Tq, num_heads] (with Q_INT8 only)   */
+
+typedef struct mla_prolog_prompt_dims {
+    int32_t  Tq;         /* rows of q, out and lse                                  */
+    int32_t  Tk;         /* rows of k and v                                         */
+    int32_t  sequences;  /* packed sequences                                        */
+    int32_t  num_heads;
+    int32_t  kv_heads;
+    int32_t  qk_dim;     /* Dn + R                                                  */
+    int32_t  v_dim;      /* Dv                                                      */
+    float    scale;      /* softmax scale                                           */
+    uint32_t flags;      /* OR of MLA_PROMPT_*                                      */
+} mla_prolog_prompt_dims;
+
+/*
+ *   q        BF16 [Tq, num_heads, qk_dim], or int8 with MLA_PROMPT_Q_INT8
+ *   q_scale  FP32 [Tq], or [Tq, num_heads] with Q_SCALE_PER_HEAD; NULL for BF16 q
+ *   k        BF16 [Tk, kv_heads, qk_dim]
+ *   v        BF16 [Tk, kv_heads, v_dim]
+ *   cu_q     int32 [sequences + 1]: sequence s holds rows cu_q[s] .. cu_q[s+1] - 1
+ *            of q, out and lse (0 <= cu_q[s] <= cu_q[s+1] <= Tq)
+ *   cu_k     int32 [sequences + 1]: the same for k and v (may be cu_q itself)
+ *   out      BF16 [Tq, num_heads, v_dim]
+ *   lse      FP32 [Tq, num_heads]; may be NULL
+ *   status   int32 (device); MLA_STATUS_* bits are ORed in; may be NULL
+ * Rows of out and lse that belong to no sequence are left as they were.  A
+ * sequence whose offsets break the rule above is cut to its part inside the
+ * buffers (none if they decrease) and sets MLA_STATUS_SEQ_RANGE.  No
+ * workspace; calls on different streams may overlap.  Inputs and outputs must
+ * not overlap.  Errors: INVALID_ARG, UNSUPPORTED_DIMS, DEVICE, CUDA.
+ */
+int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* dims, const void* q, const float* q_scale, const void* k,
+                             const void* v, const int32_t* cu_q, const int32_t* cu_k, void* out, float* lse,
+                             int32_t* status, void* stream);
+
+/*
+ * One decoding step over the latent KV cache: one query token per sequence,
+ * every head on the cache row [c_kv (Lkv) | k_pe (R)] that
+ * mla_prolog_run_cached() writes (the absorbed form: the query carries W_UK,
+ * and the caller applies W_UV to the result).
+ *
+ *   s_j = scale * <q, row_j>,  out = sum_j softmax_j(s_j) row_j[0 .. Lkv),
+ *   lse = log sum_j exp(s_j),   j = 0 .. seq_lens[b] - 1
+ *
+ * row_j is the row of slot page_table[b][j / page_size] * page_size +
+ * j % page_size of the cache.  The keys of a prefix that the batch shares
+ * are read and multiplied once for all rows of the batch: with
+ * *shared_len = n > 0 the caller states that the sequences of at least n
+ * tokens have the same pages under their first n tokens (as
+ * mla_prolog_pages_fork() leaves them).  Sequences shorter than n (a padded
+ * batch's empty rows among them) are handled on their own.  A sequence of
+ * length 0 gets out = 0 and lse = -inf.  Rows past a sequence's end never
+ * reach a result, whatever they hold.
+ *
+ * Precision as mla_prolog_attend_prompt(); partial results of a key range
+ * are kept in FP32 and joined in a fixed order, so equal inputs give equal
+ * bits.
+ *
+ * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): batch >= 0, num_heads >= 1,
+ * batch * num_heads <= 2^24; Lkv a positive multiple of 16 up to 512, R a
+ * multiple of 16 (0 .. 128) with Lkv + R <= 576; page_size a positive
+ * multiple of 16; num_pages * page_size <= 2^31 - 1; max_pages >= 1 and
+ * max_pages * page_size <= 2^30; table_rows >= 0; scale finite and > 0.
+ */
+typedef struct mla_prolog_cache_dims {
+    int32_t batch;         /* rows of q                                             */
+    int32_t num_heads;
+    int32_t kv_lora_rank;  /* Lkv                                                   */
+    int32_t rope_dim;      /* R                                                     */
+    int32_t page_size;     /* cache rows (tokens) per page                          */
+    int32_t table_rows;    /* rows of page_table and seq_lens                       */
+    int32_t max_pages;     /* columns of page_table                                 */
+    float   scale;         /* softmax scale                                         */
+    int64_t num_pages;     /* pages of the cache                                    */
+} mla_prolog_cache_dims;
+
+/*
+ *   q           BF16 [batch, num_heads, Lkv + R]
+ *   kv_cache    BF16 [num_pages, page_size, Lkv + R]
+ *   page_table  int32 [table_rows, max_pages]
+ *   seq_lens    int32 [table_rows], tokens of each sequence (0 <= n <= max_pages * page_size)
+ *   seqs        int32 [batch]: the table row of each batch row; NULL: row b is
+ *               table row b (then table_rows >= batch)
+ *   shared_len  int32 [1], see above; NULL: no shared prefix
+ *   out         BF16 [batch, num_heads, Lkv]
+ *   lse         FP32 [batch, num_heads]; may be NULL
+ *   workspace   16-byte aligned, at least mla_prolog_attend_cache_workspace()
+ *               bytes; its contents need not be kept between calls.  Calls that
+ *               may overlap (two streams, two captured graphs) need one each.
+ *   status      int32; MLA_STATUS_* bits are ORed in; may be NULL
+ * All device pointers; lengths and tables are read on the device, so a
+ * captured call follows them.  A seqs entry or length outside its range is
+ * cut to it (the entry: an empty sequence) and sets MLA_STATUS_SEQ_RANGE; a
+ * page outside [0, num_pages) reads as rows of zeros and sets
+ * MLA_STATUS_PAGE_RANGE.  Errors: INVALID_ARG, UNSUPPORTED_DIMS, DEVICE, CUDA.
+ */
+int mla_prolog_attend_cache(const mla_prolog_cache_dims* dims, const void* q, const void* kv_cache,
+                            const int32_t* page_table, const int32_t* seq_lens, const int32_t* seqs,
+                            const int32_t* shared_len, void* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* status, void* stream);
+
+/* Bytes of workspace that mla_prolog_attend_cache() needs for these dims on
+ * the current device (only batch, num_heads, kv_lora_rank and rope_dim
+ * count).  Errors: INVALID_ARG, UNSUPPORTED_DIMS, CUDA. */
+int mla_prolog_attend_cache_workspace(const mla_prolog_cache_dims* dims, size_t* bytes);
+
+/* ---- pages of the latent cache ------------------------------------------ */
+
+/*
+ * A pool of cache pages, kept by three device arrays that the caller owns.
+ * Sequence s of length n = seq_lens[s] holds the pages page_table[s][0 ..
+ * ceil(n / page_size)); its token j lies in slot page_table[s][j / page_size]
+ * * page_size + j % page_size of every layer's cache.  refs[p] counts the
+ * table entries that hold page p; a page with refs 0 is free, and the lowest
+ * free pages are taken first, so equal states give equal results.  Table
+ * entries behind a sequence's pages are -1.  The calls below move whole
+ * numbers only; mla_prolog_copy_pages() moves the cache's contents.
+ * Calls on one pool must be ordered (one stream).
+ * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): sequences, num_pages >= 0;
+ * page_size, max_pages >= 1; num_pages * page_size and max_pages * page_size
+ * <= 2^31 - 1; lists of 0 .. 1024 entries.
+ * Errors of all: INVALID_ARG, UNSUPPORTED_DIMS, CUDA.
+ */
+typedef struct mla_prolog_pool {
+    int32_t  sequences;   /* rows of page_table                                   */
+    int32_t  max_pages;   /* its columns                                          */
+    int32_t  page_size;   /* tokens per page                                      */
+    int32_t  num_pages;
+    int32_t* page_table;  /* int32 [sequences, max_pages]                         */
+    int32_t* seq_lens;    /* int32 [sequences]                                    */
+    int32_t* refs;        /* int32 [num_pages]                                    */
+    int32_t* status;      /* int32, MLA_STATUS_* bits are ORed in; may be NULL    */
+} mla_prolog_pool;
+
+/*
+ * Grows sequence seqs[i] by counts[i] tokens, i = 0 .. n - 1, taking free
+ * pages in the order of the list.  The slots of the new tokens, sequence
+ * after sequence, go to slot_mapping (as mla_prolog_run_cached() takes it)
+ * and their places in the sequence to positions; entry i starts at the sum of
+ * the counts before it, and entries of either buffer from the sum of all
+ * counts up to `total` (the length of both) are set to -1 and 0, which marks
+ * padding tokens.  An entry that does not fit is left out whole: its sequence
+ * stays as it was, its slots are -1, and MLA_STATUS_POOL_FULL is set.  It does
+ * not fit when its tokens need more than max_pages columns, or when the needs
+ * of the entries up to it (those that fit the columns) sum to more than the
+ * free pages.
+ * A sequence listed twice, or outside [0, sequences), or a negative count, is
+ * left out with MLA_STATUS_SEQ_RANGE (the first listing counts).  Tokens
+ * beyond `total` get a page but no slot, and set MLA_STATUS_SLOT_RANGE.
+ * slot_mapping and positions may each be NULL.
+ */
+int mla_prolog_pages_extend(const mla_prolog_pool* pool, const int32_t* seqs, const int32_t* counts, int32_t n,
+                            int32_t* slot_mapping, int32_t* positions, int32_t total, void* stream);
+
+/*
+ * Makes sequence children[i] a copy of parents[i]: full pages are shared
+ * (refs + 1), a last page that is not full gets a page of its own, and
+ * (copy_src[i], copy_dst[i]) names that copy for mla_prolog_copy_pages()
+ * (-1, -1 where none is due).  One parent may have several children in a
+ * call.  A child has to be empty before the call and be listed once; a child
+ * that is not, or an index outside [0, sequences), is left out with
+ * MLA_STATUS_SEQ_RANGE (of two equal children the first counts), one without
+ * a free page with MLA_STATUS_POOL_FULL; the call reads every parent as it
+ * was before.
+ */
+int mla_prolog_pages_fork(const mla_prolog_pool* pool, const int32_t* parents, const int32_t* children, int32_t n,
+                          int32_t* copy_src, int32_t* copy_dst, void* stream);
+
+/*
+ * Ends sequences seqs[0 .. n): refs - 1 for each of their pages, length 0,
+ * table row -1.  A sequence listed twice ends once; an index outside
+ * [0, sequences) is left out with MLA_STATUS_SEQ_RANGE.
+ */
+int mla_prolog_pages_release(const mla_prolog_pool* pool, const int32_t* seqs, int32_t n, void* stream);
+
+/*
+ * Moves the L live pages to the pages 0 .. L - 1: the j-th live page at or
+ * above L goes to the j-th free page below L, the others stay.  moved_to
+ * (int32 [num_pages]) receives each live page's new place (its own where it
+ * stays) and -1 for free pages; live (int32 [1], may be NULL) receives L.
+ * page_table and refs follow; mla_prolog_copy_pages(.., NULL, moved_to,
+ * num_pages) moves the contents.
+ */
+int mla_prolog_pages_compact(const mla_prolog_pool* pool, int32_t* moved_to, int32_t* live, void* stream);
+
+/*
+ * Copies whole pages within each of `layers` caches that lie `layer_stride`
+ * bytes apart: page src[i] to page dst[i], i = 0 .. n - 1 (src NULL: page i).
+ * An entry with a negative src or dst, or src == dst, is skipped; one at or
+ * above num_pages is skipped and sets MLA_STATUS_PAGE_RANGE in *status (may
+ * be NULL).  No dst may be listed twice or be another entry's src (the order
+ * of the copies is not specified).  page_bytes a positive multiple of 16;
+ * cache and layer_stride (>= num_pages * page_bytes for two layers or more)
+ * 16-byte aligned; 0 <= layers <= 65535.
+ */
+int mla_prolog_copy_pages(void* cache, int32_t layers, int64_t layer_stride, int64_t num_pages, int64_t page_bytes,
+                          const int32_t* src, const int32_t* dst, int32_t n, int32_t* status, void* stream);
 
 #ifdef __cplusplus
 }

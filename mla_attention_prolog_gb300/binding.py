@@ -26,6 +26,12 @@ MLA_PROLOG_W8A8 = 16
 STATUS_POSITION_RANGE = 0x1
 STATUS_WAIT_TIMEOUT = 0x2
 STATUS_SLOT_RANGE = 0x4
+STATUS_SEQ_RANGE = 0x8
+STATUS_PAGE_RANGE = 0x10
+STATUS_POOL_FULL = 0x20
+MLA_PROMPT_CAUSAL = 1
+MLA_PROMPT_Q_INT8 = 2
+MLA_PROMPT_Q_SCALE_PER_HEAD = 4
 
 EXPORTED = [
     "mla_prolog_create", "mla_prolog_run", "mla_prolog_destroy", "mla_prolog_device_status",
@@ -35,6 +41,9 @@ EXPORTED = [
     "mla_prolog_workspace_bytes", "mla_prolog_schedule", "mla_prolog_copy_tap", "mla_prolog_set_tuning",
     "mla_prolog_run_noalloc", "mla_prolog_run_cached", "mla_prolog_plan", "mla_prolog_lpt",
     "mla_prolog_load_w8a8",
+    "mla_prolog_attend_prompt", "mla_prolog_attend_cache", "mla_prolog_attend_cache_workspace",
+    "mla_prolog_pages_extend", "mla_prolog_pages_fork", "mla_prolog_pages_release", "mla_prolog_pages_compact",
+    "mla_prolog_copy_pages",
 ]
 TAP_NORMED, TAP_Q, TAP_AMAX = 1, 2, 3
 TAP_X_CODES, TAP_X_SCALE, TAP_NORM_SCALE = 4, 5, 6
@@ -65,6 +74,23 @@ class MlaPrologPlanInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "decode", "bn_a", "splits_a", "group_a", "compress_jobs", "bn_kv", "kv_halves")] + \
         [("busiest_bytes", ctypes.c_int64)]
+
+
+class MlaPrologPromptDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "Tq", "Tk", "sequences", "num_heads", "kv_heads", "qk_dim", "v_dim")] + \
+        [("scale", ctypes.c_float), ("flags", ctypes.c_uint32)]
+
+
+class MlaPrologCacheDims(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "batch", "num_heads", "kv_lora_rank", "rope_dim", "page_size", "table_rows", "max_pages")] + \
+        [("scale", ctypes.c_float), ("num_pages", ctypes.c_int64)]
+
+
+class MlaPrologPool(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("sequences", "max_pages", "page_size", "num_pages")] + \
+        [(n, ctypes.c_void_p) for n in ("page_table", "seq_lens", "refs", "status")]
 
 
 class MlaPrologError(RuntimeError):
@@ -112,6 +138,14 @@ def lib(path: Optional[str] = None):
     L.mla_prolog_plan.argtypes = [P(MlaPrologDims), I32, P(MlaPrologPlanInfo)]
     L.mla_prolog_lpt.argtypes = [P(ctypes.c_int64), I32, I32, P(I32), P(ctypes.c_int64)]
     L.mla_prolog_load_w8a8.argtypes = [V, V, V, V, V]
+    L.mla_prolog_attend_prompt.argtypes = [P(MlaPrologPromptDims)] + [V] * 10
+    L.mla_prolog_attend_cache.argtypes = [P(MlaPrologCacheDims)] + [V] * 9 + [ctypes.c_size_t, V, V]
+    L.mla_prolog_attend_cache_workspace.argtypes = [P(MlaPrologCacheDims), P(ctypes.c_size_t)]
+    L.mla_prolog_pages_extend.argtypes = [P(MlaPrologPool), V, V, I32, V, V, I32, V]
+    L.mla_prolog_pages_fork.argtypes = [P(MlaPrologPool), V, V, I32, V, V, V]
+    L.mla_prolog_pages_release.argtypes = [P(MlaPrologPool), V, I32, V]
+    L.mla_prolog_pages_compact.argtypes = [P(MlaPrologPool), V, V, V]
+    L.mla_prolog_copy_pages.argtypes = [V, I32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, V, V, I32, V, V]
     for n in EXPORTED:
         if n not in ("mla_prolog_strerror", "mla_prolog_last_cuda_error", "mla_prolog_kernel_count",
                      "mla_prolog_kernel_name"):
@@ -331,3 +365,148 @@ def lpt(cost: Sequence[int], groups: int):
     offs = list(table[:groups + 1])
     ids = list(table[groups + 1:])
     return [ids[offs[g]:offs[g + 1]] for g in range(groups)], busiest.value
+
+
+def _on(t: torch.Tensor, name: str, dims: int) -> torch.device:
+    """The device that the other tensors of a call have to be on."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
+    return t.device
+
+
+def _stream_on(device, stream: Optional[torch.cuda.Stream]) -> Optional[int]:
+    s = stream if stream is not None else torch.cuda.current_stream(device)
+    if s.device != device:
+        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
+    return s.cuda_stream or None
+
+
+def attend_prompt(q, k, v, cu_q, cu_k, out, lse=None, *, scale: float, causal: bool = True, q_scale=None,
+                  status=None, stream=None) -> None:
+    """Attention of a packed batch of prompts over per-head K and V
+    (``mla_prolog_attend_prompt``): q BF16 [Tq, H, Dqk], or int8 codes with
+    ``q_scale`` [Tq] or [Tq, H]; k [Tk, Hk, Dqk], v [Tk, Hk, Dv]; cu_q, cu_k
+    int32 [sequences + 1]; out BF16 [Tq, H, Dv], lse FP32 [Tq, H]."""
+    dev = _on(q, "q", 3)
+    (Tq, H, Dqk), _, _ = q.shape, _on(k, "k", 3), _on(v, "v", 3)
+    Tk, Hk, Dv, n = k.shape[0], k.shape[1], v.shape[2], cu_q.numel() - 1
+    if n < 0:
+        raise ValueError("cu_q must have at least one entry")
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    flags = MLA_PROMPT_CAUSAL if causal else 0
+    scale_shape = (Tq,)
+    if q_scale is not None:
+        flags |= MLA_PROMPT_Q_INT8
+        if q_scale.dim() == 2:
+            flags |= MLA_PROMPT_Q_SCALE_PER_HEAD
+            scale_shape = (Tq, H)
+    d = MlaPrologPromptDims(Tq, Tk, n, H, Hk, Dqk, Dv, scale, flags)
+    args = [_ptr(q, "q", torch.int8 if q_scale is not None else bf, (Tq, H, Dqk), dev),
+            _ptr(q_scale, "q_scale", f32, scale_shape, dev), _ptr(k, "k", bf, (Tk, Hk, Dqk), dev),
+            _ptr(v, "v", bf, (Tk, Hk, Dv), dev), _ptr(cu_q, "cu_q", i32, (n + 1,), dev),
+            _ptr(cu_k, "cu_k", i32, (n + 1,), dev), _ptr(out, "out", bf, (Tq, H, Dv), dev),
+            _ptr(lse, "lse", f32, (Tq, H), dev), _ptr(status, "status", i32, (1,), dev)]
+    with torch.cuda.device(dev):
+        _check(lib().mla_prolog_attend_prompt(ctypes.byref(d), *args, _stream_on(dev, stream)),
+               "mla_prolog_attend_prompt")
+
+
+def attend_cache_workspace_bytes(batch: int, num_heads: int, kv_lora_rank: int, rope_dim: int) -> int:
+    """Workspace bytes of ``attend_cache`` for these sizes on the current device."""
+    d = MlaPrologCacheDims(batch, num_heads, kv_lora_rank, rope_dim, 16, batch, 1, 1.0, 0)
+    v = ctypes.c_size_t(0)
+    _check(lib().mla_prolog_attend_cache_workspace(ctypes.byref(d), ctypes.byref(v)), "attend_cache_workspace")
+    return int(v.value)
+
+
+def attend_cache(q, kv_cache, page_table, seq_lens, out, lse, workspace, *, scale: float, seqs=None, shared_len=None,
+                 status=None, stream=None) -> None:
+    """One decoding step over the paged latent cache
+    (``mla_prolog_attend_cache``): q BF16 [B, H, Lkv + R]; kv_cache BF16
+    [num_pages, page_size, Lkv + R]; page_table int32 [S, max_pages]; seq_lens
+    int32 [S]; seqs int32 [B] (None: row b is sequence b); shared_len int32 [1];
+    out BF16 [B, H, Lkv]; lse FP32 [B, H] or None; workspace uint8 of at least
+    ``attend_cache_workspace_bytes``."""
+    dev = _on(q, "q", 3)
+    (B, H, C), _, _ = q.shape, _on(kv_cache, "kv_cache", 3), _on(page_table, "page_table", 2)
+    _on(out, "out", 3), _on(workspace, "workspace", 1)
+    pages, page_size, Lkv, (S, width) = kv_cache.shape[0], kv_cache.shape[1], out.shape[2], page_table.shape
+    bf, i32 = torch.bfloat16, torch.int32
+    d = MlaPrologCacheDims(B, H, Lkv, C - Lkv, page_size, S, width, scale, pages)
+    args = [_ptr(q, "q", bf, (B, H, C), dev), _ptr(kv_cache, "kv_cache", bf, (pages, page_size, C), dev),
+            _ptr(page_table, "page_table", i32, (S, width), dev), _ptr(seq_lens, "seq_lens", i32, (S,), dev),
+            _ptr(seqs, "seqs", i32, (B,), dev), _ptr(shared_len, "shared_len", i32, (1,), dev),
+            _ptr(out, "out", bf, (B, H, Lkv), dev), _ptr(lse, "lse", torch.float32, (B, H), dev),
+            _ptr(workspace, "workspace", torch.uint8, tuple(workspace.shape), dev), workspace.numel(),
+            _ptr(status, "status", i32, (1,), dev)]
+    with torch.cuda.device(dev):
+        _check(lib().mla_prolog_attend_cache(ctypes.byref(d), *args, _stream_on(dev, stream)), "mla_prolog_attend_cache")
+
+
+class PagePool:
+    """The pool calls (``mla_prolog_pages_*``) on the caller's page_table int32
+    [S, max_pages], seq_lens int32 [S], refs int32 [num_pages] and, optionally,
+    status int32 [1]."""
+
+    def __init__(self, page_table, seq_lens, refs, page_size: int, status=None):
+        self.device = _on(page_table, "page_table", 2)
+        S, width = page_table.shape
+        i32 = torch.int32
+        self._tensors = (page_table, seq_lens, refs, status)
+        self._pool = MlaPrologPool(S, width, page_size, refs.numel(), _ptr(page_table, "page_table", i32, (S, width), self.device),
+                                   _ptr(seq_lens, "seq_lens", i32, (S,), self.device),
+                                   _ptr(refs, "refs", i32, (refs.numel(),), self.device),
+                                   _ptr(status, "status", i32, (1,), self.device))
+
+    def _list(self, t, name, n):
+        return _ptr(t, name, torch.int32, (n,), self.device)
+
+    def _call(self, name, *args, stream):
+        with torch.cuda.device(self.device):
+            _check(getattr(lib(), name)(ctypes.byref(self._pool), *args, _stream_on(self.device, stream)), name)
+
+    def extend(self, seqs, counts, slot_mapping=None, positions=None, stream=None) -> None:
+        """Grows sequence seqs[i] by counts[i] tokens; slot_mapping and
+        positions (int32 [total], as ``run_cached`` takes them) receive the new
+        tokens' slots and places."""
+        n = seqs.numel()
+        total = next((t.numel() for t in (slot_mapping, positions) if t is not None), 0)
+        self._call("mla_prolog_pages_extend", self._list(seqs, "seqs", n), self._list(counts, "counts", n), n,
+                   self._list(slot_mapping, "slot_mapping", total), self._list(positions, "positions", total), total,
+                   stream=stream)
+
+    def fork(self, parents, children, copy_src, copy_dst, stream=None) -> None:
+        """Makes children[i] a copy of parents[i]; (copy_src[i], copy_dst[i]) is
+        the page that ``copy_pages`` has to copy in every cache (-1: none)."""
+        n = parents.numel()
+        self._call("mla_prolog_pages_fork", *(self._list(t, name, n) for t, name in (
+            (parents, "parents"), (children, "children"))), n, self._list(copy_src, "copy_src", n),
+            self._list(copy_dst, "copy_dst", n), stream=stream)
+
+    def release(self, seqs, stream=None) -> None:
+        """Ends sequences: their pages lose a reference each."""
+        self._call("mla_prolog_pages_release", self._list(seqs, "seqs", seqs.numel()), seqs.numel(), stream=stream)
+
+    def compact(self, moved_to, live=None, stream=None) -> None:
+        """Moves the live pages to the lowest places; ``copy_pages(cache, None,
+        moved_to)`` then moves their contents in every cache."""
+        n = self._pool.num_pages
+        self._call("mla_prolog_pages_compact", self._list(moved_to, "moved_to", n), self._list(live, "live", 1),
+                   stream=stream)
+
+
+def copy_pages(cache, src, dst, status=None, stream=None) -> None:
+    """Copies page src[i] to dst[i] (src None: page i; negative: skipped) in
+    every layer of a BF16 cache [layers, num_pages, page_size, Lkv + R], or in
+    one of [num_pages, page_size, Lkv + R]."""
+    dev = _on(cache, "cache", 3 if isinstance(cache, torch.Tensor) and cache.dim() == 3 else 4)
+    shape = tuple(cache.shape) if cache.dim() == 4 else (1,) + tuple(cache.shape)
+    page_bytes = shape[2] * shape[3] * 2
+    n = dst.numel()
+    args = [_ptr(cache, "cache", torch.bfloat16, tuple(cache.shape), dev), shape[0], shape[1] * page_bytes, shape[1],
+            page_bytes, _ptr(src, "src", torch.int32, (n,), dev), _ptr(dst, "dst", torch.int32, (n,), dev), n,
+            _ptr(status, "status", torch.int32, (1,), dev)]
+    with torch.cuda.device(dev):
+        _check(lib().mla_prolog_copy_pages(*args, _stream_on(dev, stream)), "mla_prolog_copy_pages")

@@ -82,6 +82,15 @@ const char* const kFusedKernelName = "mla_decode_kernel";
 
 }  // namespace
 
+namespace mlap {
+
+// For the entry points of other files: the same error text, and the driver's
+// tensor-map encoder (null where the driver has none).
+int report_cuda(cudaError_t e, const char* where) { return cuda_fail(e, where); }
+void* tensor_map_encoder() { return reinterpret_cast<void*>(encode_fn()); }
+
+}  // namespace mlap
+
 struct mla_prolog {
     mla_prolog_dims d{};
     int device = 0;
