@@ -1,4 +1,23 @@
 // Attention over whole prompts: mla_prolog_attend_prompt.
+//
+// One CTA takes 256 query rows of one sequence and head, as two tiles of 128
+// rows, and walks the keys in tiles of 128 with the running maximum and sum
+// of a softmax (one pass over K and V).  Per key tile and query tile:
+//
+//   S = Q K^T         tcgen05.mma, Q and K tiles in shared memory (TMA), S in TMEM
+//   P = exp2(S c - m) the tile's softmax warpgroup: one row per thread, S read
+//                     from TMEM once, P written back over S as BF16
+//   O += P V          tcgen05.mma, P from TMEM, V in shared memory read along
+//                     its columns, O in TMEM in FP32
+//
+// Two query tiles, because the tensor core then works on one tile's products
+// while the other tile's warpgroup is at its exponentials; S, P and O of two
+// tiles fill the 512 columns of TMEM exactly (v_dim <= 128).  Warp roles: 0-3
+// and 4-7 softmax of tile 0 and 1, 8 issues the MMAs, 9 the TMA loads.
+//
+// The maximum that P is scaled by moves only when a row's maximum has grown
+// by more than 2^8: until then P <= 2^8, which neither BF16 nor the FP32 sums
+// mind, and O need not be rescaled.
 #include <cmath>
 #include <cstdint>
 
@@ -8,10 +27,21 @@
 namespace mlap {
 namespace {
 
+constexpr int kTile = 128;                 // query rows per tile, keys per tile
+constexpr int kSlotBytes = kTile * 128;    // 128 rows x 64 BF16 columns: one TMA box
+constexpr int kMaxSlots = 8;
+constexpr int kThreads = 320;
+constexpr int kMmaWarp = 8, kLoadWarp = 9;
+constexpr int kMiscBytes = 512;
+constexpr int kSmemMax = 232448;           // 227 KB
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+constexpr uint32_t kColS = 0, kColO = 256;  // TMEM: S/P of tile t at 128 t, O of tile t at 256 + 128 t
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;              // log2 of the largest P
+
 struct PromptParams {
-    const void* q;
+    const int8_t* q8;  // null: BF16 q
     const float* q_scale;
-    const uint16_t* k;
     const uint16_t* v;
     const int32_t* cu_q;
     const int32_t* cu_k;
@@ -20,68 +50,458 @@ struct PromptParams {
     int32_t* status;
     int Tq, Tk, B, H, Hk, Dqk, Dv;
     float scale;
-    int causal, q_int8, q_per_head;
+    int causal, q_per_head;
+    int slots;        // ring slots
+    int tile_bound;   // >= 256-row tiles of all sequences
+    int head_group;   // query heads whose K and V stay in L2 together
 };
 
-__device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+// Everything the roles share.  (Shared memory, after the tiles.)
+struct Shared {
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain;
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint32_t tmem;
+    int abort_flag;
+    int job[5];        // q0, nq, k0, nk, first row of the tile pair; job[1] = 0: nothing to do
+    uint32_t bad[12];  // keys of the masked tiles whose v holds a NaN or an infinity
+};
+static_assert(sizeof(Shared) <= kMiscBytes, "");
 
-// One warp per (row, head): each lane scores a key of 32, then the lanes share
-// the columns of v.
-__global__ void __launch_bounds__(128) mla_attend_prompt_kernel(PromptParams p) {
+struct Job {
+    int q0, nq, k0, nk, r0;
+};
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return x < lo ? lo : (x > hi ? hi : x); }
+
+// Rows [*a, *a + *n) of sequence s in a buffer of `rows`, cut to the buffer.
+__device__ __forceinline__ bool seq_rows(const int32_t* cu, int s, int rows, int* a, int* n) {
+    const int x = cu[s], y = cu[s + 1];
+    const int lo = clampi(x, 0, rows), hi = clampi(y, 0, rows);
+    *a = lo;
+    *n = hi > lo ? hi - lo : 0;
+    return x >= 0 && y >= x && y <= rows;
+}
+
+// The sequence and tile pair of index `t` in the order of the sequences (one
+// warp; -1: there are fewer).  `all`: look at every sequence for the status.
+__device__ __forceinline__ void find_job(const PromptParams& p, int t, bool all, Shared* sh) {
     const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * 4 + (threadIdx.x >> 5), h = blockIdx.y, hk = h / (p.H / p.Hk);
-    if (row >= p.Tq) return;
-    int bits = 0, found = -1, q0 = 0, q1 = 0;
-    for (int s = 0; s < p.B; ++s) {
-        const int a = p.cu_q[s], b = p.cu_q[s + 1];
-        const int ka = p.cu_k[s], kb = p.cu_k[s + 1];
-        if (a < 0 || b < a || b > p.Tq || ka < 0 || kb < ka || kb > p.Tk) bits = kStatusSeqRange;
-        const int lo = max(a, 0), hi = min(b, p.Tq);
-        if (found < 0 && row >= lo && row < hi) found = s, q0 = lo, q1 = hi;
-    }
-    if (lane == 0 && row == 0 && h == 0) raise_status(p.status, bits);
-    if (found < 0) return;
-    const int k0 = max(p.cu_k[found], 0), k1 = max(k0, min(p.cu_k[found + 1], p.Tk));
-    int n = k1 - k0;
-    if (p.causal) n = min(n, row - q0 + 1 + (k1 - k0) - (q1 - q0));
-    float c = p.scale;
-    if (p.q_int8) c *= p.q_scale[p.q_per_head ? static_cast<int64_t>(row) * p.H + h : row];
-    const int64_t qat = (static_cast<int64_t>(row) * p.H + h) * p.Dqk;
-    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 < n; j0 += 32) {
-        const int j = j0 + lane;
-        float s = 0.f;
-        if (j < n) {
-            const uint16_t* k = p.k + (static_cast<int64_t>(k0 + j) * p.Hk + hk) * p.Dqk;
-            for (int d = 0; d < p.Dqk; ++d) {
-                const float qd = p.q_int8 ? static_cast<float>(static_cast<const int8_t*>(p.q)[qat + d])
-                                          : bf16f(static_cast<const uint16_t*>(p.q)[qat + d]);
-                s = fmaf(qd, bf16f(k[d]), s);
+    int before = 0, found = 0, total = 0;
+    bool good = true;
+    if (all || p.B > 0) {
+        // tiles of all sequences: the heaviest (last) tiles come first
+        for (int pass = 0; pass < 2; ++pass) {
+            before = 0;
+            for (int s0 = 0; s0 < p.B; s0 += 32) {
+                const int s = s0 + lane;
+                int a = 0, n = 0, ka = 0, kn = 0;
+                if (s < p.B) {
+                    good &= seq_rows(p.cu_q, s, p.Tq, &a, &n);
+                    good &= seq_rows(p.cu_k, s, p.Tk, &ka, &kn);
+                }
+                const int tiles = (n + 2 * kTile - 1) / (2 * kTile);
+                int inc = tiles;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(~0u, inc, o);
+                    if (lane >= o) inc += y;
+                }
+                const int end = before + inc;
+                if (pass == 1 && t >= end - tiles && t < end) {
+                    sh->job[0] = a;
+                    sh->job[1] = n;
+                    sh->job[2] = ka;
+                    sh->job[3] = kn;
+                    sh->job[4] = (t - (end - tiles)) * 2 * kTile;
+                    found = 1;
+                }
+                before = __shfl_sync(~0u, end, 31);
+                if (pass == 1 && __any_sync(~0u, found)) break;
+            }
+            if (pass == 0) {
+                total = before;
+                t = total - 1 - t;
+                if (t < 0) break;
             }
         }
-        s = j < n ? s * c : -INFINITY;
-        float mx = s;
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
-        const float keep = expf(m - ref), e = j < n ? expf(s - ref) : 0.f;
-        float sum = e;
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        l = l * keep + sum;
-        m = mn;
-        for (int x = 0; x < 4; ++x) acc[x] *= keep;
-        for (int i = 0; i < 32 && j0 + i < n; ++i) {
-            const float w = __shfl_sync(~0u, e, i);
-            const uint16_t* v = p.v + (static_cast<int64_t>(k0 + j0 + i) * p.Hk + hk) * p.Dv;
-            for (int x = 0; x < 4; ++x)
-                if (x * 32 + lane < p.Dv) acc[x] = fmaf(w, bf16f(v[x * 32 + lane]), acc[x]);
+    }
+    if (!__any_sync(~0u, found) && lane == 0) sh->job[1] = 0;
+    if (all && !__all_sync(~0u, good) && lane == 0) raise_status(p.status, kStatusSeqRange);
+}
+
+// Zeroes what no row may multiply: v rows behind the sequence's end, and NaN
+// or infinite elements of v (in tiles where the mask hides keys from some
+// rows); their keys are noted, and the rows that do see them add them in the
+// epilogue.  One key row per thread of the warpgroup.
+__device__ __forceinline__ void clean_v(uint32_t smem, int chunks, int row, bool inside, uint32_t* bad) {
+    const int lane = threadIdx.x & 31;
+    bool hit = false;
+    for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t at = smem + c * kSlotBytes + row * 128 + (((i + lane) & 7) << 4);
+            uint32_t w[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                         : "r"(at)
+                         : "memory");
+            bool change = false;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t m = 0;
+                if (!inside || (w[k] & 0x7F80u) == 0x7F80u) m |= 0xFFFFu;
+                if (!inside || (w[k] & 0x7F800000u) == 0x7F800000u) m |= 0xFFFF0000u;
+                if (m) {
+                    w[k] &= ~m;
+                    change = true;
+                }
+            }
+            if (change) {
+                if (inside && !hit) {  // noted before it is gone
+                    hit = true;
+                    atomicOr(bad + (row >> 5), 1u << (row & 31));
+                    __threadfence_block();
+                }
+                st_shared_v4(at, w[0], w[1], w[2], w[3]);
+            }
         }
     }
-    const int64_t at = static_cast<int64_t>(row) * p.H + h;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int x = 0; x < 4; ++x)
-        if (x * 32 + lane < p.Dv)
-            p.out[at * p.Dv + x * 32 + lane] = static_cast<uint16_t>(pack_bf16x2(acc[x] * inv, 0.f) & 0xFFFFu);
-    if (lane == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_attend_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                             const __grid_constant__ CUtensorMap tm_v, const PromptParams p) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t raw_at = smem_u32(raw);
+    const uint32_t pad = (1024u - (raw_at & 1023u)) & 1023u;
+    const int nqk = (p.Dqk + 63) / 64, nv = (p.Dv + 63) / 64;
+    const uint32_t sm_q = raw_at + pad, sm_ring = sm_q + 2 * nqk * kSlotBytes;
+    Shared* sh = reinterpret_cast<Shared*>(raw + pad + (2 * nqk + p.slots) * kSlotBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    // blockIdx -> (group of heads, tile pair, head of the group)
+    const int per_group = p.head_group * p.tile_bound;
+    const int g = blockIdx.x / per_group, in_group = blockIdx.x % per_group;
+    const int width = min(p.head_group, p.H - g * p.head_group);
+    const int tile = in_group / width, h = g * p.head_group + in_group % width;
+    const int hk = h / (p.H / p.Hk);
+    if (warp == 0) find_job(p, tile, blockIdx.x == 0, sh);
+    if (warp == kLoadWarp && lane == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(smem_u32(&sh->q_full[t]), p.q8 ? kTile : 1);
+            mbar_init(smem_u32(&sh->s_full[t]), 1);
+            mbar_init(smem_u32(&sh->p_full[t]), kTile);
+            mbar_init(smem_u32(&sh->o_done[t]), 1);
+        }
+        for (int s = 0; s < p.slots; ++s) {
+            mbar_init(smem_u32(&sh->full[s]), 1);
+            mbar_init(smem_u32(&sh->empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sh->drain), 1);
+        sh->abort_flag = 0;
+        for (int i = 0; i < 12; ++i) sh->bad[i] = 0;
+        fence_barrier_init();
+    }
+    __syncthreads();
+    const Job jb{sh->job[0], sh->job[1], sh->job[2], sh->job[3], sh->job[4]};
+    if (jb.nq == 0) return;
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&sh->tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+
+    // Keys that row r of the sequence sees: [0, limit(r)).
+    const int off = jb.nk - jb.nq;
+    auto limit = [&](int r) { return p.causal ? clampi(off + r + 1, 0, jb.nk) : jb.nk; };
+    int rows[2], n[2];
+    for (int t = 0; t < 2; ++t) {
+        rows[t] = clampi(jb.nq - jb.r0 - t * kTile, 0, kTile);
+        n[t] = rows[t] ? (limit(jb.r0 + t * kTile + rows[t] - 1) + kTile - 1) / kTile : 0;
+    }
+    const int nmax = n[0] > n[1] ? n[0] : n[1];
+    const int first_masked = limit(jb.r0) / kTile;
+    const int span = nqk + nv;  // ring slots per key tile: K's, then V's
+    auto slot_of = [&](int use) { return use % p.slots; };
+    auto full_parity = [&](int use) { return static_cast<uint32_t>(use / p.slots) & 1u; };
+    const volatile int* abort_flag = &sh->abort_flag;
+    bool ok = true;
+
+    if (warp < 8) {
+        // ------------------------------------------------------------ softmax
+        const int t = warp >> 2, r = threadIdx.x & 127;  // r: TMEM lane, row of the tile
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + kColS + t * kTile, to = tmem + lanes + kColO + t * kTile;
+        const int row = jb.r0 + t * kTile + r;                    // of the sequence
+        const int64_t at = (static_cast<int64_t>(jb.q0) + row) * p.H + h;  // of out and lse
+        const bool mine = r < rows[t];
+        float c = p.scale * kLog2e;
+        if (p.q8 && n[t]) {
+            const float qs = mine ? p.q_scale[p.q_per_head ? at : jb.q0 + row] : 0.f;
+            c *= fabsf(qs);  // a negative scale turns the codes' sign, so that c > 0 keeps the order of the scores
+            if (c < 1e-30f) c = 1e-30f;  // a zero row: its scores are 0 (hidden ones stay -inf)
+            const uint32_t qt = sm_q + t * nqk * kSlotBytes + r * 128;
+            for (int d = 0; d < p.Dqk; d += 16) {
+                uint4 w = mine ? *reinterpret_cast<const uint4*>(p.q8 + at * p.Dqk + d) : make_uint4(0, 0, 0, 0);
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                uint32_t y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t two = x[i >> 1] >> ((i & 1) * 16);
+                    float a = static_cast<float>(static_cast<int8_t>(two)), b = static_cast<float>(static_cast<int8_t>(two >> 8));
+                    if (qs < 0.f) a = -a, b = -b;
+                    y[i] = pack_bf16x2(a, b);
+                }
+                const uint32_t dst = qt + (d >> 6) * kSlotBytes;
+                const uint32_t j = (d & 63) >> 3;
+                st_shared_v4(dst + ((j ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
+                st_shared_v4(dst + (((j + 1) ^ (r & 7)) << 4), y[4], y[5], y[6], y[7]);
+            }
+            fence_proxy_async_shared();
+            mbar_arrive(smem_u32(&sh->q_full[t]));
+        }
+        const int lim = mine ? limit(row) : jb.nk;
+        const int lim0 = limit(jb.r0 + t * kTile);  // of the tile's first row, which sees the fewest
+        float m = -INFINITY, ms = 0.f, l = 0.f;     // row maximum of S, ms = m c, row sum of P
+        for (int j = 0; j < n[t]; ++j) {
+            ok = mbar_wait(smem_u32(&sh->s_full[t]), j & 1, kTimeoutNs, abort_flag);
+            if (!__all_sync(~0u, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t s[kTile];
+            tmem_ld128_raw(ts, s);
+            const bool masked = (j + 1) * kTile > lim0;
+            if (masked) {
+                const int left = lim - j * kTile;
+#pragma unroll
+                for (int i = 0; i < kTile; ++i)
+                    if (i >= left) s[i] = 0xFF800000u;
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < kTile; i += 8)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[i + k])), __uint_as_float(s[i + 4 + k]));
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // rows that have no maximum yet take this tile's; the others only one that has grown by the slack
+            const bool grow = mt > m && (m == -INFINITY || mt * c > ms + kSlack);
+            if (__any_sync(~0u, grow)) {
+                float alpha = 1.f;
+                if (mt > m) {
+                    const float next = mt * c;
+                    if (m != -INFINITY) alpha = ex2(ms - next);
+                    m = mt;
+                    ms = next;
+                }
+                l *= alpha;
+                if (j > 0 && __any_sync(~0u, alpha != 1.f)) {
+                    ok = mbar_wait(smem_u32(&sh->o_done[t]), (j - 1) & 1, kTimeoutNs, abort_flag);
+                    if (!__all_sync(~0u, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int d = 0; d < p.Dv; d += 16) {
+                        float o[16];
+                        tmem_ld16(to + d, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                        tmem_st16(to + d, o);
+                    }
+                }
+            }
+            const uint64_t cc = pk2(c, c), mm = pk2(-ms, -ms);
+            uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+            for (int b = 0; b < kTile; b += 32) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    float e0, e1, e2, e3;
+                    upk2(fma2(pk2(__uint_as_float(s[b + i]), __uint_as_float(s[b + i + 1])), cc, mm), e0, e1);
+                    upk2(fma2(pk2(__uint_as_float(s[b + i + 2]), __uint_as_float(s[b + i + 3])), cc, mm), e2, e3);
+                    e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
+                    sum0 = add2(sum0, pk2(e0, e1));
+                    sum1 = add2(sum1, pk2(e2, e3));
+                    w[i >> 1] = pack_bf16x2(e0, e1);
+                    w[(i >> 1) + 1] = pack_bf16x2(e2, e3);
+                }
+                tmem_st16_raw(ts + b / 2, w);
+            }
+            float a0, a1;
+            upk2(add2(sum0, sum1), a0, a1);
+            l += a0 + a1;
+            if (masked) {
+                const int use = j * span + nqk;
+                for (int cidx = 0; cidx < nv; ++cidx)
+                    ok &= mbar_wait(smem_u32(&sh->full[slot_of(use + cidx)]), full_parity(use + cidx), kTimeoutNs, abort_flag);
+                if (!__all_sync(~0u, ok)) {
+                    ok = false;
+                    break;
+                }
+                for (int cidx = 0; cidx < nv; ++cidx)
+                    clean_v(sm_ring + slot_of(use + cidx) * kSlotBytes, 1, r, j * kTile + r < jb.nk,
+                            sh->bad + (j - first_masked) * 4);
+                fence_proxy_async_shared();
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh->p_full[t]));
+        }
+        if (ok && rows[t]) {
+            if (n[t]) {
+                ok = mbar_wait(smem_u32(&sh->o_done[t]), (n[t] - 1) & 1, kTimeoutNs, abort_flag);
+                ok = __all_sync(~0u, ok);
+                tc_fence_after();
+            }
+            if (ok) {
+                uint32_t any_bad = 0;
+#pragma unroll
+                for (int i = 0; i < 12; ++i) any_bad |= *const_cast<volatile uint32_t*>(sh->bad + i);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+                for (int d = 0; d < p.Dv; d += 16) {
+                    float o[16];
+                    if (n[t]) tmem_ld16(to + d, o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
+                    if (any_bad) {
+                        for (int w = 0; w < 12; ++w)
+                            for (uint32_t bits = *const_cast<volatile uint32_t*>(sh->bad + w); bits; bits &= bits - 1) {
+                                const int key = (first_masked + w / 4) * kTile + (w & 3) * 32 + __ffs(bits) - 1;
+                                if (key >= lim) continue;
+                                const uint16_t* v = p.v + ((static_cast<int64_t>(jb.k0) + key) * p.Hk + hk) * p.Dv + d;
+#pragma unroll 1
+                                for (int i = 0; i < 16; ++i)
+                                    if ((v[i] & 0x7F80) == 0x7F80) {
+                                        const float x = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
+#pragma unroll
+                                        for (int k = 0; k < 16; ++k)
+                                            if (k == i) o[k] += x;
+                                    }
+                            }
+                    }
+                    if (mine) {
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + at * p.Dv + d);
+                        dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                            pack_bf16x2(o[6], o[7]));
+                        dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]),
+                                            pack_bf16x2(o[12], o[13]), pack_bf16x2(o[14], o[15]));
+                    }
+                }
+                if (mine && p.lse) p.lse[at] = l == 0.f ? -INFINITY : ms * kLn2 + logf(l);
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- MMA
+        if (lane == 0) {
+            const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
+            const uint32_t idesc_o = idesc_bf16_f32(kTile, p.Dv) | kIdescBMnMajor;
+            const int ksteps = p.Dqk / 16;
+            auto wait_slots = [&](int use, int count) {
+                for (int i = 0; i < count && ok; ++i)
+                    ok = mbar_wait(smem_u32(&sh->full[slot_of(use + i)]), full_parity(use + i), kTimeoutNs, abort_flag);
+                tc_fence_after();
+            };
+            auto free_slots = [&](int use, int count) {
+                for (int i = 0; i < count; ++i) mma_commit(smem_u32(&sh->empty[slot_of(use + i)]));
+            };
+            auto last_user = [&](int t, int j) { return t == 1 || j >= n[1]; };
+            auto scores = [&](int t, int j) {
+                const int use = j * span;
+                wait_slots(use, nqk);
+                if (!ok) return;
+                for (int k = 0; k < ksteps; ++k) {
+                    const uint64_t a = smem_desc_sw128(sm_q + (t * nqk + (k >> 2)) * kSlotBytes) + 2 * (k & 3);
+                    const uint64_t b = smem_desc_sw128(sm_ring + slot_of(use + (k >> 2)) * kSlotBytes) + 2 * (k & 3);
+                    mma_bf16(tmem + kColS + t * kTile, a, b, idesc_s, k > 0);
+                }
+                mma_commit(smem_u32(&sh->s_full[t]));
+                if (last_user(t, j)) free_slots(use, nqk);
+            };
+            for (int t = 0; t < 2 && ok; ++t)
+                if (n[t]) {
+                    ok = mbar_wait(smem_u32(&sh->q_full[t]), 0, kTimeoutNs, abort_flag);
+                    tc_fence_after();
+                    if (ok) scores(t, 0);
+                }
+            for (int j = 0; j < nmax && ok; ++j)
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (j >= n[t]) continue;
+                    const int use = j * span + nqk;
+                    wait_slots(use, nv);
+                    if (ok) ok = mbar_wait(smem_u32(&sh->p_full[t]), j & 1, kTimeoutNs, abort_flag);
+                    tc_fence_after();
+                    if (!ok) break;
+                    // one product over V's two slots where they are neighbours, two of 64 columns where the ring wraps
+                    const bool whole = nv == 1 || slot_of(use + 1) == slot_of(use) + 1;
+                    for (int cidx = 0; cidx < (whole ? 1 : nv); ++cidx) {
+                        const uint64_t b = smem_desc_sw128_mn(sm_ring + slot_of(use + cidx) * kSlotBytes, kSlotBytes);
+                        const uint32_t cols = whole ? p.Dv : min(64, p.Dv - cidx * 64);
+                        const uint32_t idesc = (idesc_o & ~(0x3Fu << 17)) | (cols >> 3) << 17;
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_bf16_ts(tmem + kColO + t * kTile + cidx * 64, tmem + kColS + t * kTile + k * 8,
+                                        b + k * (2048 >> 4), idesc, j > 0 || k > 0);
+                    }
+                    mma_commit(smem_u32(&sh->o_done[t]));
+                    if (last_user(t, j)) free_slots(use, nv);
+                    if (j + 1 < n[t]) scores(t, j + 1);
+                }
+            if (!ok) {  // no MMA may still run when the CTA leaves
+                mma_commit(smem_u32(&sh->drain));
+                mbar_wait(smem_u32(&sh->drain), 0, kTimeoutNs, nullptr);
+            }
+        }
+    } else if (lane == 0) {
+        // --------------------------------------------------------------- TMA
+        int use = 0, q_loaded = 0;
+        auto load_q = [&](int t) {
+            if (p.q8 || !n[t]) return;
+            mbar_arrive_expect_tx(smem_u32(&sh->q_full[t]), nqk * kSlotBytes);
+            for (int cidx = 0; cidx < nqk; ++cidx)
+                tma_load_3d(sm_q + (t * nqk + cidx) * kSlotBytes, &tm_q, smem_u32(&sh->q_full[t]), cidx * 64, h,
+                            jb.q0 + jb.r0 + t * kTile);
+            q_loaded |= 1 << t;
+        };
+        auto load = [&](const CUtensorMap* map, int chunks, int j) {
+            for (int cidx = 0; cidx < chunks && ok; ++cidx, ++use) {
+                const int s = slot_of(use);
+                ok = mbar_wait(smem_u32(&sh->empty[s]), full_parity(use) ^ 1u, kTimeoutNs, abort_flag);
+                if (!ok) return;
+                mbar_arrive_expect_tx(smem_u32(&sh->full[s]), kSlotBytes);
+                tma_load_3d(sm_ring + s * kSlotBytes, map, smem_u32(&sh->full[s]), cidx * 64, hk, jb.k0 + j * kTile);
+            }
+        };
+        load_q(0);
+        for (int j = 0; j < nmax && ok; ++j) {
+            load(&tm_k, nqk, j);
+            if (j == 0) load_q(1);
+            load(&tm_v, nv, j);
+        }
+        // no copy may still be landing when the CTA leaves
+        for (int u = use > p.slots ? use - p.slots : 0; u < use; ++u)
+            mbar_wait(smem_u32(&sh->full[slot_of(u)]), full_parity(u), kTimeoutNs, nullptr);
+        for (int t = 0; t < 2; ++t)
+            if (q_loaded >> t & 1) mbar_wait(smem_u32(&sh->q_full[t]), 0, kTimeoutNs, nullptr);
+    }
+    if (!ok) {
+        sh->abort_flag = 1;
+        if (lane == 0) raise_status(p.status, kStatusWaitTimeout);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
 }
 
 }  // namespace
@@ -105,13 +525,43 @@ extern "C" int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* d, const v
     if (!ptr_ok(q, 16) || !ptr_ok(out, 16) || !ptr_ok(cu_q, 4) || !ptr_ok(cu_k, 4)) return MLA_ERR_INVALID_ARG;
     if (d->Tk && (!ptr_ok(k, 16) || !ptr_ok(v, 16))) return MLA_ERR_INVALID_ARG;
     if ((lse && !ptr_ok(lse, 4)) || (status && !ptr_ok(status, 4))) return MLA_ERR_INVALID_ARG;
+    // 256-row tiles: at most one ragged tile per sequence that holds a row
+    const int64_t ragged = d->sequences < d->Tq ? d->sequences : d->Tq;
+    const int64_t tiles = d->Tq / (2 * kTile) + ragged;
+    if (tiles * d->num_heads > INT32_MAX) return MLA_ERR_UNSUPPORTED_DIMS;
     int sms;
     const int rc = current_sm103(&sms);
     if (rc != MLA_OK) return rc;
-    PromptParams p{q, q_scale, static_cast<const uint16_t*>(k), static_cast<const uint16_t*>(v), cu_q, cu_k,
+    CUtensorMap tq, tk, tv;
+    bool good = true;
+    if (!int8) good &= encode_bf16_3d(&tq, q, d->qk_dim, d->num_heads, d->Tq, 1, kTile);
+    if (d->Tk) {
+        good &= encode_bf16_3d(&tk, k, d->qk_dim, d->kv_heads, d->Tk, 1, kTile);
+        good &= encode_bf16_3d(&tv, v, d->v_dim, d->kv_heads, d->Tk, 1, kTile);
+    }
+    if (!good) return report_cuda(cudaErrorInvalidValue, "tensor maps of attend_prompt");
+    if (int8) tq = d->Tk ? tk : CUtensorMap{};  // not read
+    if (!d->Tk) tk = tv = tq;                   // not read
+    const int nqk = (d->qk_dim + 63) / 64;
+    int slots = (kSmemMax - 1024 - kMiscBytes) / kSlotBytes - 2 * nqk;
+    if (slots > kMaxSlots) slots = kMaxSlots;
+    const int smem = 1024 + kMiscBytes + (2 * nqk + slots) * kSlotBytes;
+    // Heads go in groups whose K and V fit L2 together, and within a group the
+    // tile pairs with the most keys first: few heads at a time keep K and V on
+    // chip when they are large, many spread uneven tiles over the SMs when
+    // they are small.
+    const int64_t kv_bytes = static_cast<int64_t>(d->Tk) * (d->qk_dim + d->v_dim) * 2;
+    const int per_kv = d->num_heads / d->kv_heads;
+    int64_t group = kv_bytes > 0 ? (int64_t(48) << 20) / kv_bytes : d->kv_heads;
+    group = (group < 1 ? 1 : group > d->kv_heads ? d->kv_heads : group) * per_kv;
+    PromptParams p{int8 ? static_cast<const int8_t*>(q) : nullptr, q_scale, static_cast<const uint16_t*>(v), cu_q, cu_k,
                    static_cast<uint16_t*>(out), lse, status, d->Tq, d->Tk, d->sequences, d->num_heads, d->kv_heads,
-                   d->qk_dim, d->v_dim, d->scale, (d->flags & MLA_PROMPT_CAUSAL) != 0, int8, per_head};
-    mla_attend_prompt_kernel<<<dim3((d->Tq + 3) / 4, d->num_heads), 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+                   d->qk_dim, d->v_dim, d->scale, (d->flags & MLA_PROMPT_CAUSAL) != 0, per_head, slots,
+                   static_cast<int>(tiles), static_cast<int>(group)};
+    cudaError_t e = cudaFuncSetAttribute(mla_attend_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return report_cuda(e, "mla_attend_prompt_kernel attributes");
+    mla_attend_prompt_kernel<<<static_cast<unsigned>(tiles * d->num_heads), kThreads, smem,
+                               static_cast<cudaStream_t>(stream)>>>(tq, tk, tv, p);
+    e = cudaGetLastError();
     return e == cudaSuccess ? MLA_OK : report_cuda(e, "launch mla_attend_prompt_kernel");
 }
