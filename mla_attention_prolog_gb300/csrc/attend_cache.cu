@@ -1,4 +1,25 @@
 // One decoding step over the latent KV cache: mla_prolog_attend_cache.
+//
+// A tile is 128 query rows (sequence, head) that see the same keys: the rows
+// of one sequence on its own pages, or 128 rows of any sequences on the
+// shared prefix, whose rows are thus read and multiplied once per 128 rows
+// instead of once per sequence.  Every key is one cache row of Lkv + R
+// columns, of which the first Lkv are the value too.
+//
+//   S = Q K^T   128 x 64 keys, 576 deep     O += P V   128 x Lkv, 64 deep
+//
+// O of 128 rows x 512 columns in FP32 would fill TMEM alone, so two CTAs share
+// a tile: each makes all of S and half of the columns of O (256 TMEM columns).
+// Doing S twice costs 1.5 times the products of a perfect split; halving the
+// rows instead would cost twice the key traffic into each SM for the same
+// products, and exchanging S or P between the CTAs a round trip per key tile.
+// Two thirds of Q stay in TMEM as well (192 columns, read as the A operand),
+// S takes the last 64; the rest of Q, two key tiles and P fill shared memory.
+//
+// The work is cut into as many equal runs of key tiles as there are CTA pairs
+// (a tile costs its key tiles plus kOverhead for its start and end); a run
+// takes whole or partial tiles.  Partial results go to the workspace in FP32,
+// and a second kernel joins them.
 #include <cmath>
 #include <cstdint>
 
@@ -8,77 +29,634 @@
 namespace mlap {
 namespace {
 
+constexpr int kRows = 128;                // query rows per tile
+constexpr int kKeys = 64;                 // keys per step
+constexpr int kSlotBytes = kKeys * 128;   // 64 keys x 64 BF16 columns
+constexpr int kQBytes = kRows * 128;      // 128 rows x 64 BF16 columns
+constexpr int kMaxChunks = 9;             // 64-column chunks of a cache row
+constexpr int kTmemChunks = 6;            // chunks of Q kept in TMEM
+constexpr int kHalf = 256;                // columns of O per CTA
+constexpr int kThreads = 192;
+constexpr int kMmaWarp = 4, kLoadWarp = 5;
+constexpr int kMiscBytes = 1024;
+constexpr int kSmem = 1024 + kMiscBytes + (kMaxChunks - kTmemChunks) * kQBytes + 2 * kMaxChunks * kSlotBytes + kQBytes;
+constexpr uint32_t kColO = 0, kColQ = 256, kColS = 448;
+constexpr uint64_t kTimeoutNs = 1000000000ull;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.f;             // log2 of the largest P
+constexpr int kOverhead = 4;              // a tile's start and end, in key steps
+constexpr int kMinRun = 8;                // shortest run worth a CTA pair, in key steps
+
+// What the join kernel needs to know of the cut (start of the workspace).
+struct Cut {
+    int64_t prefix_cost;  // cost of the prefix tiles
+    int64_t run;          // cost per unit
+    int32_t shared;       // keys of the shared prefix (a multiple of kKeys; 0: none)
+    int32_t source;       // batch row whose pages hold it
+};
+
 struct CacheParams {
     const uint16_t* q;
-    const uint16_t* cache;
     const int32_t* table;
     const int32_t* lens;
     const int32_t* seqs;
-    const int32_t* shared;
+    const int32_t* shared_len;
     uint16_t* out;
     float* lse;
     int32_t* status;
-    int B, H, Lkv, C, page_size, table_rows, max_pages;
-    int64_t num_pages;
+    Cut* cut;           // workspace: the cut,
+    int64_t* bases;     //   cost of the sequences before each [B],
+    float* part_o;      //   partial results [part rows][Lkv]
+    float* part_lse;    //   and their log2-sum-exp [part rows]
+    int B, H, Lkv, C, page_size, table_rows, max_pages, num_rows, num_pages, box;
+    int row_tiles, head_tiles, halves, units;
     float scale;
 };
 
-__device__ __forceinline__ float bf16f(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
-
-// One warp per (sequence, head): each lane scores a key of 32, then the lanes
-// share the columns of c_kv.
-__global__ void __launch_bounds__(128) mla_attend_cache_kernel(CacheParams p) {
-    const int lane = threadIdx.x & 31;
-    const int r = blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (r >= p.B * p.H) return;
-    const int b = r / p.H;
-    int bits = 0, n = 0;
+// Table row (-1: none) and length of batch row b.
+__device__ __forceinline__ int batch_len(const CacheParams& p, int b, int* row, int* bits) {
     const int s = p.seqs ? p.seqs[b] : b;
-    const int cap = p.max_pages * p.page_size;
     if (s < 0 || s >= p.table_rows) {
-        bits = kStatusSeqRange;
+        *row = -1;
+        *bits |= kStatusSeqRange;
+        return 0;
+    }
+    *row = s;
+    const int n = p.lens[s], cap = p.max_pages * p.page_size;
+    if (n < 0 || n > cap) *bits |= kStatusSeqRange;
+    return n < 0 ? 0 : n > cap ? cap : n;
+}
+
+// Keys of batch row b before its own ones, and steps over its own.
+__device__ __forceinline__ int own_start(int len, int shared) { return len >= shared ? shared : 0; }
+__device__ __forceinline__ int own_steps(int len, int shared) {
+    return (len - own_start(len, shared) + kKeys - 1) / kKeys;
+}
+__device__ __forceinline__ int64_t seq_cost(const CacheParams& p, int steps) {
+    return steps ? static_cast<int64_t>(p.head_tiles) * (steps + kOverhead) : 0;
+}
+
+// The steps [*j0, *j1) of a tile of `steps` at cost `base` that the costs
+// [from, to) cover.
+__device__ __forceinline__ void covered(int64_t base, int steps, int64_t from, int64_t to, int* j0, int* j1) {
+    const int64_t a = from - base - kOverhead, e = to - base - kOverhead;
+    *j0 = a < 0 ? 0 : a > steps ? steps : static_cast<int>(a);
+    *j1 = e < 0 ? 0 : e > steps ? steps : static_cast<int>(e);
+}
+
+// First row of the partial results of (tile, unit): the tile's rows in a list
+// of all tiles' rows, moved on by a tile per unit, so that no two overlap.
+__device__ __forceinline__ int64_t part_row(const CacheParams& p, int64_t tile_row, int unit) {
+    return tile_row + static_cast<int64_t>(unit) * kRows;
+}
+
+struct Piece {
+    int64_t part;    // first row of its partial result
+    int row0, rows;  // rows of q
+    int page_row;    // row of the page table
+    int key0, end;   // first key of the first step, end of the keys
+    int n;           // steps
+    bool prefix, whole;  // whole: covers the tile's keys
+};
+
+// A unit's walk over its pieces; every role walks on its own.
+struct Walk {
+    int64_t at, end, prefix_cost, base;  // base: cost before batch row b
+    int shared, source_row, b, len, row, unit;
+
+    __device__ __forceinline__ void enter(const CacheParams& p) {
+        int bits = 0;
+        if (b < p.B) len = batch_len(p, b, &row, &bits);
+    }
+
+    __device__ __forceinline__ bool next(const CacheParams& p, Piece* x) {
+        while (at < end) {
+            int64_t tile_base, tile_row;
+            int steps;
+            if (at < prefix_cost) {
+                steps = shared / kKeys;
+                const int t = static_cast<int>(at / (steps + kOverhead));
+                tile_base = static_cast<int64_t>(t) * (steps + kOverhead);
+                x->row0 = t * kRows;
+                x->rows = min(kRows, p.B * p.H - x->row0);
+                tile_row = x->row0;
+                x->page_row = source_row;
+                x->key0 = 0;
+                x->end = shared;
+                x->prefix = true;
+            } else {
+                steps = own_steps(len, shared);
+                while (b < p.B && at >= base + seq_cost(p, steps)) {
+                    base += seq_cost(p, steps);
+                    ++b;
+                    enter(p);
+                    steps = own_steps(len, shared);
+                }
+                if (b >= p.B) return false;
+                const int ht = static_cast<int>((at - base) / (steps + kOverhead));
+                tile_base = base + static_cast<int64_t>(ht) * (steps + kOverhead);
+                x->row0 = b * p.H + ht * kRows;
+                x->rows = min(kRows, p.H - ht * kRows);
+                tile_row = static_cast<int64_t>(p.row_tiles) * kRows + x->row0;
+                x->page_row = row;
+                x->key0 = own_start(len, shared);
+                x->end = len;
+                x->prefix = false;
+            }
+            int j0, j1;
+            covered(tile_base, steps, at, end, &j0, &j1);
+            const int64_t tile_end = tile_base + steps + kOverhead;
+            at = tile_end < end ? tile_end : end;
+            if (j1 <= j0) continue;
+            x->part = part_row(p, tile_row, unit);
+            x->key0 += j0 * kKeys;
+            x->n = j1 - j0;
+            x->whole = x->n == steps;
+            return true;
+        }
+        return false;
+    }
+};
+
+struct Shared {
+    uint64_t full[2 * kMaxChunks], empty[2 * kMaxChunks];
+    uint64_t q_full, s_full, s_free, p_full, pv_done, drain;
+    uint32_t tmem;
+    int abort_flag;
+    int64_t scan[kThreads / 32];
+    int64_t total, first_base;
+    int first_b, sharers, source, shared;
+};
+static_assert(sizeof(Shared) <= kMiscBytes, "");
+
+// Exclusive prefix sum over the block; *total: the block's sum.
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64_t* total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(~0u, x, o);
+        if (lane >= o) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) scratch[warp] = x;
+    __syncthreads();
+    int64_t before = 0, sum = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += scratch[w];
+        sum += scratch[w];
+    }
+    *total = sum;
+    return before + x - v;
+}
+
+// The cut, and where this unit's run starts.  Every CTA computes it from the
+// lengths (a few hundred loads at most batch sizes); CTA 0 leaves it in the
+// workspace for the join.  False: the unit has no run.
+__device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared* sh, Walk* w) {
+    const bool writer = blockIdx.x == 0;
+    int bits = 0, row;
+    // who shares the prefix
+    int shared = p.shared_len ? *p.shared_len : 0;
+    const int cap = p.max_pages * p.page_size;
+    shared = shared < 0 ? 0 : (shared > cap ? cap : shared) / kKeys * kKeys;
+    if (threadIdx.x == 0) sh->sharers = 0, sh->source = p.B;
+    __syncthreads();
+    if (shared > 0) {
+        int count = 0, first = p.B;
+        for (int b = threadIdx.x; b < p.B; b += kThreads)
+            if (batch_len(p, b, &row, &bits) >= shared) ++count, first = min(first, b);
+        if (count) {
+            atomicAdd(&sh->sharers, count);
+            atomicMin(&sh->source, first);
+        }
+        __syncthreads();
+        if (sh->sharers < 2) shared = 0;
+    }
+    const int source = sh->source;
+    const int64_t prefix = shared ? static_cast<int64_t>(p.row_tiles) * (shared / kKeys + kOverhead) : 0;
+    int64_t total = prefix, sum;
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        const int b = b0 + threadIdx.x;
+        const int len = b < p.B ? batch_len(p, b, &row, &bits) : 0;
+        const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
+        const int64_t before = total + block_scan(mine, sh->scan, &sum);
+        if (writer && b < p.B) p.bases[b] = before;
+        total += sum;
+    }
+    int64_t run = (total + p.units - 1) / p.units;
+    if (run < kMinRun) run = kMinRun;
+    if (writer) {
+        if (threadIdx.x == 0) *p.cut = Cut{prefix, run, shared, source};
+        raise_status(p.status, bits);
+    }
+    w->unit = unit;
+    w->at = run * unit;
+    w->end = w->at + run < total ? w->at + run : total;
+    w->prefix_cost = prefix;
+    w->shared = shared;
+    w->b = 0;
+    w->base = prefix;
+    w->len = w->row = 0;
+    w->source_row = -1;
+    if (w->at >= total) return false;
+    if (shared) batch_len(p, source, &w->source_row, &bits);
+    if (w->at >= prefix) {  // the batch row that holds `at`
+        if (p.B <= kThreads) {
+            const int b = threadIdx.x;
+            const int len = b < p.B ? batch_len(p, b, &row, &bits) : 0;
+            const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
+            const int64_t before = prefix + block_scan(mine, sh->scan, &sum);
+            if (mine && w->at >= before && w->at < before + mine) sh->first_b = b, sh->first_base = before;
+        } else {
+            int64_t base = prefix;
+            for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+                const int b = b0 + threadIdx.x;
+                const int len = b < p.B ? batch_len(p, b, &row, &bits) : 0;
+                const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
+                const int64_t before = base + block_scan(mine, sh->scan, &sum);
+                if (mine && w->at >= before && w->at < before + mine) sh->first_b = b, sh->first_base = before;
+                base += sum;
+                if (base > w->at) break;
+            }
+        }
+        __syncthreads();
+        w->b = sh->first_b;
+        w->base = sh->first_base;
+    }
+    w->enter(p);
+    return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_c, const CacheParams p) {
+    extern __shared__ uint8_t raw[];
+    const uint32_t raw_at = smem_u32(raw);
+    const uint32_t pad = (1024u - (raw_at & 1023u)) & 1023u;
+    const int chunks = (p.C + 63) / 64;
+    const uint32_t sm_q = raw_at + pad, sm_p = sm_q + (kMaxChunks - kTmemChunks) * kQBytes, sm_ring = sm_p + kQBytes;
+    Shared* sh = reinterpret_cast<Shared*>(raw + pad + (kMaxChunks - kTmemChunks + 1) * kQBytes +
+                                           2 * kMaxChunks * kSlotBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int unit = blockIdx.x / p.halves, half = blockIdx.x % p.halves;
+    // this CTA's columns of O, the chunks that hold them (loaded last, kept longest)
+    const int dv0 = half * kHalf, dv = min(kHalf, p.Lkv - dv0);
+    const int vc0 = dv0 / 64, nvc = (dv + 63) / 64, others = chunks - nvc;
+    auto chunk_at = [&](int pos) { return pos < others ? (pos < vc0 ? pos : pos + nvc) : vc0 + pos - others; };
+
+    Walk walk;
+    if (!make_cut(p, unit, sh, &walk)) return;
+    if (warp == kLoadWarp && lane == 0) {
+        for (int s = 0; s < 2 * chunks; ++s) {
+            mbar_init(smem_u32(&sh->full[s]), 1);
+            mbar_init(smem_u32(&sh->empty[s]), 1);
+        }
+        mbar_init(smem_u32(&sh->q_full), kRows);
+        mbar_init(smem_u32(&sh->s_full), 1);
+        mbar_init(smem_u32(&sh->s_free), kRows);
+        mbar_init(smem_u32(&sh->p_full), kRows);
+        mbar_init(smem_u32(&sh->pv_done), 1);
+        mbar_init(smem_u32(&sh->drain), 1);
+        sh->abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) {
+        tmem_alloc(smem_u32(&sh->tmem), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh->tmem;
+    const volatile int* abort_flag = &sh->abort_flag;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return mbar_wait(smem_u32(bar), parity & 1u, kTimeoutNs, abort_flag);
+    };
+    bool ok = true;
+    int step = 0;  // key steps so far, over all pieces: the phase of every barrier
+    Piece x;
+
+    if (warp < 4) {
+        // ------------------------------------------------------------ softmax
+        const int r = threadIdx.x;
+        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+        const float c = p.scale * kLog2e;
+        while (ok && walk.next(p, &x)) {
+            const bool mine = r < x.rows;
+            // Q: chunks 0-5 to TMEM, the rest to shared memory in the swizzled layout of a TMA box
+            const uint4* q = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(x.row0) + r) * p.C);
+            for (int k = 0; k < chunks; ++k) {
+                uint4 w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    w[i] = mine && k * 64 + i * 8 < p.C ? q[k * 8 + i] : make_uint4(0, 0, 0, 0);
+                if (k < kTmemChunks) {
+                    uint32_t y[32];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        y[4 * i] = w[i].x, y[4 * i + 1] = w[i].y, y[4 * i + 2] = w[i].z, y[4 * i + 3] = w[i].w;
+                    tmem_st32_raw(tmem + lanes + kColQ + k * 32, y);
+                } else {
+                    const uint32_t dst = sm_q + (k - kTmemChunks) * kQBytes + r * 128;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_shared_v4(dst + ((i ^ (r & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
+                }
+            }
+            tmem_wait_st();
+            fence_proxy_async_shared();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&sh->q_full));
+            float m = -INFINITY, ms = 0.f, l = 0.f;
+            for (int j = 0; j < x.n; ++j, ++step) {
+                ok = __all_sync(~0u, wait(&sh->s_full, step));
+                if (!ok) break;
+                tc_fence_after();
+                uint32_t s[kKeys];
+                tmem_ld64_raw(tmem + lanes + kColS, s);
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh->s_free));
+                const int left = x.end - x.key0 - j * kKeys;
+                if (left < kKeys) {
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i)
+                        if (i >= left) s[i] = 0xFF800000u;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[i + k])), __uint_as_float(s[i + 4 + k]));
+                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool grow = mt > m && (m == -INFINITY || mt * c > ms + kSlack);
+                float alpha = 1.f;
+                if (__any_sync(~0u, grow)) {
+                    if (mt > m) {
+                        const float next = mt * c;
+                        if (m != -INFINITY) alpha = ex2(ms - next);
+                        m = mt;
+                        ms = next;
+                    }
+                    l *= alpha;
+                }
+                const uint64_t cc = pk2(c, c), mm = pk2(-ms, -ms);
+                uint64_t sum0 = 0, sum1 = 0;
+                uint32_t w[kKeys / 2];
+#pragma unroll
+                for (int i = 0; i < kKeys; i += 4) {
+                    float e0, e1, e2, e3;
+                    upk2(fma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cc, mm), e0, e1);
+                    upk2(fma2(pk2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), cc, mm), e2, e3);
+                    e0 = ex2(e0), e1 = ex2(e1), e2 = ex2(e2), e3 = ex2(e3);
+                    sum0 = add2(sum0, pk2(e0, e1));
+                    sum1 = add2(sum1, pk2(e2, e3));
+                    w[i >> 1] = pack_bf16x2(e0, e1);
+                    w[(i >> 1) + 1] = pack_bf16x2(e2, e3);
+                }
+                float a0, a1;
+                upk2(add2(sum0, sum1), a0, a1);
+                l += a0 + a1;
+                // the step before has read P, and O is at rest
+                if (step > 0) {
+                    ok = __all_sync(~0u, wait(&sh->pv_done, step - 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                }
+                if (j > 0 && __any_sync(~0u, alpha != 1.f)) {
+#pragma unroll 1
+                    for (int d = 0; d < dv; d += 16) {
+                        float o[16];
+                        tmem_ld16(tmem + lanes + kColO + d, o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                        tmem_st16(tmem + lanes + kColO + d, o);
+                    }
+                }
+                const uint32_t dst = sm_p + r * 128;
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    st_shared_v4(dst + ((i ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (left < kKeys) {
+                    // rows behind the end may hold anything: as values they have to be zero
+                    const int st = (step & 1) * chunks + others;
+                    for (int k = r; k < (kKeys - left) * nvc * 8; k += kRows) {
+                        const int row = left + k / (nvc * 8), in = k % (nvc * 8);
+                        st_shared_v4(sm_ring + (st + in / 8) * kSlotBytes + row * 128 + (in & 7) * 16, 0, 0, 0, 0);
+                    }
+                }
+                fence_proxy_async_shared();
+                tc_fence_before();
+                mbar_arrive(smem_u32(&sh->p_full));
+            }
+            if (!ok) break;
+            ok = __all_sync(~0u, wait(&sh->pv_done, step - 1));
+            if (!ok) break;
+            tc_fence_after();
+            // A row whose keys this piece covers alone is finished; the others leave a partial result.
+            bool direct = x.whole;
+            const int b = (x.row0 + r) / p.H;
+            if (walk.shared && direct && mine) {
+                int trow, bits = 0;
+                const int len = batch_len(p, b, &trow, &bits);
+                direct = x.prefix ? len == walk.shared : len < walk.shared;
+            }
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const int64_t at = static_cast<int64_t>(x.row0) + r;
+#pragma unroll 1
+            for (int d = 0; d < dv; d += 16) {
+                float o[16];
+                tmem_ld16(tmem + lanes + kColO + d, o);
+                if (!mine) continue;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
+                if (direct) {
+                    uint4* dst = reinterpret_cast<uint4*>(p.out + at * p.Lkv + dv0 + d);
+                    dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
+                                        pack_bf16x2(o[6], o[7]));
+                    dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]),
+                                        pack_bf16x2(o[14], o[15]));
+                } else {
+                    float4* dst = reinterpret_cast<float4*>(p.part_o + (x.part + r) * p.Lkv + dv0 + d);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                }
+            }
+            if (mine && half == 0) {
+                const float lg = l == 0.f ? -INFINITY : ms + log2f(l);
+                if (!direct) p.part_lse[x.part + r] = lg;
+                else if (p.lse) p.lse[at] = lg * kLn2;
+            }
+            tc_fence_before();
+        }
+    } else if (warp == kMmaWarp) {
+        // ---------------------------------------------------------------- MMA
+        if (lane == 0) {
+            const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
+            const uint32_t idesc_o = idesc_bf16_f32(kRows, dv) | kIdescBMnMajor;
+            auto scores = [&](int st) {
+                if (st > 0) ok = wait(&sh->s_free, st - 1);
+                for (int pos = 0; pos < chunks && ok; ++pos) {
+                    const int slot = (st & 1) * chunks + pos, ck = chunk_at(pos);
+                    ok = wait(&sh->full[slot], st >> 1);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t b = smem_desc_sw128(sm_ring + slot * kSlotBytes);
+                    const int ks = min(4, (p.C - ck * 64) / 16);
+                    if (ck < kTmemChunks) {
+                        for (int k = 0; k < ks; ++k)
+                            mma_bf16_ts(tmem + kColS, tmem + kColQ + ck * 32 + k * 8, b + 2 * k, idesc_s, pos > 0 || k > 0);
+                    } else {
+                        const uint64_t a = smem_desc_sw128(sm_q + (ck - kTmemChunks) * kQBytes);
+                        for (int k = 0; k < ks; ++k) mma_bf16(tmem + kColS, a + 2 * k, b + 2 * k, idesc_s, pos > 0 || k > 0);
+                    }
+                    if (pos < others) mma_commit(smem_u32(&sh->empty[slot]));
+                }
+                if (ok) mma_commit(smem_u32(&sh->s_full));
+            };
+            for (int piece = 0; ok && walk.next(p, &x); ++piece) {
+                ok = wait(&sh->q_full, piece);
+                tc_fence_after();
+                if (ok) scores(step);
+                for (int j = 0; j < x.n && ok; ++j, ++step) {
+                    if (j + 1 < x.n) scores(step + 1);
+                    if (ok) ok = wait(&sh->p_full, step);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int slot = (step & 1) * chunks + others;
+                    const uint64_t a = smem_desc_sw128(sm_p);
+                    const uint64_t b = smem_desc_sw128_mn(sm_ring + slot * kSlotBytes, kSlotBytes);
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_bf16(tmem + kColO, a + 2 * k, b + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
+                    mma_commit(smem_u32(&sh->pv_done));
+                    for (int k = 0; k < nvc; ++k) mma_commit(smem_u32(&sh->empty[slot + k]));
+                }
+            }
+            if (!ok) {  // no MMA may still run when the CTA leaves
+                mma_commit(smem_u32(&sh->drain));
+                mbar_wait(smem_u32(&sh->drain), 0, kTimeoutNs, nullptr);
+            }
+        }
     } else {
-        n = p.lens[s];
-        if (n < 0 || n > cap) bits = kStatusSeqRange, n = n < 0 ? 0 : cap;
-    }
-    const uint16_t* q = p.q + static_cast<int64_t>(r) * p.C;
-    float m = -INFINITY, l = 0.f, acc[16] = {};
-    for (int j0 = 0; j0 < n; j0 += 32) {
-        const int j = j0 + lane;
-        float x = 0.f;
-        const uint16_t* row = nullptr;
-        if (j < n) {
-            const int page = p.table[static_cast<int64_t>(s) * p.max_pages + j / p.page_size];
-            if (page < 0 || page >= p.num_pages) bits |= kStatusPageRange;
-            else row = p.cache + (static_cast<int64_t>(page) * p.page_size + j % p.page_size) * p.C;
-            if (row)
-                for (int d = 0; d < p.C; ++d) x = fmaf(bf16f(q[d]), bf16f(row[d]), x);
+        // --------------------------------------------------------------- TMA
+        // One lane per chunk; the rows of 32 boxes ahead are looked up by the lanes together.
+        const int per = kKeys / p.box;  // boxes per step
+        uint32_t issued = 0;            // uses of this lane's two slots
+        int bits = 0;
+        bool armed = true;              // this lane's wait for its slot succeeded
+        while (ok && walk.next(p, &x)) {
+            const int boxes = x.n * per;
+            int rows = 0;
+            for (int i = 0; i < boxes && ok; ++i) {
+                if ((i & 31) == 0) {
+                    const int key = x.key0 + (i + lane) * p.box;
+                    rows = p.num_rows;  // outside the cache: reads as zeros
+                    if (i + lane < boxes && key < x.end) {
+                        const int page = p.table[static_cast<int64_t>(x.page_row) * p.max_pages + key / p.page_size];
+                        if (page >= 0 && page < p.num_pages) rows = page * p.page_size + key % p.page_size;
+                        else bits |= kStatusPageRange;
+                    }
+                }
+                const int row = __shfl_sync(~0u, rows, i & 31);
+                const int in = i % per;
+                if (lane < chunks) {
+                    const int slot = (step & 1) * chunks + lane;
+                    const uint32_t bar = smem_u32(&sh->full[slot]);
+                    if (in == 0) {
+                        armed = wait(&sh->empty[slot], (step >> 1) ^ 1);
+                        if (armed) {
+                            mbar_arrive_expect_tx(bar, kSlotBytes);
+                            ++issued;
+                        }
+                    }
+                    if (armed) tma_load_3d(sm_ring + slot * kSlotBytes + in * p.box * 128, &tm_c, bar, chunk_at(lane) * 64, 0, row);
+                }
+                if (in == per - 1) {
+                    ++step;
+                    ok = __all_sync(~0u, armed);
+                }
+            }
         }
-        x = j < n ? x * p.scale : -INFINITY;
-        float mx = x;
-        for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, o));
-        const float mn = fmaxf(m, mx), ref = mn == -INFINITY ? 0.f : mn;
-        const float keep = expf(m - ref), e = j < n ? expf(x - ref) : 0.f;
-        float sum = e;
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        l = l * keep + sum;
-        m = mn;
-        for (int i = 0; i < 16; ++i) acc[i] *= keep;
-        for (int i = 0; i < 32 && j0 + i < n; ++i) {
-            const float w = __shfl_sync(~0u, e, i);
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(
-                __shfl_sync(~0u, reinterpret_cast<unsigned long long>(row), i));
-            if (!v) continue;
-            for (int c = 0; c < 16; ++c)
-                if (c * 32 + lane < p.Lkv) acc[c] = fmaf(w, bf16f(v[c * 32 + lane]), acc[c]);
-        }
+        // no copy may still be landing when the CTA leaves
+        for (uint32_t u = issued > 2 ? issued - 2 : 0; u < issued; ++u)
+            mbar_wait(smem_u32(&sh->full[(u & 1) * chunks + lane]), (u >> 1) & 1, kTimeoutNs, nullptr);
+        if (bits) raise_status(p.status, bits);
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int c = 0; c < 16; ++c)
-        if (c * 32 + lane < p.Lkv)
-            p.out[static_cast<int64_t>(r) * p.Lkv + c * 32 + lane] = static_cast<uint16_t>(pack_bf16x2(acc[c] * inv, 0.f) & 0xFFFFu);
-    if (lane == 0 && p.lse) p.lse[r] = l == 0.f ? -INFINITY : m + logf(l);
-    raise_status(p.status, bits);
+    if (!ok) {
+        sh->abort_flag = 1;
+        raise_status(p.status, kStatusWaitTimeout);
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the partial results of each row, in the order of the cut; a row with
+// one piece was finished by that piece.  One warp per row.
+__global__ void __launch_bounds__(128) mla_attend_join_kernel(const CacheParams p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+    if (row >= static_cast<int64_t>(p.B) * p.H) return;
+    const Cut cut = *p.cut;
+    const int b = static_cast<int>(row / p.H), h = static_cast<int>(row % p.H);
+    int trow, bits = 0;
+    const int len = batch_len(p, b, &trow, &bits);
+    // the tile of the prefix, the tile of the own keys: cost, steps, units that hold steps of it, partial row
+    int64_t base[2], part[2];
+    int steps[2], u0[2], u1[2], count = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if (k == 0) {
+            steps[0] = len >= cut.shared ? cut.shared / kKeys : 0;
+            base[0] = row / kRows * (cut.shared / kKeys + kOverhead);
+            part[0] = row;
+        } else {
+            steps[1] = own_steps(len, cut.shared);
+            base[1] = p.bases[b] + static_cast<int64_t>(h / kRows) * (steps[1] + kOverhead);
+            part[1] = static_cast<int64_t>(p.row_tiles) * kRows + row;
+        }
+        u0[k] = static_cast<int>((base[k] + kOverhead) / cut.run);
+        u1[k] = steps[k] ? static_cast<int>((base[k] + kOverhead + steps[k] - 1) / cut.run) : u0[k] - 1;
+        count += u1[k] - u0[k] + 1;
+    }
+    if (count == 1) return;
+    float top = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        for (int u = u0[k]; u <= u1[k]; ++u) {
+            const float v = p.part_lse[part_row(p, part[k], u)];
+            top = v != v ? v : fmaxf(top, v);
+        }
+    const float ref = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 acc[4] = {};
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        for (int u = u0[k]; u <= u1[k]; ++u) {
+            const int64_t at = part_row(p, part[k], u);
+            const float w = exp2f(p.part_lse[at] - ref);
+            sum += w;
+            const float4* o = reinterpret_cast<const float4*>(p.part_o + at * p.Lkv);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((i * 32 + lane) * 4 < p.Lkv) {
+                    const float4 v = o[i * 32 + lane];
+                    acc[i].x = fmaf(w, v.x, acc[i].x), acc[i].y = fmaf(w, v.y, acc[i].y);
+                    acc[i].z = fmaf(w, v.z, acc[i].z), acc[i].w = fmaf(w, v.w, acc[i].w);
+                }
+        }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if ((i * 32 + lane) * 4 < p.Lkv)
+            reinterpret_cast<uint2*>(p.out + row * p.Lkv)[i * 32 + lane] =
+                make_uint2(pack_bf16x2(acc[i].x * inv, acc[i].y * inv), pack_bf16x2(acc[i].z * inv, acc[i].w * inv));
+    if (lane == 0 && p.lse) p.lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * kLn2;
 }
 
 int check_cache_dims(const mla_prolog_cache_dims& d) {
@@ -94,6 +672,30 @@ int check_cache_dims(const mla_prolog_cache_dims& d) {
     return MLA_OK;
 }
 
+// Workspace: the cut, the costs before each sequence, the partial results.
+struct Layout {
+    int row_tiles, head_tiles, halves, units;
+    size_t bases, part_lse, part_o, bytes;
+};
+
+Layout layout(const mla_prolog_cache_dims& d, int sms) {
+    Layout y;
+    const int64_t rows = static_cast<int64_t>(d.batch) * d.num_heads;
+    y.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
+    y.head_tiles = (d.num_heads + kRows - 1) / kRows;
+    y.halves = d.kv_lora_rank > kHalf ? 2 : 1;
+    y.units = sms / y.halves > 0 ? sms / y.halves : 1;
+    auto round = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t parts = static_cast<size_t>(y.row_tiles) * kRows + rows + static_cast<size_t>(y.units) * kRows;
+    y.bases = round(sizeof(Cut));
+    y.part_lse = y.bases + round(sizeof(int64_t) * d.batch);
+    y.part_o = y.part_lse + round(sizeof(float) * parts);
+    y.bytes = y.part_o + sizeof(float) * parts * d.kv_lora_rank;
+    return y;
+}
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
+
 }  // namespace
 }  // namespace mlap
 
@@ -104,9 +706,9 @@ extern "C" {
 int mla_prolog_attend_cache_workspace(const mla_prolog_cache_dims* d, size_t* bytes) {
     if (!d || !bytes) return MLA_ERR_INVALID_ARG;
     *bytes = 0;
-    const int rc = check_cache_dims(*d);
-    if (rc != MLA_OK) return rc;
-    *bytes = 16;
+    int rc = check_cache_dims(*d), sms;
+    if (rc != MLA_OK || (rc = current_sm103(&sms)) != MLA_OK) return rc;
+    *bytes = layout(*d, sms).bytes;
     return MLA_OK;
 }
 
@@ -122,19 +724,34 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     if (!ptr_ok(q, 16) || !ptr_ok(out, 16) || (d->num_pages && !ptr_ok(kv_cache, 16))) return MLA_ERR_INVALID_ARG;
     if (d->table_rows && (!ptr_ok(page_table, 4) || !ptr_ok(seq_lens, 4))) return MLA_ERR_INVALID_ARG;
     if ((seqs && !ptr_ok(seqs, 4)) || (shared_len && !ptr_ok(shared_len, 4)) || (lse && !ptr_ok(lse, 4)) ||
-        (status && !ptr_ok(status, 4)))
+        (status && !ptr_ok(status, 4)) || !ptr_ok(workspace, 16))
         return MLA_ERR_INVALID_ARG;
     int sms;
     if ((rc = current_sm103(&sms)) != MLA_OK) return rc;
-    size_t need = 0;
-    if ((rc = mla_prolog_attend_cache_workspace(d, &need)) != MLA_OK) return rc;
-    if (!ptr_ok(workspace, 16) || workspace_bytes < need) return MLA_ERR_INVALID_ARG;
-    CacheParams p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(kv_cache), page_table, seq_lens, seqs,
-                  shared_len, static_cast<uint16_t*>(out), lse, status, d->batch, d->num_heads, d->kv_lora_rank,
-                  d->kv_lora_rank + d->rope_dim, d->page_size, d->table_rows, d->max_pages, d->num_pages, d->scale};
-    mla_attend_cache_kernel<<<(d->batch * d->num_heads + 3) / 4, 128, 0, static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? MLA_OK : report_cuda(e, "launch mla_attend_cache_kernel");
+    const Layout y = layout(*d, sms);
+    if (workspace_bytes < y.bytes) return MLA_ERR_INVALID_ARG;
+    const int C = d->kv_lora_rank + d->rope_dim, box = gcd(d->page_size, kKeys);
+    const int64_t rows = d->num_pages * d->page_size;
+    CUtensorMap tm;
+    // an empty cache has no valid page: every read is outside the map, which then only needs a valid address
+    if (!encode_bf16_3d(&tm, rows ? kv_cache : q, C, 1, rows ? rows : 1, 1, box))
+        return report_cuda(cudaErrorInvalidValue, "tensor map of attend_cache");
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    CacheParams p{static_cast<const uint16_t*>(q), page_table, seq_lens, seqs, shared_len, static_cast<uint16_t*>(out),
+                  lse, status, reinterpret_cast<Cut*>(ws), reinterpret_cast<int64_t*>(ws + y.bases),
+                  reinterpret_cast<float*>(ws + y.part_o), reinterpret_cast<float*>(ws + y.part_lse), d->batch,
+                  d->num_heads, d->kv_lora_rank, C, d->page_size, d->table_rows, d->max_pages,
+                  static_cast<int>(rows ? rows : 1), static_cast<int>(d->num_pages), box, y.row_tiles, y.head_tiles,
+                  y.halves, y.units, d->scale};
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaFuncSetAttribute(mla_attend_cache_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return report_cuda(e, "mla_attend_cache_kernel attributes");
+    mla_attend_cache_kernel<<<y.units * y.halves, kThreads, kSmem, st>>>(tm, p);
+    if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
+    const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
+    mla_attend_join_kernel<<<static_cast<unsigned>(blocks), 128, 0, st>>>(p);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? MLA_OK : report_cuda(e, "launch mla_attend_join_kernel");
 }
 
 }  // extern "C"
