@@ -492,26 +492,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
             const uint32_t idesc_o = idesc_bf16_f32(kRows, dv) | kIdescBMnMajor;
+            constexpr uint64_t kSlotStep = kSlotBytes >> 4;
+            const uint64_t dq = smem_desc_sw128(sm_q), dk = smem_desc_sw128(sm_ring);
+            const uint64_t dp = smem_desc_sw128(sm_p), dvals = smem_desc_sw128_mn(sm_ring, kSlotBytes);
+            const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
+            const uint32_t d = tmem + kColS;
             auto scores = [&](int st) {
                 if (st > 0) ok = wait(&sh->s_free, st - 1);
+                const int base = (st & 1) * chunks;
                 for (int pos = 0; pos < chunks && ok; ++pos) {
-                    const int slot = (st & 1) * chunks + pos, ck = chunk_at(pos);
-                    ok = wait(&sh->full[slot], st >> 1);
+                    const int slot = base + pos, ck = chunk_at(pos);
+                    ok = mbar_wait(full0 + 8 * slot, (st >> 1) & 1, kTimeoutNs, abort_flag);
                     if (!ok) return;
                     tc_fence_after();
-                    const uint64_t b = smem_desc_sw128(sm_ring + slot * kSlotBytes);
+                    const uint64_t b = dk + slot * kSlotStep;
                     const int ks = min(4, (p.C - ck * 64) / 16);
                     if (ck < kTmemChunks) {
-                        for (int k = 0; k < ks; ++k)
-                            mma_bf16_ts(tmem + kColS, tmem + kColQ + ck * 32 + k * 8, b + 2 * k, idesc_s, pos > 0 || k > 0);
+                        const uint32_t a = tmem + kColQ + ck * 32;
+                        mma_bf16_ts(d, a, b, idesc_s, pos > 0);
+                        if (ks == 4) {
+#pragma unroll
+                            for (int k = 1; k < 4; ++k) mma_bf16_ts(d, a + k * 8, b + 2 * k, idesc_s, 1);
+                        } else {
+                            for (int k = 1; k < ks; ++k) mma_bf16_ts(d, a + k * 8, b + 2 * k, idesc_s, 1);
+                        }
                     } else {
-                        const uint64_t a = smem_desc_sw128(sm_q + (ck - kTmemChunks) * kQBytes);
-                        for (int k = 0; k < ks; ++k) mma_bf16(tmem + kColS, a + 2 * k, b + 2 * k, idesc_s, pos > 0 || k > 0);
+                        const uint64_t a = dq + (ck - kTmemChunks) * (kQBytes >> 4);
+                        mma_bf16(d, a, b, idesc_s, pos > 0);
+                        if (ks == 4) {
+#pragma unroll
+                            for (int k = 1; k < 4; ++k) mma_bf16(d, a + 2 * k, b + 2 * k, idesc_s, 1);
+                        } else {
+                            for (int k = 1; k < ks; ++k) mma_bf16(d, a + 2 * k, b + 2 * k, idesc_s, 1);
+                        }
                     }
-                    if (pos < others) mma_commit(smem_u32(&sh->empty[slot]));
+                    if (pos < others) mma_commit(empty0 + 8 * slot);
                 }
                 if (ok) mma_commit(smem_u32(&sh->s_full));
             };
@@ -525,12 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const int slot = (step & 1) * chunks + others;
-                    const uint64_t a = smem_desc_sw128(sm_p);
-                    const uint64_t b = smem_desc_sw128_mn(sm_ring + slot * kSlotBytes, kSlotBytes);
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_bf16(tmem + kColO, a + 2 * k, b + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
+                    const uint64_t b = dvals + slot * kSlotStep;
+                    mma_bf16(tmem + kColO, dp, b, idesc_o, j > 0);
+#pragma unroll
+                    for (int k = 1; k < kKeys / 16; ++k)
+                        mma_bf16(tmem + kColO, dp + 2 * k, b + k * (2048 >> 4), idesc_o, 1);
                     mma_commit(smem_u32(&sh->pv_done));
-                    for (int k = 0; k < nvc; ++k) mma_commit(smem_u32(&sh->empty[slot + k]));
+                    for (int k = 0; k < nvc; ++k) mma_commit(empty0 + 8 * (slot + k));
                 }
             }
             if (!ok) {  // no MMA may still run when the CTA leaves

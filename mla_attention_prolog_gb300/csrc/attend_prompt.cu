@@ -401,59 +401,83 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA
-        if (lane == 0) {
+        if (elect_one()) {
             const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
             const uint32_t idesc_o = idesc_bf16_f32(kTile, p.Dv) | kIdescBMnMajor;
-            const int ksteps = p.Dqk / 16;
-            auto wait_slots = [&](int use, int count) {
-                for (int i = 0; i < count && ok; ++i)
-                    ok = mbar_wait(smem_u32(&sh->full[slot_of(use + i)]), full_parity(use + i), kTimeoutNs, abort_flag);
-                tc_fence_after();
+            constexpr uint64_t kSlotStep = kSlotBytes >> 4;
+            const uint64_t dq = smem_desc_sw128(sm_q), dk = smem_desc_sw128(sm_ring);
+            const uint64_t dv = smem_desc_sw128_mn(sm_ring, kSlotBytes);
+            const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
+            // a place in the ring: slot, and the parity of its current use
+            struct Place {
+                int slot;
+                uint32_t parity;
             };
-            auto free_slots = [&](int use, int count) {
-                for (int i = 0; i < count; ++i) mma_commit(smem_u32(&sh->empty[slot_of(use + i)]));
+            auto after = [&](Place x, int n) {
+                x.slot += n;
+                if (x.slot >= p.slots) x.slot -= p.slots, x.parity ^= 1u;
+                return x;
             };
-            auto last_user = [&](int t, int j) { return t == 1 || j >= n[1]; };
-            auto scores = [&](int t, int j) {
-                const int use = j * span;
-                wait_slots(use, nqk);
-                if (!ok) return;
-                for (int k = 0; k < ksteps; ++k) {
-                    const uint64_t a = smem_desc_sw128(sm_q + (t * nqk + (k >> 2)) * kSlotBytes) + 2 * (k & 3);
-                    const uint64_t b = smem_desc_sw128(sm_ring + slot_of(use + (k >> 2)) * kSlotBytes) + 2 * (k & 3);
-                    mma_bf16(tmem + kColS + t * kTile, a, b, idesc_s, k > 0);
+            auto scores = [&](int t, Place at, bool last) {
+                const uint64_t a0 = dq + t * nqk * kSlotStep;
+                const uint32_t d = tmem + kColS + t * kTile;
+                for (int cidx = 0; cidx < nqk; ++cidx) {
+                    const Place x = after(at, cidx);
+                    ok = mbar_wait(full0 + 8 * x.slot, x.parity, kTimeoutNs, abort_flag);
+                    if (!ok) return;
+                    tc_fence_after();
+                    const uint64_t a = a0 + cidx * kSlotStep, b = dk + x.slot * kSlotStep;
+                    const int ks = min(4, p.Dqk / 16 - cidx * 4);
+                    mma_bf16(d, a, b, idesc_s, cidx > 0);
+                    if (ks == 4) {
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) mma_bf16(d, a + 2 * k, b + 2 * k, idesc_s, 1);
+                    } else {
+                        for (int k = 1; k < ks; ++k) mma_bf16(d, a + 2 * k, b + 2 * k, idesc_s, 1);
+                    }
                 }
                 mma_commit(smem_u32(&sh->s_full[t]));
-                if (last_user(t, j)) free_slots(use, nqk);
+                if (last)
+                    for (int cidx = 0; cidx < nqk; ++cidx) mma_commit(empty0 + 8 * after(at, cidx).slot);
             };
+            Place kp{0, 0}, vp{0, 0};
             for (int t = 0; t < 2 && ok; ++t)
                 if (n[t]) {
                     ok = mbar_wait(smem_u32(&sh->q_full[t]), 0, kTimeoutNs, abort_flag);
                     tc_fence_after();
-                    if (ok) scores(t, 0);
+                    if (ok) scores(t, kp, t == 1 || n[1] == 0);
                 }
-            for (int j = 0; j < nmax && ok; ++j)
+            for (int j = 0; j < nmax && ok; ++j) {
+                vp = after(kp, nqk);
+                kp = after(vp, nv);
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (j >= n[t]) continue;
-                    const int use = j * span + nqk;
-                    wait_slots(use, nv);
+                    for (int cidx = 0; cidx < nv && ok; ++cidx) {
+                        const Place x = after(vp, cidx);
+                        ok = mbar_wait(full0 + 8 * x.slot, x.parity, kTimeoutNs, abort_flag);
+                    }
                     if (ok) ok = mbar_wait(smem_u32(&sh->p_full[t]), j & 1, kTimeoutNs, abort_flag);
                     tc_fence_after();
                     if (!ok) break;
+                    const uint32_t o = tmem + kColO + t * kTile, pr = tmem + kColS + t * kTile;
                     // one product over V's two slots where they are neighbours, two of 64 columns where the ring wraps
-                    const bool whole = nv == 1 || slot_of(use + 1) == slot_of(use) + 1;
+                    const bool whole = nv == 1 || vp.slot + 1 < p.slots;
                     for (int cidx = 0; cidx < (whole ? 1 : nv); ++cidx) {
-                        const uint64_t b = smem_desc_sw128_mn(sm_ring + slot_of(use + cidx) * kSlotBytes, kSlotBytes);
+                        const uint64_t b = dv + after(vp, cidx).slot * kSlotStep;
                         const uint32_t cols = whole ? p.Dv : min(64, p.Dv - cidx * 64);
                         const uint32_t idesc = (idesc_o & ~(0x3Fu << 17)) | (cols >> 3) << 17;
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_bf16_ts(tmem + kColO + t * kTile + cidx * 64, tmem + kColS + t * kTile + k * 8,
-                                        b + k * (2048 >> 4), idesc, j > 0 || k > 0);
+                        mma_bf16_ts(o + cidx * 64, pr, b, idesc, j > 0);
+#pragma unroll
+                        for (int k = 1; k < kTile / 16; ++k)
+                            mma_bf16_ts(o + cidx * 64, pr + k * 8, b + k * (2048 >> 4), idesc, 1);
                     }
                     mma_commit(smem_u32(&sh->o_done[t]));
-                    if (last_user(t, j)) free_slots(use, nv);
-                    if (j + 1 < n[t]) scores(t, j + 1);
+                    const bool last = t == 1 || j >= n[1];
+                    if (last)
+                        for (int cidx = 0; cidx < nv; ++cidx) mma_commit(empty0 + 8 * after(vp, cidx).slot);
+                    if (j + 1 < n[t]) scores(t, kp, t == 1 || j + 1 >= n[1]);
                 }
+            }
             if (!ok) {  // no MMA may still run when the CTA leaves
                 mma_commit(smem_u32(&sh->drain));
                 mbar_wait(smem_u32(&sh->drain), 0, kTimeoutNs, nullptr);
@@ -493,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (!ok) {
         sh->abort_flag = 1;
-        if (lane == 0) raise_status(p.status, kStatusWaitTimeout);
+        raise_status(p.status, kStatusWaitTimeout);
     }
     __syncwarp();
     tc_fence_before();

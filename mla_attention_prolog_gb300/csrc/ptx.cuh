@@ -567,6 +567,20 @@ __device__ __forceinline__ uint64_t smem_desc_sw128_mn(uint32_t addr, uint32_t m
 }
 constexpr uint32_t kIdescBMnMajor = 1u << 16;  // B is MN-major (its rows run along K)
 
+// True in one lane of a converged warp.  The MMA loops run under it with their
+// instructions unrolled and the descriptors a constant apart: an issuing
+// thread that computes each descriptor in a rolled loop takes ~100 cycles per
+// instruction, more than a 128 x 128 x 16 product (64 cycles) lasts.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // 3-D tiled bulk tensor load global -> shared (c0 innermost, elements).
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t c0, int32_t c1,
                                             int32_t c2) {
