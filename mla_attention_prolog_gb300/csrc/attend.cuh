@@ -31,22 +31,30 @@ inline int current_sm103(int* sms) {
     return major == 10 && minor == 3 ? MLA_OK : MLA_ERR_DEVICE;
 }
 
-// BF16 operand [outer, mid, inner] (contiguous), loaded in boxes of box_outer
-// x box_mid x 64 columns with 128-byte swizzle; what lies outside reads as 0.
-inline bool encode_bf16_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,
-                           uint32_t box_mid, uint32_t box_outer) {
+inline bool encode_bf16_dims(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3],
+                             const cuuint64_t (&strides)[2], const cuuint32_t (&box)[3]) {
     auto fn = reinterpret_cast<CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                             const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
                                             CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
                                             CUtensorMapFloatOOBfill)>(tensor_map_encoder());
-    if (!fn) return false;
-    const cuuint64_t dims[3] = {inner, mid, outer};
-    const cuuint64_t strides[2] = {inner * 2, inner * mid * 2};
-    const cuuint32_t box[3] = {64, box_mid, box_outer};
     const cuuint32_t estr[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn && fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// BF16 operand [outer, mid, inner] (contiguous), loaded in boxes of box_outer
+// x box_mid x 64 columns with 128-byte swizzle; what lies outside reads as 0.
+inline bool encode_bf16_3d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t mid, uint64_t outer,
+                           uint32_t box_mid, uint32_t box_outer) {
+    return encode_bf16_dims(m, base, {inner, mid, outer}, {inner * 2, inner * mid * 2}, {64, box_mid, box_outer});
+}
+
+// The whole 64-column chunks of a BF16 operand [rows, inner] as [chunk][row]
+// [64]: one copy brings `count` chunks of box_rows rows, chunk after chunk.
+inline bool encode_bf16_chunks(CUtensorMap* m, const void* base, uint64_t inner, uint64_t rows, uint32_t box_rows,
+                               uint32_t count) {
+    return encode_bf16_dims(m, base, {64, rows, inner / 64}, {inner * 2, 128}, {64, box_rows, count});
 }
 
 __device__ __forceinline__ void raise_status(int32_t* status, int bits) {

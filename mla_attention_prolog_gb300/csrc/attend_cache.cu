@@ -34,6 +34,8 @@ constexpr int kKeys = 64;                 // keys per step
 constexpr int kSlotBytes = kKeys * 128;   // 64 keys x 64 BF16 columns
 constexpr int kQBytes = kRows * 128;      // 128 rows x 64 BF16 columns
 constexpr int kMaxChunks = 9;             // 64-column chunks of a cache row
+constexpr int kGroup = 4;                 // chunks per TMA copy and barrier (the columns of O of one CTA)
+constexpr int kMaxGroups = 3;
 constexpr int kTmemChunks = 6;            // chunks of Q kept in TMEM
 constexpr int kHalf = 256;                // columns of O per CTA
 constexpr int kThreads = 192;
@@ -179,10 +181,10 @@ struct Walk {
 };
 
 struct Shared {
-    uint64_t full[2 * kMaxChunks], empty[2 * kMaxChunks];
+    uint64_t full[2][kMaxGroups], empty[2][kMaxGroups];  // per stage and group of chunks
     uint64_t q_full, s_full, s_free, p_full, pv_done, drain;
     uint32_t tmem;
-    int abort_flag;
+    int abort_flag, loaded;
     int64_t scan[kThreads / 32];
     int64_t total, first_base;
     int first_b, sharers, source, shared;
@@ -290,7 +292,8 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_c, const CacheParams p) {
+    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_g,
+                            const CacheParams p) {
     extern __shared__ uint8_t raw[];
     const uint32_t raw_at = smem_u32(raw);
     const uint32_t pad = (1024u - (raw_at & 1023u)) & 1023u;
@@ -300,18 +303,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            2 * kMaxChunks * kSlotBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = blockIdx.x / p.halves, half = blockIdx.x % p.halves;
-    // this CTA's columns of O, the chunks that hold them (loaded last, kept longest)
+    // This CTA's columns of O lie in the chunks of group `half`, which are
+    // multiplied last and kept until P V has read them.
     const int dv0 = half * kHalf, dv = min(kHalf, p.Lkv - dv0);
-    const int vc0 = dv0 / 64, nvc = (dv + 63) / 64, others = chunks - nvc;
-    auto chunk_at = [&](int pos) { return pos < others ? (pos < vc0 ? pos : pos + nvc) : vc0 + pos - others; };
+    const int nvc = (dv + 63) / 64, groups = (chunks + kGroup - 1) / kGroup;
+    auto group_at = [&](int i) { return i == groups - 1 ? half : (i < half ? i : i + 1); };
+    auto group_chunks = [&](int g) { return min(kGroup, chunks - g * kGroup); };
 
     Walk walk;
     if (!make_cut(p, unit, sh, &walk)) return;
     if (warp == kLoadWarp && lane == 0) {
-        for (int s = 0; s < 2 * chunks; ++s) {
-            mbar_init(smem_u32(&sh->full[s]), 1);
-            mbar_init(smem_u32(&sh->empty[s]), 1);
-        }
+        for (int s = 0; s < 2; ++s)
+            for (int g = 0; g < groups; ++g) {
+                mbar_init(smem_u32(&sh->full[s][g]), 1);
+                mbar_init(smem_u32(&sh->empty[s][g]), 1);
+            }
         mbar_init(smem_u32(&sh->q_full), kRows);
         mbar_init(smem_u32(&sh->s_full), 1);
         mbar_init(smem_u32(&sh->s_free), kRows);
@@ -319,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh->pv_done), 1);
         mbar_init(smem_u32(&sh->drain), 1);
         sh->abort_flag = 0;
+        sh->loaded = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -440,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     st_shared_v4(dst + ((i ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 if (left < kKeys) {
                     // rows behind the end may hold anything: as values they have to be zero
-                    const int st = (step & 1) * chunks + others;
+                    const int st = (step & 1) * chunks + half * kGroup;
                     for (int k = r; k < (kKeys - left) * nvc * 8; k += kRows) {
                         const int row = left + k / (nvc * 8), in = k % (nvc * 8);
                         st_shared_v4(sm_ring + (st + in / 8) * kSlotBytes + row * 128 + (in & 7) * 16, 0, 0, 0, 0);
@@ -498,40 +505,41 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint64_t kSlotStep = kSlotBytes >> 4;
             const uint64_t dq = smem_desc_sw128(sm_q), dk = smem_desc_sw128(sm_ring);
             const uint64_t dp = smem_desc_sw128(sm_p), dvals = smem_desc_sw128_mn(sm_ring, kSlotBytes);
-            const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
             const uint32_t d = tmem + kColS;
             auto scores = [&](int st) {
                 if (st > 0) ok = wait(&sh->s_free, st - 1);
-                const int base = (st & 1) * chunks;
-                for (int pos = 0; pos < chunks && ok; ++pos) {
-                    const int slot = base + pos, ck = chunk_at(pos);
-                    ok = mbar_wait(full0 + 8 * slot, (st >> 1) & 1, kTimeoutNs, abort_flag);
+                for (int i = 0; i < groups && ok; ++i) {
+                    const int g = group_at(i), nc = group_chunks(g);
+                    ok = wait(&sh->full[st & 1][g], st >> 1);
                     if (!ok) return;
                     tc_fence_after();
-                    const uint64_t b = dk + slot * kSlotStep;
-                    const int ks = min(4, (p.C - ck * 64) / 16);
-                    if (ck < kTmemChunks) {
-                        const uint32_t a = tmem + kColQ + ck * 32;
-                        mma_bf16_ts(d, a, b, idesc_s, pos > 0);
-                        if (ks == 4) {
+                    for (int k = 0; k < nc; ++k) {
+                        const int ck = g * kGroup + k;
+                        const uint64_t b = dk + ((st & 1) * chunks + ck) * kSlotStep;
+                        const int ks = min(4, p.C / 16 - ck * 4);
+                        if (ck < kTmemChunks) {
+                            const uint32_t a = tmem + kColQ + ck * 32;
+                            mma_bf16_ts(d, a, b, idesc_s, i > 0 || k > 0);
+                            if (ks == 4) {
 #pragma unroll
-                            for (int k = 1; k < 4; ++k) mma_bf16_ts(d, a + k * 8, b + 2 * k, idesc_s, 1);
+                                for (int e = 1; e < 4; ++e) mma_bf16_ts(d, a + e * 8, b + 2 * e, idesc_s, 1);
+                            } else {
+                                for (int e = 1; e < ks; ++e) mma_bf16_ts(d, a + e * 8, b + 2 * e, idesc_s, 1);
+                            }
                         } else {
-                            for (int k = 1; k < ks; ++k) mma_bf16_ts(d, a + k * 8, b + 2 * k, idesc_s, 1);
-                        }
-                    } else {
-                        const uint64_t a = dq + (ck - kTmemChunks) * (kQBytes >> 4);
-                        mma_bf16(d, a, b, idesc_s, pos > 0);
-                        if (ks == 4) {
+                            const uint64_t a = dq + (ck - kTmemChunks) * (kQBytes >> 4);
+                            mma_bf16(d, a, b, idesc_s, i > 0 || k > 0);
+                            if (ks == 4) {
 #pragma unroll
-                            for (int k = 1; k < 4; ++k) mma_bf16(d, a + 2 * k, b + 2 * k, idesc_s, 1);
-                        } else {
-                            for (int k = 1; k < ks; ++k) mma_bf16(d, a + 2 * k, b + 2 * k, idesc_s, 1);
+                                for (int e = 1; e < 4; ++e) mma_bf16(d, a + 2 * e, b + 2 * e, idesc_s, 1);
+                            } else {
+                                for (int e = 1; e < ks; ++e) mma_bf16(d, a + 2 * e, b + 2 * e, idesc_s, 1);
+                            }
                         }
                     }
-                    if (pos < others) mma_commit(empty0 + 8 * slot);
+                    if (g != half) mma_commit(smem_u32(&sh->empty[st & 1][g]));
                 }
-                if (ok) mma_commit(smem_u32(&sh->s_full));
+                mma_commit(smem_u32(&sh->s_full));
             };
             for (int piece = 0; ok && walk.next(p, &x); ++piece) {
                 ok = wait(&sh->q_full, piece);
@@ -542,14 +550,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (ok) ok = wait(&sh->p_full, step);
                     if (!ok) break;
                     tc_fence_after();
-                    const int slot = (step & 1) * chunks + others;
-                    const uint64_t b = dvals + slot * kSlotStep;
+                    const uint64_t b = dvals + ((step & 1) * chunks + half * kGroup) * kSlotStep;
                     mma_bf16(tmem + kColO, dp, b, idesc_o, j > 0);
 #pragma unroll
                     for (int k = 1; k < kKeys / 16; ++k)
                         mma_bf16(tmem + kColO, dp + 2 * k, b + k * (2048 >> 4), idesc_o, 1);
                     mma_commit(smem_u32(&sh->pv_done));
-                    for (int k = 0; k < nvc; ++k) mma_commit(empty0 + 8 * (slot + k));
+                    mma_commit(smem_u32(&sh->empty[step & 1][half]));
                 }
             }
             if (!ok) {  // no MMA may still run when the CTA leaves
@@ -559,15 +566,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // --------------------------------------------------------------- TMA
-        // One lane per chunk; the rows of 32 boxes ahead are looked up by the lanes together.
+        // The lanes look up the rows of 32 boxes ahead; one thread issues the copies.
         const int per = kKeys / p.box;  // boxes per step
-        uint32_t issued = 0;            // uses of this lane's two slots
         int bits = 0;
-        bool armed = true;              // this lane's wait for its slot succeeded
         while (ok && walk.next(p, &x)) {
             const int boxes = x.n * per;
             int rows = 0;
-            for (int i = 0; i < boxes && ok; ++i) {
+            for (int j = 0; j < x.n && ok; ++j) {
+                const int i = j * per;
                 if ((i & 31) == 0) {
                     const int key = x.key0 + (i + lane) * p.box;
                     rows = p.num_rows;  // outside the cache: reads as zeros
@@ -577,29 +583,41 @@ __global__ void __launch_bounds__(kThreads, 1)
                         else bits |= kStatusPageRange;
                     }
                 }
-                const int row = __shfl_sync(~0u, rows, i & 31);
-                const int in = i % per;
-                if (lane < chunks) {
-                    const int slot = (step & 1) * chunks + lane;
-                    const uint32_t bar = smem_u32(&sh->full[slot]);
-                    if (in == 0) {
-                        armed = wait(&sh->empty[slot], (step >> 1) ^ 1);
-                        if (armed) {
-                            mbar_arrive_expect_tx(bar, kSlotBytes);
-                            ++issued;
+                int row[kKeys / 16];
+#pragma unroll
+                for (int k = 0; k < kKeys / 16; ++k) row[k] = __shfl_sync(~0u, rows, (i + k) & 31);
+                if (elect_one()) {
+                    const int st = step & 1;
+                    for (int k = 0; k < groups && ok; ++k) {
+                        const int g = group_at(k), nc = group_chunks(g);
+                        const uint32_t bar = smem_u32(&sh->full[st][g]);
+                        ok = wait(&sh->empty[st][g], (step >> 1) ^ 1);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(bar, nc * kSlotBytes);
+                        sh->loaded = step * groups + k + 1;
+                        const uint32_t dst = sm_ring + (st * chunks + g * kGroup) * kSlotBytes;
+#pragma unroll
+                        for (int e = 0; e < kKeys / 16; ++e) {
+                            if (e >= per) break;
+                            const uint32_t at = dst + e * p.box * 128;
+                            if (nc == kGroup && (g + 1) * kGroup * 64 <= p.C && p.box == kKeys) {
+                                tma_load_3d(at, &tm_g, bar, 0, row[e], g * kGroup);
+                            } else {
+                                for (int cidx = 0; cidx < nc; ++cidx)
+                                    tma_load_3d(at + cidx * kSlotBytes, &tm_c, bar, (g * kGroup + cidx) * 64, 0, row[e]);
+                            }
                         }
                     }
-                    if (armed) tma_load_3d(sm_ring + slot * kSlotBytes + in * p.box * 128, &tm_c, bar, chunk_at(lane) * 64, 0, row);
                 }
-                if (in == per - 1) {
-                    ++step;
-                    ok = __all_sync(~0u, armed);
-                }
+                __syncwarp();
+                ok = __all_sync(~0u, ok);
+                ++step;
             }
         }
         // no copy may still be landing when the CTA leaves
-        for (uint32_t u = issued > 2 ? issued - 2 : 0; u < issued; ++u)
-            mbar_wait(smem_u32(&sh->full[(u & 1) * chunks + lane]), (u >> 1) & 1, kTimeoutNs, nullptr);
+        if (lane == 0)
+            for (int u = max(sh->loaded - 2 * groups, 0); u < sh->loaded; ++u)
+                mbar_wait(smem_u32(&sh->full[u / groups & 1][group_at(u % groups)]), (u / groups >> 1) & 1, kTimeoutNs, nullptr);
         if (bits) raise_status(p.status, bits);
     }
     if (!ok) {
@@ -751,9 +769,13 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     if (workspace_bytes < y.bytes) return MLA_ERR_INVALID_ARG;
     const int C = d->kv_lora_rank + d->rope_dim, box = gcd(d->page_size, kKeys);
     const int64_t rows = d->num_pages * d->page_size;
-    CUtensorMap tm;
+    CUtensorMap tm, tm_group;
     // an empty cache has no valid page: every read is outside the map, which then only needs a valid address
     if (!encode_bf16_3d(&tm, rows ? kv_cache : q, C, 1, rows ? rows : 1, 1, box))
+        return report_cuda(cudaErrorInvalidValue, "tensor map of attend_cache");
+    // the same rows by whole chunks, [chunk][row][64]: a copy of kGroup chunks lands chunk after chunk
+    if (C >= 64 * kGroup ? !encode_bf16_chunks(&tm_group, rows ? kv_cache : q, C, rows ? rows : 1, box, kGroup)
+                         : (tm_group = tm, false))
         return report_cuda(cudaErrorInvalidValue, "tensor map of attend_cache");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     CacheParams p{static_cast<const uint16_t*>(q), page_table, seq_lens, seqs, shared_len, static_cast<uint16_t*>(out),
@@ -765,7 +787,7 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaFuncSetAttribute(mla_attend_cache_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return report_cuda(e, "mla_attend_cache_kernel attributes");
-    mla_attend_cache_kernel<<<y.units * y.halves, kThreads, kSmem, st>>>(tm, p);
+    mla_attend_cache_kernel<<<y.units * y.halves, kThreads, kSmem, st>>>(tm, tm_group, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
     const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
     mla_attend_join_kernel<<<static_cast<unsigned>(blocks), 128, 0, st>>>(p);
