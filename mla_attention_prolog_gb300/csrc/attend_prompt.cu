@@ -30,6 +30,7 @@ namespace {
 constexpr int kTile = 128;                 // query rows per tile, keys per tile
 constexpr int kSlotBytes = kTile * 128;    // 128 rows x 64 BF16 columns: one TMA box
 constexpr int kMaxSlots = 8;
+constexpr int kAhead = 4;                  // K (V) tiles whose barriers are in use at once
 constexpr int kThreads = 320;
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kMiscBytes = 512;
@@ -59,13 +60,18 @@ struct PromptParams {
 // Everything the roles share.  (Shared memory, after the tiles.)
 struct Shared {
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], drain;
-    uint64_t full[kMaxSlots], empty[kMaxSlots];
+    uint64_t k_full[kAhead], v_full[kAhead], k_free[kAhead], v_free[kAhead];  // of key tile j at j % kAhead
     uint32_t tmem;
     int abort_flag;
     int job[5];        // q0, nq, k0, nk, first row of the tile pair; job[1] = 0: nothing to do
     uint32_t bad[12];  // keys of the masked tiles whose v holds a NaN or an infinity
 };
 static_assert(sizeof(Shared) <= kMiscBytes, "");
+
+template <int N>
+struct Steps {
+    static constexpr int value = N;
+};
 
 struct Job {
     int q0, nq, k0, nk, r0;
@@ -193,9 +199,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(smem_u32(&sh->p_full[t]), kTile);
             mbar_init(smem_u32(&sh->o_done[t]), 1);
         }
-        for (int s = 0; s < p.slots; ++s) {
-            mbar_init(smem_u32(&sh->full[s]), 1);
-            mbar_init(smem_u32(&sh->empty[s]), 1);
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(smem_u32(&sh->k_full[i]), 1);
+            mbar_init(smem_u32(&sh->v_full[i]), 1);
+            mbar_init(smem_u32(&sh->k_free[i]), 1);
+            mbar_init(smem_u32(&sh->v_free[i]), 1);
         }
         mbar_init(smem_u32(&sh->drain), 1);
         sh->abort_flag = 0;
@@ -217,16 +225,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Keys that row r of the sequence sees: [0, limit(r)).
     const int off = jb.nk - jb.nq;
     auto limit = [&](int r) { return p.causal ? clampi(off + r + 1, 0, jb.nk) : jb.nk; };
-    int rows[2], n[2];
-    for (int t = 0; t < 2; ++t) {
-        rows[t] = clampi(jb.nq - jb.r0 - t * kTile, 0, kTile);
-        n[t] = rows[t] ? (limit(jb.r0 + t * kTile + rows[t] - 1) + kTile - 1) / kTile : 0;
-    }
-    const int nmax = n[0] > n[1] ? n[0] : n[1];
+    auto rows_of = [&](int t) { return clampi(jb.nq - jb.r0 - t * kTile, 0, kTile); };
+    auto tiles_of = [&](int t) {
+        const int rows = rows_of(t);
+        return rows ? (limit(jb.r0 + t * kTile + rows - 1) + kTile - 1) / kTile : 0;
+    };
+    const int n0 = tiles_of(0), n1 = tiles_of(1), nmax = max(n0, n1);
     const int first_masked = limit(jb.r0) / kTile;
     const int span = nqk + nv;  // ring slots per key tile: K's, then V's
-    auto slot_of = [&](int use) { return use % p.slots; };
-    auto full_parity = [&](int use) { return static_cast<uint32_t>(use / p.slots) & 1u; };
+    auto phase_of = [&](int j) { return static_cast<uint32_t>(j / kAhead) & 1u; };  // of key tile j's barriers
     const volatile int* abort_flag = &sh->abort_flag;
     bool ok = true;
 
@@ -237,9 +244,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ts = tmem + lanes + kColS + t * kTile, to = tmem + lanes + kColO + t * kTile;
         const int row = jb.r0 + t * kTile + r;                    // of the sequence
         const int64_t at = (static_cast<int64_t>(jb.q0) + row) * p.H + h;  // of out and lse
-        const bool mine = r < rows[t];
+        const int rows = rows_of(t), n = t ? n1 : n0;
+        const bool mine = r < rows;
         float c = p.scale * kLog2e;
-        if (p.q8 && n[t]) {
+        if (p.q8 && n) {
             const float qs = mine ? p.q_scale[p.q_per_head ? at : jb.q0 + row] : 0.f;
             c *= fabsf(qs);  // a negative scale turns the codes' sign, so that c > 0 keeps the order of the scores
             if (c < 1e-30f) c = 1e-30f;  // a zero row: its scores are 0 (hidden ones stay -inf)
@@ -266,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lim = mine ? limit(row) : jb.nk;
         const int lim0 = limit(jb.r0 + t * kTile);  // of the tile's first row, which sees the fewest
         float m = -INFINITY, ms = 0.f, l = 0.f;     // row maximum of S, ms = m c, row sum of P
-        for (int j = 0; j < n[t]; ++j) {
+        for (int j = 0; j < n; ++j) {
             ok = mbar_wait(smem_u32(&sh->s_full[t]), j & 1, kTimeoutNs, abort_flag);
             if (!__all_sync(~0u, ok)) {
                 ok = false;
@@ -340,14 +348,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             l += a0 + a1;
             if (masked) {
                 const int use = j * span + nqk;
-                for (int cidx = 0; cidx < nv; ++cidx)
-                    ok &= mbar_wait(smem_u32(&sh->full[slot_of(use + cidx)]), full_parity(use + cidx), kTimeoutNs, abort_flag);
+                ok = mbar_wait(smem_u32(&sh->v_full[j % kAhead]), phase_of(j), kTimeoutNs, abort_flag);
                 if (!__all_sync(~0u, ok)) {
                     ok = false;
                     break;
                 }
                 for (int cidx = 0; cidx < nv; ++cidx)
-                    clean_v(sm_ring + slot_of(use + cidx) * kSlotBytes, 1, r, j * kTile + r < jb.nk,
+                    clean_v(sm_ring + (use + cidx) % p.slots * kSlotBytes, 1, r, j * kTile + r < jb.nk,
                             sh->bad + (j - first_masked) * 4);
                 fence_proxy_async_shared();
             }
@@ -355,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             mbar_arrive(smem_u32(&sh->p_full[t]));
         }
-        if (ok && rows[t]) {
-            if (n[t]) {
-                ok = mbar_wait(smem_u32(&sh->o_done[t]), (n[t] - 1) & 1, kTimeoutNs, abort_flag);
+        if (ok && rows) {
+            if (n) {
+                ok = mbar_wait(smem_u32(&sh->o_done[t]), (n - 1) & 1, kTimeoutNs, abort_flag);
                 ok = __all_sync(~0u, ok);
                 tc_fence_after();
             }
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int d = 0; d < p.Dv; d += 16) {
                     float o[16];
-                    if (n[t]) tmem_ld16(to + d, o);
+                    if (n) tmem_ld16(to + d, o);
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
                     if (any_bad) {
@@ -404,78 +411,93 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             const uint32_t idesc_s = idesc_bf16_f32(kTile, kTile);
             const uint32_t idesc_o = idesc_bf16_f32(kTile, p.Dv) | kIdescBMnMajor;
-            constexpr uint64_t kSlotStep = kSlotBytes >> 4;
+            constexpr uint32_t kSlotStep = kSlotBytes >> 4;
             const uint64_t dq = smem_desc_sw128(sm_q), dk = smem_desc_sw128(sm_ring);
             const uint64_t dv = smem_desc_sw128_mn(sm_ring, kSlotBytes);
-            const uint32_t full0 = smem_u32(&sh->full[0]), empty0 = smem_u32(&sh->empty[0]);
-            // a place in the ring: slot, and the parity of its current use
-            struct Place {
-                int slot;
-                uint32_t parity;
-            };
-            auto after = [&](Place x, int n) {
-                x.slot += n;
-                if (x.slot >= p.slots) x.slot -= p.slots, x.parity ^= 1u;
+            const int ksteps = p.Dqk / 16;
+            // slots of the key tile at hand: the descriptors of K's chunks, and V's first slot
+            int at = 0;
+            uint64_t kd[4];
+            auto take = [&](int count) {
+                const int x = at;
+                at += count;
+                if (at >= p.slots) at -= p.slots;
                 return x;
             };
-            auto scores = [&](int t, Place at, bool last) {
-                const uint64_t a0 = dq + t * nqk * kSlotStep;
-                const uint32_t d = tmem + kColS + t * kTile;
-                for (int cidx = 0; cidx < nqk; ++cidx) {
-                    const Place x = after(at, cidx);
-                    ok = mbar_wait(full0 + 8 * x.slot, x.parity, kTimeoutNs, abort_flag);
-                    if (!ok) return;
-                    tc_fence_after();
-                    const uint64_t a = a0 + cidx * kSlotStep, b = dk + x.slot * kSlotStep;
-                    const int ks = min(4, p.Dqk / 16 - cidx * 4);
-                    mma_bf16(d, a, b, idesc_s, cidx > 0);
-                    if (ks == 4) {
+            auto take_k = [&]() {
+                int x = take(nqk);
 #pragma unroll
-                        for (int k = 1; k < 4; ++k) mma_bf16(d, a + 2 * k, b + 2 * k, idesc_s, 1);
-                    } else {
-                        for (int k = 1; k < ks; ++k) mma_bf16(d, a + 2 * k, b + 2 * k, idesc_s, 1);
-                    }
+                for (int c = 0; c < 4; ++c) {
+                    kd[c] = dk + x * kSlotStep;
+                    if (++x == p.slots) x = 0;
                 }
-                mma_commit(smem_u32(&sh->s_full[t]));
-                if (last)
-                    for (int cidx = 0; cidx < nqk; ++cidx) mma_commit(empty0 + 8 * after(at, cidx).slot);
             };
-            Place kp{0, 0}, vp{0, 0};
-            for (int t = 0; t < 2 && ok; ++t)
-                if (n[t]) {
-                    ok = mbar_wait(smem_u32(&sh->q_full[t]), 0, kTimeoutNs, abort_flag);
-                    tc_fence_after();
-                    if (ok) scores(t, kp, t == 1 || n[1] == 0);
-                }
-            for (int j = 0; j < nmax && ok; ++j) {
-                vp = after(kp, nqk);
-                kp = after(vp, nv);
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (j >= n[t]) continue;
-                    for (int cidx = 0; cidx < nv && ok; ++cidx) {
-                        const Place x = after(vp, cidx);
-                        ok = mbar_wait(full0 + 8 * x.slot, x.parity, kTimeoutNs, abort_flag);
-                    }
-                    if (ok) ok = mbar_wait(smem_u32(&sh->p_full[t]), j & 1, kTimeoutNs, abort_flag);
-                    tc_fence_after();
-                    if (!ok) break;
-                    const uint32_t o = tmem + kColO + t * kTile, pr = tmem + kColS + t * kTile;
-                    // one product over V's two slots where they are neighbours, two of 64 columns where the ring wraps
-                    const bool whole = nv == 1 || vp.slot + 1 < p.slots;
-                    for (int cidx = 0; cidx < (whole ? 1 : nv); ++cidx) {
-                        const uint64_t b = dv + after(vp, cidx).slot * kSlotStep;
-                        const uint32_t cols = whole ? p.Dv : min(64, p.Dv - cidx * 64);
-                        const uint32_t idesc = (idesc_o & ~(0x3Fu << 17)) | (cols >> 3) << 17;
-                        mma_bf16_ts(o + cidx * 64, pr, b, idesc, j > 0);
+            auto scores = [&](int t, int j, bool last) {
+                const uint64_t a = dq + t * nqk * kSlotStep;
+                const uint32_t d = tmem + kColS + t * kTile;
+                auto run = [&](auto steps) {
 #pragma unroll
-                        for (int k = 1; k < kTile / 16; ++k)
-                            mma_bf16_ts(o + cidx * 64, pr + k * 8, b + k * (2048 >> 4), idesc, 1);
+                    for (int k = 0; k < decltype(steps)::value; ++k)
+                        mma_bf16(d, a + (k >> 2) * kSlotStep + 2 * (k & 3), kd[k >> 2] + 2 * (k & 3), idesc_s, k > 0);
+                };
+                if (ksteps == 12) run(Steps<12>());
+                else if (ksteps == 8) run(Steps<8>());
+                else if (ksteps == 4) run(Steps<4>());
+                else
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        for (int k = 0; k < 4 && c * 4 + k < ksteps; ++k)
+                            mma_bf16(d, a + c * kSlotStep + 2 * k, kd[c] + 2 * k, idesc_s, c > 0 || k > 0);
+                mma_commit(smem_u32(&sh->s_full[t]));
+                if (last) mma_commit(smem_u32(&sh->k_free[j % kAhead]));
+            };
+            auto values = [&](int t, int j, int slot, bool last) {
+                const uint32_t o = tmem + kColO + t * kTile, pr = tmem + kColS + t * kTile;
+                const uint64_t b = dv + slot * kSlotStep;
+                // one product over V's two slots where they are neighbours, two of 64 columns where the ring wraps
+                if (nv == 1 || slot + 1 < p.slots) {
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_bf16_ts(o, pr + k * 8, b + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
+                } else {
+                    const uint32_t id0 = (idesc_o & ~(0x3Fu << 17)) | 8u << 17;
+                    const uint32_t id1 = (idesc_o & ~(0x3Fu << 17)) | static_cast<uint32_t>((p.Dv - 64) >> 3) << 17;
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k) {
+                        mma_bf16_ts(o, pr + k * 8, b + k * (2048 >> 4), id0, j > 0 || k > 0);
+                        mma_bf16_ts(o + 64, pr + k * 8, dv + k * (2048 >> 4), id1, j > 0 || k > 0);
                     }
-                    mma_commit(smem_u32(&sh->o_done[t]));
-                    const bool last = t == 1 || j >= n[1];
-                    if (last)
-                        for (int cidx = 0; cidx < nv; ++cidx) mma_commit(empty0 + 8 * after(vp, cidx).slot);
-                    if (j + 1 < n[t]) scores(t, kp, t == 1 || j + 1 >= n[1]);
+                }
+                mma_commit(smem_u32(&sh->o_done[t]));
+                if (last) mma_commit(smem_u32(&sh->v_free[j % kAhead]));
+            };
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && mbar_wait(smem_u32(bar), parity, kTimeoutNs, abort_flag);
+                tc_fence_after();
+                return ok;
+            };
+            take_k();
+            if (n0 && wait(&sh->q_full[0], 0) && wait(&sh->k_full[0], 0)) scores(0, 0, n1 == 0);
+            if (n1 && wait(&sh->q_full[1], 0) && wait(&sh->k_full[0], 0)) scores(1, 0, true);
+            for (int j = 0; j < nmax && ok; ++j) {
+                const int v = take(nv);
+                take_k();
+                if (!wait(&sh->v_full[j % kAhead], phase_of(j))) break;
+                if (j < n0) {
+                    if (!wait(&sh->p_full[0], j & 1)) break;
+                    values(0, j, v, j >= n1);
+                    if (j + 1 < n0) {
+                        if (!wait(&sh->k_full[(j + 1) % kAhead], phase_of(j + 1))) break;
+                        scores(0, j + 1, j + 1 >= n1);
+                    }
+                }
+                if (j < n1) {
+                    if (!wait(&sh->p_full[1], j & 1)) break;
+                    values(1, j, v, true);
+                    if (j + 1 < n1) {
+                        if (!wait(&sh->k_full[(j + 1) % kAhead], phase_of(j + 1))) break;
+                        scores(1, j + 1, true);
+                    }
                 }
             }
             if (!ok) {  // no MMA may still run when the CTA leaves
@@ -485,33 +507,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (lane == 0) {
         // --------------------------------------------------------------- TMA
-        int use = 0, q_loaded = 0;
+        // Tiles go out in the order of their use (K 0, V 0, K 1, ...), each as soon as the ring has room for it.
+        int slot = 0, room = p.slots, q_loaded = 0, sent = 0, freed = 0;  // sent, freed: tiles 2 j (K) and 2 j + 1 (V)
         auto load_q = [&](int t) {
-            if (p.q8 || !n[t]) return;
+            if (p.q8 || !(t ? n1 : n0)) return;
             mbar_arrive_expect_tx(smem_u32(&sh->q_full[t]), nqk * kSlotBytes);
-            for (int cidx = 0; cidx < nqk; ++cidx)
-                tma_load_3d(sm_q + (t * nqk + cidx) * kSlotBytes, &tm_q, smem_u32(&sh->q_full[t]), cidx * 64, h,
+            for (int c = 0; c < nqk; ++c)
+                tma_load_3d(sm_q + (t * nqk + c) * kSlotBytes, &tm_q, smem_u32(&sh->q_full[t]), c * 64, h,
                             jb.q0 + jb.r0 + t * kTile);
             q_loaded |= 1 << t;
         };
-        auto load = [&](const CUtensorMap* map, int chunks, int j) {
-            for (int cidx = 0; cidx < chunks && ok; ++cidx, ++use) {
-                const int s = slot_of(use);
-                ok = mbar_wait(smem_u32(&sh->empty[s]), full_parity(use) ^ 1u, kTimeoutNs, abort_flag);
-                if (!ok) return;
-                mbar_arrive_expect_tx(smem_u32(&sh->full[s]), kSlotBytes);
-                tma_load_3d(sm_ring + s * kSlotBytes, map, smem_u32(&sh->full[s]), cidx * 64, hk, jb.k0 + j * kTile);
+        auto load = [&](const CUtensorMap* map, uint64_t* full, int chunks, int j) {
+            while (ok && (room < chunks || freed < sent - 2 * kAhead + 1)) {
+                const int f = freed >> 1;
+                ok = mbar_wait(smem_u32(freed & 1 ? &sh->v_free[f % kAhead] : &sh->k_free[f % kAhead]), phase_of(f),
+                               kTimeoutNs, abort_flag);
+                room += freed & 1 ? nv : nqk;
+                ++freed;
+            }
+            if (!ok) return;
+            room -= chunks;
+            ++sent;
+            mbar_arrive_expect_tx(smem_u32(&full[j % kAhead]), chunks * kSlotBytes);
+            for (int c = 0; c < chunks; ++c) {
+                tma_load_3d(sm_ring + slot * kSlotBytes, map, smem_u32(&full[j % kAhead]), c * 64, hk, jb.k0 + j * kTile);
+                if (++slot == p.slots) slot = 0;
             }
         };
         load_q(0);
         for (int j = 0; j < nmax && ok; ++j) {
-            load(&tm_k, nqk, j);
+            load(&tm_k, sh->k_full, nqk, j);
             if (j == 0) load_q(1);
-            load(&tm_v, nv, j);
+            load(&tm_v, sh->v_full, nv, j);
         }
         // no copy may still be landing when the CTA leaves
-        for (int u = use > p.slots ? use - p.slots : 0; u < use; ++u)
-            mbar_wait(smem_u32(&sh->full[slot_of(u)]), full_parity(u), kTimeoutNs, nullptr);
+        for (int u = max(sent - 2 * kAhead, 0); u < sent; ++u)
+            mbar_wait(smem_u32(u & 1 ? &sh->v_full[(u >> 1) % kAhead] : &sh->k_full[(u >> 1) % kAhead]), phase_of(u >> 1),
+                      kTimeoutNs, nullptr);
         for (int t = 0; t < 2; ++t)
             if (q_loaded >> t & 1) mbar_wait(smem_u32(&sh->q_full[t]), 0, kTimeoutNs, nullptr);
     }
