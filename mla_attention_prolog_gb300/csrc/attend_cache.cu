@@ -180,6 +180,11 @@ struct Walk {
     }
 };
 
+template <int N>
+struct Number {
+    static constexpr int value = N;
+};
+
 struct Shared {
     uint64_t full[2][kMaxGroups], empty[2][kMaxGroups];  // per stage and group of chunks
     uint64_t q_full, s_full, s_free, p_full, pv_done, drain;
@@ -502,40 +507,53 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
             const uint32_t idesc_o = idesc_bf16_f32(kRows, dv) | kIdescBMnMajor;
-            constexpr uint64_t kSlotStep = kSlotBytes >> 4;
+            constexpr uint32_t kSlotStep = kSlotBytes >> 4;
             const uint64_t dq = smem_desc_sw128(sm_q), dk = smem_desc_sw128(sm_ring);
             const uint64_t dp = smem_desc_sw128(sm_p), dvals = smem_desc_sw128_mn(sm_ring, kSlotBytes);
             const uint32_t d = tmem + kColS;
+            // S (+)= Q K^T over the chunks of group g, from ring stage `stage`
+            auto group_mma = [&](int g, int nc, uint64_t stage, bool first) {
+                for (int k = 0; k < nc; ++k) {
+                    const int ck = g * kGroup + k;
+                    const uint64_t b = stage + ck * kSlotStep;
+                    const int ks = min(4, p.C / 16 - ck * 4);
+                    if (ck < kTmemChunks) {
+                        for (int e = 0; e < ks; ++e)
+                            mma_bf16_ts(d, tmem + kColQ + ck * 32 + e * 8, b + 2 * e, idesc_s, !(first && k == 0 && e == 0));
+                    } else {
+                        const uint64_t a = dq + (ck - kTmemChunks) * (kQBytes >> 4);
+                        for (int e = 0; e < ks; ++e) mma_bf16(d, a + 2 * e, b + 2 * e, idesc_s, !(first && k == 0 && e == 0));
+                    }
+                }
+            };
+            // the same for a whole group of the widest rows, unrolled
+            auto whole_mma = [&](auto group, auto count, uint64_t stage, bool first) {
+#pragma unroll
+                for (int k = 0; k < decltype(count)::value * 4; ++k) {
+                    constexpr int kChunk0 = decltype(group)::value * kGroup;
+                    const int ck = kChunk0 + (k >> 2);
+                    const uint64_t b = stage + ck * kSlotStep + 2 * (k & 3);
+                    if (ck < kTmemChunks)
+                        mma_bf16_ts(d, tmem + kColQ + ck * 32 + (k & 3) * 8, b, idesc_s, k > 0 || !first);
+                    else
+                        mma_bf16(d, dq + (ck - kTmemChunks) * (kQBytes >> 4) + 2 * (k & 3), b, idesc_s, k > 0 || !first);
+                }
+            };
+            const bool widest = p.C == 64 * kMaxChunks;
             auto scores = [&](int st) {
                 if (st > 0) ok = wait(&sh->s_free, st - 1);
+                const uint64_t stage = dk + (st & 1) * chunks * kSlotStep;
                 for (int i = 0; i < groups && ok; ++i) {
-                    const int g = group_at(i), nc = group_chunks(g);
+                    const int g = group_at(i);
                     ok = wait(&sh->full[st & 1][g], st >> 1);
                     if (!ok) return;
                     tc_fence_after();
-                    for (int k = 0; k < nc; ++k) {
-                        const int ck = g * kGroup + k;
-                        const uint64_t b = dk + ((st & 1) * chunks + ck) * kSlotStep;
-                        const int ks = min(4, p.C / 16 - ck * 4);
-                        if (ck < kTmemChunks) {
-                            const uint32_t a = tmem + kColQ + ck * 32;
-                            mma_bf16_ts(d, a, b, idesc_s, i > 0 || k > 0);
-                            if (ks == 4) {
-#pragma unroll
-                                for (int e = 1; e < 4; ++e) mma_bf16_ts(d, a + e * 8, b + 2 * e, idesc_s, 1);
-                            } else {
-                                for (int e = 1; e < ks; ++e) mma_bf16_ts(d, a + e * 8, b + 2 * e, idesc_s, 1);
-                            }
-                        } else {
-                            const uint64_t a = dq + (ck - kTmemChunks) * (kQBytes >> 4);
-                            mma_bf16(d, a, b, idesc_s, i > 0 || k > 0);
-                            if (ks == 4) {
-#pragma unroll
-                                for (int e = 1; e < 4; ++e) mma_bf16(d, a + 2 * e, b + 2 * e, idesc_s, 1);
-                            } else {
-                                for (int e = 1; e < ks; ++e) mma_bf16(d, a + 2 * e, b + 2 * e, idesc_s, 1);
-                            }
-                        }
+                    if (widest) {
+                        if (g == 0) whole_mma(Number<0>(), Number<4>(), stage, i == 0);
+                        else if (g == 1) whole_mma(Number<1>(), Number<4>(), stage, i == 0);
+                        else whole_mma(Number<2>(), Number<1>(), stage, i == 0);
+                    } else {
+                        group_mma(g, group_chunks(g), stage, i == 0);
                     }
                     if (g != half) mma_commit(smem_u32(&sh->empty[st & 1][g]));
                 }
