@@ -46,7 +46,7 @@ constexpr uint32_t kColO = 0, kColQ = 256, kColS = 448;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;             // log2 of the largest P
-constexpr int kOverhead = 4;              // a tile's start and end, in key steps
+constexpr int kOverhead = 7;              // a tile's start and end, in key steps
 constexpr int kMinRun = 8;                // shortest run worth a CTA pair, in key steps
 
 // What the join kernel needs to know of the cut (start of the workspace).
@@ -131,7 +131,8 @@ struct Walk {
         if (b < p.B) len = batch_len(p, b, &row, &bits);
     }
 
-    __device__ __forceinline__ bool next(const CacheParams& p, Piece* x) {
+    // (Out of line: one copy for the three roles keeps their loops in the instruction cache.)
+    __device__ __noinline__ bool next(const CacheParams& p, Piece* x) {
         while (at < end) {
             int64_t tile_base, tile_row;
             int steps;
@@ -180,16 +181,11 @@ struct Walk {
     }
 };
 
-template <int N>
-struct Number {
-    static constexpr int value = N;
-};
-
 struct Shared {
     uint64_t full[2][kMaxGroups], empty[2][kMaxGroups];  // per stage and group of chunks
     uint64_t q_full, s_full, s_free, p_full, pv_done, drain;
     uint32_t tmem;
-    int abort_flag, loaded;
+    int abort_flag;
     int64_t scan[kThreads / 32];
     int64_t total, first_base;
     int first_b, sharers, source, shared;
@@ -313,6 +309,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int dv0 = half * kHalf, dv = min(kHalf, p.Lkv - dv0);
     const int nvc = (dv + 63) / 64, groups = (chunks + kGroup - 1) / kGroup;
     auto group_at = [&](int i) { return i == groups - 1 ? half : (i < half ? i : i + 1); };
+    // Place of a chunk of Q: 0-5 in TMEM, this CTA's value chunks first, 6-8 in shared memory.
+    auto q_place = [&](int ck) { return ck >= 2 * kGroup ? ck : (ck ^ (half * kGroup)); };
     auto group_chunks = [&](int g) { return min(kGroup, chunks - g * kGroup); };
 
     Walk walk;
@@ -330,7 +328,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh->pv_done), 1);
         mbar_init(smem_u32(&sh->drain), 1);
         sh->abort_flag = 0;
-        sh->loaded = 0;
         fence_barrier_init();
     }
     if (warp == kMmaWarp) {
@@ -343,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tmem = sh->tmem;
     const volatile int* abort_flag = &sh->abort_flag;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
-        return mbar_wait(smem_u32(bar), parity & 1u, kTimeoutNs, abort_flag);
+        return mbar_wait_lean(smem_u32(bar), parity & 1u, kTimeoutNs, abort_flag);
     };
     bool ok = true;
     int step = 0;  // key steps so far, over all pieces: the phase of every barrier
@@ -356,24 +353,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c = p.scale * kLog2e;
         while (ok && walk.next(p, &x)) {
             const bool mine = r < x.rows;
-            // Q: chunks 0-5 to TMEM, the rest to shared memory in the swizzled layout of a TMA box
-            const uint4* q = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(x.row0) + r) * p.C);
-            for (int k = 0; k < chunks; ++k) {
-                uint4 w[8];
+            // Q: places 0-5 to TMEM, by way of the warp's rows of the shared-memory places 6-8, and those then to
+            // shared memory in the swizzled layout of a TMA box.  A warp reads four rows of 128 bytes at a time.
+            const uint4* q = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(x.row0) + warp * 32) * p.C);
+            const int pitch = p.C / 8, wrows = x.rows - warp * 32;
+#pragma unroll 1
+            for (int place0 = 0; place0 < kMaxChunks; place0 += 3) {
+                uint4 w[24];
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    w[i] = mine && k * 64 + i * 8 < p.C ? q[k * 8 + i] : make_uint4(0, 0, 0, 0);
-                if (k < kTmemChunks) {
-                    uint32_t y[32];
+                for (int e = 0; e < 3; ++e) {
+                    const int ck = q_place(place0 + e);  // its own inverse
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        y[4 * i] = w[i].x, y[4 * i + 1] = w[i].y, y[4 * i + 2] = w[i].z, y[4 * i + 3] = w[i].w;
-                    tmem_st32_raw(tmem + lanes + kColQ + k * 32, y);
-                } else {
-                    const uint32_t dst = sm_q + (k - kTmemChunks) * kQBytes + r * 128;
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = i * 4 + (lane >> 3), col = ck * 8 + (lane & 7);
+                        w[8 * e + i] = row < wrows && col < pitch ? q[row * pitch + col] : make_uint4(0, 0, 0, 0);
+                    }
+                }
+                const uint32_t base = sm_q + warp * 32 * 128;
+                __syncwarp();  // the round before has been read
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        st_shared_v4(dst + ((i ^ (r & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
+                for (int e = 0; e < 3; ++e)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row = i * 4 + (lane >> 3);
+                        st_shared_v4(base + e * kQBytes + row * 128 + (((lane & 7) ^ (row & 7)) << 4), w[8 * e + i].x,
+                                     w[8 * e + i].y, w[8 * e + i].z, w[8 * e + i].w);
+                    }
+                if (place0 < kTmemChunks) {
+                    __syncwarp();
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) {
+                        uint32_t y[32];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            ld_shared_v4(base + e * kQBytes + lane * 128 + ((i ^ (lane & 7)) << 4), y[4 * i], y[4 * i + 1],
+                                         y[4 * i + 2], y[4 * i + 3]);
+                        tmem_st32_raw(tmem + lanes + kColQ + (place0 + e) * 32, y);
+                    }
                 }
             }
             tmem_wait_st();
@@ -474,25 +490,55 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int len = batch_len(p, b, &trow, &bits);
                 direct = x.prefix ? len == walk.shared : len < walk.shared;
             }
+            // A warp's rows pass through its part of P's buffer, 128 bytes of each at a time, so that it stores
+            // four rows' whole lines at once: 64 columns of finished rows, 32 of partial ones.
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t at = static_cast<int64_t>(x.row0) + r;
+            const uint32_t direct_rows = __ballot_sync(~0u, direct && mine), part_rows = __ballot_sync(~0u, !direct && mine);
+            const uint32_t stage = sm_p + warp * 32 * 128;
+            auto put = [&](int i, uint32_t a, uint32_t b, uint32_t c2, uint32_t d2) {
+                st_shared_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), a, b, c2, d2);
+            };
+            auto flush = [&](uint8_t* rows, int64_t row_bytes, uint32_t which, int bytes) {
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row = i * 4 + (lane >> 3), col = (lane & 7) * 16;
+                    uint4 v;
+                    ld_shared_v4(stage + row * 128 + (((lane & 7) ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
+                    if ((which >> row & 1u) && col < bytes) *reinterpret_cast<uint4*>(rows + row * row_bytes + col) = v;
+                }
+                __syncwarp();
+            };
+            uint8_t* out = reinterpret_cast<uint8_t*>(p.out + (static_cast<int64_t>(x.row0) + warp * 32) * p.Lkv + dv0);
+            uint8_t* part = reinterpret_cast<uint8_t*>(p.part_o + (x.part + warp * 32) * p.Lkv + dv0);
 #pragma unroll 1
-            for (int d = 0; d < dv; d += 16) {
-                float o[16];
-                tmem_ld16(tmem + lanes + kColO + d, o);
-                if (!mine) continue;
+            for (int d = 0; d < dv; d += 64) {
+                uint32_t o[64];  // (what lies behind dv is not stored)
+                tmem_ld64_raw(tmem + lanes + kColO + d, o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
-                if (direct) {
-                    uint4* dst = reinterpret_cast<uint4*>(p.out + at * p.Lkv + dv0 + d);
-                    dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                        pack_bf16x2(o[6], o[7]));
-                    dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]), pack_bf16x2(o[12], o[13]),
-                                        pack_bf16x2(o[14], o[15]));
-                } else {
-                    float4* dst = reinterpret_cast<float4*>(p.part_o + (x.part + r) * p.Lkv + dv0 + d);
+                for (int i = 0; i < 64; ++i) o[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+                const int left = dv - d;
+                if (part_rows) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    for (int k = 0; k < 2; ++k) {
+                        if (k * 32 >= left) break;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            put(i, o[k * 32 + 4 * i], o[k * 32 + 4 * i + 1], o[k * 32 + 4 * i + 2], o[k * 32 + 4 * i + 3]);
+                        flush(part + (d + k * 32) * 4, p.Lkv * 4, part_rows, (left - k * 32) * 4);
+                    }
+                }
+                if (direct_rows) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
+                        put(i, w[0], w[1], w[2], w[3]);
+                    }
+                    flush(out + d * 2, p.Lkv * 2, direct_rows, left * 2);
                 }
             }
             if (mine && half == 0) {
@@ -507,75 +553,102 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (elect_one()) {
             const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
             const uint32_t idesc_o = idesc_bf16_f32(kRows, dv) | kIdescBMnMajor;
-            constexpr uint32_t kSlotStep = kSlotBytes >> 4;
-            const uint64_t dq = smem_desc_sw128(sm_q), dk = smem_desc_sw128(sm_ring);
-            const uint64_t dp = smem_desc_sw128(sm_p), dvals = smem_desc_sw128_mn(sm_ring, kSlotBytes);
-            const uint32_t d = tmem + kColS;
-            // S (+)= Q K^T over the chunks of group g, from ring stage `stage`
-            auto group_mma = [&](int g, int nc, uint64_t stage, bool first) {
-                for (int k = 0; k < nc; ++k) {
-                    const int ck = g * kGroup + k;
-                    const uint64_t b = stage + ck * kSlotStep;
-                    const int ks = min(4, p.C / 16 - ck * 4);
-                    if (ck < kTmemChunks) {
-                        for (int e = 0; e < ks; ++e)
-                            mma_bf16_ts(d, tmem + kColQ + ck * 32 + e * 8, b + 2 * e, idesc_s, !(first && k == 0 && e == 0));
-                    } else {
-                        const uint64_t a = dq + (ck - kTmemChunks) * (kQBytes >> 4);
-                        for (int e = 0; e < ks; ++e) mma_bf16(d, a + 2 * e, b + 2 * e, idesc_s, !(first && k == 0 && e == 0));
-                    }
-                }
-            };
-            // the same for a whole group of the widest rows, unrolled
-            auto whole_mma = [&](auto group, auto count, uint64_t stage, bool first) {
-#pragma unroll
-                for (int k = 0; k < decltype(count)::value * 4; ++k) {
-                    constexpr int kChunk0 = decltype(group)::value * kGroup;
-                    const int ck = kChunk0 + (k >> 2);
-                    const uint64_t b = stage + ck * kSlotStep + 2 * (k & 3);
-                    if (ck < kTmemChunks)
-                        mma_bf16_ts(d, tmem + kColQ + ck * 32 + (k & 3) * 8, b, idesc_s, k > 0 || !first);
-                    else
-                        mma_bf16(d, dq + (ck - kTmemChunks) * (kQBytes >> 4) + 2 * (k & 3), b, idesc_s, k > 0 || !first);
-                }
-            };
+            constexpr uint32_t kSlotStep = kSlotBytes >> 4, kQStep = kQBytes >> 4;
+            const uint32_t full0 = smem_u32(&sh->full[0][0]), empty0 = smem_u32(&sh->empty[0][0]);
+            const uint64_t dq = smem_desc_sw128(sm_q), dp = smem_desc_sw128(sm_p);
+            const uint32_t tq = tmem + kColQ, ts = tmem + kColS, to = tmem + kColO;
             const bool widest = p.C == 64 * kMaxChunks;
-            auto scores = [&](int st) {
-                if (st > 0) ok = wait(&sh->s_free, st - 1);
-                const uint64_t stage = dk + (st & 1) * chunks * kSlotStep;
-                for (int i = 0; i < groups && ok; ++i) {
-                    const int g = group_at(i);
-                    ok = wait(&sh->full[st & 1][g], st >> 1);
-                    if (!ok) return;
-                    tc_fence_after();
-                    if (widest) {
-                        if (g == 0) whole_mma(Number<0>(), Number<4>(), stage, i == 0);
-                        else if (g == 1) whole_mma(Number<1>(), Number<4>(), stage, i == 0);
-                        else whole_mma(Number<2>(), Number<1>(), stage, i == 0);
-                    } else {
-                        group_mma(g, group_chunks(g), stage, i == 0);
-                    }
-                    if (g != half) mma_commit(smem_u32(&sh->empty[st & 1][g]));
-                }
-                mma_commit(smem_u32(&sh->s_full));
+            auto wait_group = [&](int g, int st) {
+                ok = ok && mbar_wait_lean(full0 + 8 * ((st & 1) * kMaxGroups + g), (st >> 1) & 1, kTimeoutNs, abort_flag);
+                tc_fence_after();
             };
-            for (int piece = 0; ok && walk.next(p, &x); ++piece) {
+            auto free_group = [&](int g, int st) { mma_commit(empty0 + 8 * ((st & 1) * kMaxGroups + g)); };
+            // S (+)= Q K^T over the chunks of one group of any width
+            auto group_mma = [&](int g, uint64_t stage, bool first) {
+                const int nc = group_chunks(g);
+    #pragma unroll 1
+                for (int k = 0; k < nc; ++k) {
+                    const int ck = g * kGroup + k, place = q_place(ck), ks = min(4, p.C / 16 - ck * 4);
+                    const uint64_t b = stage + ck * kSlotStep;
+    #pragma unroll 1
+                    for (int e = 0; e < ks; ++e) {
+                        const uint32_t acc = !(first && k == 0 && e == 0);
+                        if (place < kTmemChunks) mma_bf16_ts(ts, tq + place * 32 + e * 8, b + 2 * e, idesc_s, acc);
+                        else mma_bf16(ts, dq + (place - kTmemChunks) * kQStep + 2 * e, b + 2 * e, idesc_s, acc);
+                    }
+                }
+            };
+            for (int piece = 0; walk.next(p, &x); ++piece) {
+                const int n = x.n;
                 ok = wait(&sh->q_full, piece);
                 tc_fence_after();
-                if (ok) scores(step);
-                for (int j = 0; j < x.n && ok; ++j, ++step) {
-                    if (j + 1 < x.n) scores(step + 1);
-                    if (ok) ok = wait(&sh->p_full, step);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t b = dvals + ((step & 1) * chunks + half * kGroup) * kSlotStep;
-                    mma_bf16(tmem + kColO, dp, b, idesc_o, j > 0);
-#pragma unroll
-                    for (int k = 1; k < kKeys / 16; ++k)
-                        mma_bf16(tmem + kColO, dp + 2 * k, b + k * (2048 >> 4), idesc_o, 1);
-                    mma_commit(smem_u32(&sh->pv_done));
-                    mma_commit(smem_u32(&sh->empty[step & 1][half]));
+                // Per round: the chunks of step t that only S needs; P V of step t - 1, whose softmax ran meanwhile;
+                // step t's value chunks.  In this order a step's value chunks leave the ring a whole step before the
+                // copy that refills their place is waited for.
+    #pragma unroll 1
+                for (int t = 0; t <= n && ok; ++t) {
+                    const int st = step + t;
+                    const uint64_t stage = smem_desc_sw128(sm_ring + (st & 1) * chunks * kSlotBytes);
+                    if (t < n) {
+                        if (st > 0) ok = wait(&sh->s_free, st - 1);
+                        if (widest) {
+                            const int g = half ^ 1;
+                            wait_group(g, st);
+                            if (!ok) break;
+                            const uint64_t b = stage + g * kGroup * kSlotStep, b8 = stage + 2 * kGroup * kSlotStep;
+    #pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                mma_bf16_ts(ts, tq + 128 + k * 8, b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, k > 0);
+    #pragma unroll
+                            for (int k = 8; k < 16; ++k)
+                                mma_bf16(ts, dq + ((k >> 2) - 2) * kQStep + 2 * (k & 3),
+                                            b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, 1);
+                            free_group(g, st);
+                            wait_group(2, st);
+                            if (!ok) break;
+    #pragma unroll
+                            for (int k = 0; k < 4; ++k) mma_bf16(ts, dq + 2 * kQStep + 2 * k, b8 + 2 * k, idesc_s, 1);
+                            free_group(2, st);
+                        } else {
+    #pragma unroll 1
+                            for (int i = 0; i + 1 < groups && ok; ++i) {
+                                const int g = group_at(i);
+                                wait_group(g, st);
+                                if (!ok) break;
+                                group_mma(g, stage, i == 0);
+                                free_group(g, st);
+                            }
+                        }
+                    }
+                    if (t > 0) {
+                        const int pv = st - 1;
+                        ok = ok && wait(&sh->p_full, pv);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t b =
+                            smem_desc_sw128_mn(sm_ring + ((pv & 1) * chunks + half * kGroup) * kSlotBytes, kSlotBytes);
+    #pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            mma_bf16(to, dp + 2 * k, b + k * (2048 >> 4), idesc_o, t > 1 || k > 0);
+                        mma_commit(smem_u32(&sh->pv_done));
+                        free_group(half, pv);
+                    }
+                    if (t < n) {
+                        wait_group(half, st);
+                        if (!ok) break;
+                        if (widest) {
+                            const uint64_t b = stage + half * kGroup * kSlotStep;
+    #pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                mma_bf16_ts(ts, tq + k * 8, b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, 1);
+                        } else {
+                            group_mma(half, stage, groups == 1);
+                        }
+                        mma_commit(smem_u32(&sh->s_full));
+                    }
                 }
+                if (!ok) break;
+                step += n;
             }
             if (!ok) {  // no MMA may still run when the CTA leaves
                 mma_commit(smem_u32(&sh->drain));
@@ -584,58 +657,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         // --------------------------------------------------------------- TMA
-        // The lanes look up the rows of 32 boxes ahead; one thread issues the copies.
-        const int per = kKeys / p.box;  // boxes per step
-        int bits = 0;
+        // The lanes look up the rows of 32 boxes at a time; one thread issues the copies.
+        const int per = kKeys / p.box, batch = 32 / per;  // boxes per step, steps per lookup
+        const bool lead = elect_one();
+        const uint32_t full0 = smem_u32(&sh->full[0][0]), empty0 = smem_u32(&sh->empty[0][0]);
+        const uint32_t box_bytes = p.box * 128;
+        const bool single = per == 1;
+        int bits = 0, loaded = 0;  // loaded: copies' barriers armed, in the order of group_at
         while (ok && walk.next(p, &x)) {
-            const int boxes = x.n * per;
-            int rows = 0;
-            for (int j = 0; j < x.n && ok; ++j) {
-                const int i = j * per;
-                if ((i & 31) == 0) {
-                    const int key = x.key0 + (i + lane) * p.box;
-                    rows = p.num_rows;  // outside the cache: reads as zeros
-                    if (i + lane < boxes && key < x.end) {
-                        const int page = p.table[static_cast<int64_t>(x.page_row) * p.max_pages + key / p.page_size];
-                        if (page >= 0 && page < p.num_pages) rows = page * p.page_size + key % p.page_size;
-                        else bits |= kStatusPageRange;
-                    }
+            const int n = x.n, key0 = x.key0, end = x.end;
+            const int32_t* row_table = p.table + static_cast<int64_t>(x.page_row) * p.max_pages;
+#pragma unroll 1
+            for (int j0 = 0; j0 < n && ok; j0 += batch) {
+                const int key = key0 + (j0 * per + lane) * p.box;
+                int rows = p.num_rows;  // outside the cache: reads as zeros
+                if (key < end) {
+                    const int page = row_table[key / p.page_size];
+                    if (page >= 0 && page < p.num_pages) rows = page * p.page_size + key % p.page_size;
+                    else if (j0 * per + lane < n * per) bits |= kStatusPageRange;
                 }
-                int row[kKeys / 16];
-#pragma unroll
-                for (int k = 0; k < kKeys / 16; ++k) row[k] = __shfl_sync(~0u, rows, (i + k) & 31);
-                if (elect_one()) {
+                const int steps = min(batch, n - j0);
+#pragma unroll 1
+                for (int j = 0; j < steps && ok; ++j, ++step) {
                     const int st = step & 1;
-                    for (int k = 0; k < groups && ok; ++k) {
+                    const uint32_t parity = ((step >> 1) & 1) ^ 1;
+                    const uint32_t ring = sm_ring + st * chunks * kSlotBytes;
+                    const int row0 = __shfl_sync(~0u, rows, j * per);
+#pragma unroll 1
+                    for (int k = 0; k < groups; ++k) {
                         const int g = group_at(k), nc = group_chunks(g);
-                        const uint32_t bar = smem_u32(&sh->full[st][g]);
-                        ok = wait(&sh->empty[st][g], (step >> 1) ^ 1);
+                        const uint32_t bar = full0 + 8 * (st * kMaxGroups + g), dst = ring + g * kGroup * kSlotBytes;
+                        const bool whole = single && (g + 1) * kGroup * 64 <= p.C;
+                        if (lead) {
+                            ok = mbar_wait_lean(empty0 + 8 * (st * kMaxGroups + g), parity, kTimeoutNs, abort_flag);
+                            if (ok) {
+                                mbar_arrive_expect_tx(bar, nc * kSlotBytes);
+                                ++loaded;
+                                if (whole) tma_load_3d(dst, &tm_g, bar, 0, row0, g * kGroup);
+                            }
+                        }
+                        ok = __all_sync(~0u, ok);
                         if (!ok) break;
-                        mbar_arrive_expect_tx(bar, nc * kSlotBytes);
-                        sh->loaded = step * groups + k + 1;
-                        const uint32_t dst = sm_ring + (st * chunks + g * kGroup) * kSlotBytes;
-#pragma unroll
-                        for (int e = 0; e < kKeys / 16; ++e) {
-                            if (e >= per) break;
-                            const uint32_t at = dst + e * p.box * 128;
-                            if (nc == kGroup && (g + 1) * kGroup * 64 <= p.C && p.box == kKeys) {
-                                tma_load_3d(at, &tm_g, bar, 0, row[e], g * kGroup);
-                            } else {
-                                for (int cidx = 0; cidx < nc; ++cidx)
-                                    tma_load_3d(at + cidx * kSlotBytes, &tm_c, bar, (g * kGroup + cidx) * 64, 0, row[e]);
+                        if (!whole) {
+#pragma unroll 1
+                            for (int e = 0; e < per; ++e) {
+                                const int row = __shfl_sync(~0u, rows, j * per + e);
+                                if (lead)
+                                    for (int c = 0; c < nc; ++c)
+                                        tma_load_3d(dst + e * box_bytes + c * kSlotBytes, &tm_c, bar, (g * kGroup + c) * 64, 0, row);
                             }
                         }
                     }
                 }
-                __syncwarp();
-                ok = __all_sync(~0u, ok);
-                ++step;
             }
         }
         // no copy may still be landing when the CTA leaves
-        if (lane == 0)
-            for (int u = max(sh->loaded - 2 * groups, 0); u < sh->loaded; ++u)
-                mbar_wait(smem_u32(&sh->full[u / groups & 1][group_at(u % groups)]), (u / groups >> 1) & 1, kTimeoutNs, nullptr);
+        if (lead)
+            for (int u = max(loaded - 2 * groups, 0); u < loaded; ++u)
+                mbar_wait(full0 + 8 * ((u / groups & 1) * kMaxGroups + group_at(u % groups)), (u / groups >> 1) & 1,
+                          kTimeoutNs, nullptr);
         if (bits) raise_status(p.status, bits);
     }
     if (!ok) {

@@ -220,6 +220,10 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                  : "memory");
 }
 
+__device__ __forceinline__ void ld_shared_v4(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(a), "=r"(b), "=r"(c), "=r"(d) : "r"(addr) : "memory");
+}
+
 // Starts bringing a contiguous byte range into L2 (16-byte aligned address
 // and size): sequential DRAM bursts instead of one 128-byte piece per row.
 __device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes) {
@@ -579,6 +583,17 @@ __device__ __forceinline__ bool elect_one() {
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(r));
     return r != 0;
+}
+
+// mbar_wait() with everything but the first look out of line, for loops whose
+// code has to stay small.
+static __device__ __noinline__ bool mbar_wait_long(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                            const volatile int* abort_flag) {
+    return mbar_wait(bar, parity, timeout_ns, abort_flag);
+}
+__device__ __forceinline__ bool mbar_wait_lean(uint32_t bar, uint32_t parity, uint64_t timeout_ns,
+                                               const volatile int* abort_flag) {
+    return mbar_try_wait(bar, parity) || mbar_wait_long(bar, parity, timeout_ns, abort_flag);
 }
 
 // 3-D tiled bulk tensor load global -> shared (c0 innermost, elements).
