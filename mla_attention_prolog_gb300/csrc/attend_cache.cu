@@ -34,14 +34,18 @@ constexpr int kKeys = 64;                 // keys per step
 constexpr int kSlotBytes = kKeys * 128;   // 64 keys x 64 BF16 columns
 constexpr int kQBytes = kRows * 128;      // 128 rows x 64 BF16 columns
 constexpr int kMaxChunks = 9;             // 64-column chunks of a cache row
-constexpr int kGroup = 4;                 // chunks per TMA copy and barrier (the columns of O of one CTA)
-constexpr int kMaxGroups = 3;
+constexpr int kGroup = 4;                 // value chunks of a CTA (its columns of O)
+constexpr int kOthers = kMaxChunks - kGroup;  // the chunks that only S needs, two steps of them in the ring
+constexpr int kPairs = 5;                 // pairs of value chunks in the ring: two and a half steps
 constexpr int kTmemChunks = 6;            // chunks of Q kept in TMEM
 constexpr int kHalf = 256;                // columns of O per CTA
 constexpr int kThreads = 192;
 constexpr int kMmaWarp = 4, kLoadWarp = 5;
 constexpr int kMiscBytes = 1024;
-constexpr int kSmem = 1024 + kMiscBytes + (kMaxChunks - kTmemChunks) * kQBytes + 2 * kMaxChunks * kSlotBytes + kQBytes;
+constexpr int kSmemQ = (kMaxChunks - kTmemChunks) * kQBytes, kSmemX = 2 * kOthers * kSlotBytes;
+constexpr int kSmemY = 2 * kPairs * kSlotBytes;
+constexpr int kSmem = 1024 + kMiscBytes + kSmemQ + kQBytes + kSmemX + kSmemY;
+static_assert(kSmem <= 232448, "227 KB");
 constexpr uint32_t kColO = 0, kColQ = 256, kColS = 448;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -182,7 +186,7 @@ struct Walk {
 };
 
 struct Shared {
-    uint64_t full[2][kMaxGroups], empty[2][kMaxGroups];  // per stage and group of chunks
+    uint64_t x_full[2], x_empty[2], y_full[kPairs], y_empty[kPairs];  // other chunks by step, value chunks by pair
     uint64_t q_full, s_full, s_free, p_full, pv_done, drain;
     uint32_t tmem;
     int abort_flag;
@@ -293,34 +297,34 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_g,
-                            const CacheParams p) {
+    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_4,
+                            const __grid_constant__ CUtensorMap tm_2, const CacheParams p) {
     extern __shared__ uint8_t raw[];
     const uint32_t raw_at = smem_u32(raw);
     const uint32_t pad = (1024u - (raw_at & 1023u)) & 1023u;
     const int chunks = (p.C + 63) / 64;
-    const uint32_t sm_q = raw_at + pad, sm_p = sm_q + (kMaxChunks - kTmemChunks) * kQBytes, sm_ring = sm_p + kQBytes;
-    Shared* sh = reinterpret_cast<Shared*>(raw + pad + (kMaxChunks - kTmemChunks + 1) * kQBytes +
-                                           2 * kMaxChunks * kSlotBytes);
+    const uint32_t sm_q = raw_at + pad, sm_p = sm_q + kSmemQ, sm_x = sm_p + kQBytes, sm_y = sm_x + kSmemX;
+    Shared* sh = reinterpret_cast<Shared*>(raw + pad + kSmemQ + kQBytes + kSmemX + kSmemY);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int unit = blockIdx.x / p.halves, half = blockIdx.x % p.halves;
-    // This CTA's columns of O lie in the chunks of group `half`, which are
-    // multiplied last and kept until P V has read them.
+    // This CTA's columns of O lie in value chunks 4 half .. + 3 of a cache row; the others only go into S.
     const int dv0 = half * kHalf, dv = min(kHalf, p.Lkv - dv0);
-    const int nvc = (dv + 63) / 64, groups = (chunks + kGroup - 1) / kGroup;
-    auto group_at = [&](int i) { return i == groups - 1 ? half : (i < half ? i : i + 1); };
-    // Place of a chunk of Q: 0-5 in TMEM, this CTA's value chunks first, 6-8 in shared memory.
-    auto q_place = [&](int ck) { return ck >= 2 * kGroup ? ck : (ck ^ (half * kGroup)); };
-    auto group_chunks = [&](int g) { return min(kGroup, chunks - g * kGroup); };
+    const int v0 = half * kGroup, nvc = min(kGroup, chunks - v0), nx = chunks - nvc, pairs = (nvc + 1) / 2;
+    auto other = [&](int i) { return i < v0 ? i : i + nvc; };  // chunk of ring place i
+    // Place of a chunk of Q: 0-5 in TMEM, the value chunks first, 6-8 in shared memory.
+    auto q_place = [&](int ck) { return ck >= 2 * kGroup ? ck : (ck ^ v0); };
 
     Walk walk;
     if (!make_cut(p, unit, sh, &walk)) return;
     if (warp == kLoadWarp && lane == 0) {
-        for (int s = 0; s < 2; ++s)
-            for (int g = 0; g < groups; ++g) {
-                mbar_init(smem_u32(&sh->full[s][g]), 1);
-                mbar_init(smem_u32(&sh->empty[s][g]), 1);
-            }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh->x_full[i]), 1);
+            mbar_init(smem_u32(&sh->x_empty[i]), 1);
+        }
+        for (int i = 0; i < kPairs; ++i) {
+            mbar_init(smem_u32(&sh->y_full[i]), 1);
+            mbar_init(smem_u32(&sh->y_empty[i]), 1);
+        }
         mbar_init(smem_u32(&sh->q_full), kRows);
         mbar_init(smem_u32(&sh->s_full), 1);
         mbar_init(smem_u32(&sh->s_free), kRows);
@@ -351,12 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = threadIdx.x;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
         const float c = p.scale * kLog2e;
-        while (ok && walk.next(p, &x)) {
-            const bool mine = r < x.rows;
+        auto load_q = [&](const Piece& y) {
             // Q: places 0-5 to TMEM, by way of the warp's rows of the shared-memory places 6-8, and those then to
             // shared memory in the swizzled layout of a TMA box.  A warp reads four rows of 128 bytes at a time.
-            const uint4* q = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(x.row0) + warp * 32) * p.C);
-            const int pitch = p.C / 8, wrows = x.rows - warp * 32;
+            const uint4* q = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(y.row0) + warp * 32) * p.C);
+            const int pitch = p.C / 8, wrows = y.rows - warp * 32;
 #pragma unroll 1
             for (int place0 = 0; place0 < kMaxChunks; place0 += 3) {
                 uint4 w[24];
@@ -383,12 +386,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
 #pragma unroll
                     for (int e = 0; e < 3; ++e) {
-                        uint32_t y[32];
+                        uint32_t t[32];
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
-                            ld_shared_v4(base + e * kQBytes + lane * 128 + ((i ^ (lane & 7)) << 4), y[4 * i], y[4 * i + 1],
-                                         y[4 * i + 2], y[4 * i + 3]);
-                        tmem_st32_raw(tmem + lanes + kColQ + (place0 + e) * 32, y);
+                            ld_shared_v4(base + e * kQBytes + lane * 128 + ((i ^ (lane & 7)) << 4), t[4 * i], t[4 * i + 1],
+                                         t[4 * i + 2], t[4 * i + 3]);
+                        tmem_st32_raw(tmem + lanes + kColQ + (place0 + e) * 32, t);
                     }
                 }
             }
@@ -396,8 +399,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_shared();
             tc_fence_before();
             mbar_arrive(smem_u32(&sh->q_full));
+        };
+        bool more = walk.next(p, &x);
+        if (more) load_q(x);
+        while (more && ok) {
+            const Piece now = x;
+            const bool mine = r < now.rows;
             float m = -INFINITY, ms = 0.f, l = 0.f;
-            for (int j = 0; j < x.n; ++j, ++step) {
+            for (int j = 0; j < now.n; ++j, ++step) {
                 ok = __all_sync(~0u, wait(&sh->s_full, step));
                 if (!ok) break;
                 tc_fence_after();
@@ -405,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tmem_ld64_raw(tmem + lanes + kColS, s);
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh->s_free));
-                const int left = x.end - x.key0 - j * kKeys;
+                const int left = now.end - now.key0 - j * kKeys;
                 if (left < kKeys) {
 #pragma unroll
                     for (int i = 0; i < kKeys; ++i)
@@ -468,10 +477,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     st_shared_v4(dst + ((i ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 if (left < kKeys) {
                     // rows behind the end may hold anything: as values they have to be zero
-                    const int st = (step & 1) * chunks + half * kGroup;
                     for (int k = r; k < (kKeys - left) * nvc * 8; k += kRows) {
-                        const int row = left + k / (nvc * 8), in = k % (nvc * 8);
-                        st_shared_v4(sm_ring + (st + in / 8) * kSlotBytes + row * 128 + (in & 7) * 16, 0, 0, 0, 0);
+                        const int row = left + k / (nvc * 8), in = k % (nvc * 8), c2 = in / 8;
+                        const int slot = (step * pairs + c2 / 2) % kPairs * 2 + (c2 & 1);
+                        st_shared_v4(sm_y + slot * kSlotBytes + row * 128 + (in & 7) * 16, 0, 0, 0, 0);
                     }
                 }
                 fence_proxy_async_shared();
@@ -479,21 +488,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive(smem_u32(&sh->p_full));
             }
             if (!ok) break;
+            // every score of this piece is done: the next piece's Q can take Q's place while P V finishes
+            more = walk.next(p, &x);
+            if (more) load_q(x);
             ok = __all_sync(~0u, wait(&sh->pv_done, step - 1));
             if (!ok) break;
             tc_fence_after();
             // A row whose keys this piece covers alone is finished; the others leave a partial result.
-            bool direct = x.whole;
-            const int b = (x.row0 + r) / p.H;
+            bool direct = now.whole;
+            const int b = (now.row0 + r) / p.H;
             if (walk.shared && direct && mine) {
                 int trow, bits = 0;
                 const int len = batch_len(p, b, &trow, &bits);
-                direct = x.prefix ? len == walk.shared : len < walk.shared;
+                direct = now.prefix ? len == walk.shared : len < walk.shared;
             }
             // A warp's rows pass through its part of P's buffer, 128 bytes of each at a time, so that it stores
             // four rows' whole lines at once: 64 columns of finished rows, 32 of partial ones.
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int64_t at = static_cast<int64_t>(x.row0) + r;
+            const int64_t at = static_cast<int64_t>(now.row0) + r;
             const uint32_t direct_rows = __ballot_sync(~0u, direct && mine), part_rows = __ballot_sync(~0u, !direct && mine);
             const uint32_t stage = sm_p + warp * 32 * 128;
             auto put = [&](int i, uint32_t a, uint32_t b, uint32_t c2, uint32_t d2) {
@@ -510,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            uint8_t* out = reinterpret_cast<uint8_t*>(p.out + (static_cast<int64_t>(x.row0) + warp * 32) * p.Lkv + dv0);
-            uint8_t* part = reinterpret_cast<uint8_t*>(p.part_o + (x.part + warp * 32) * p.Lkv + dv0);
+            uint8_t* out = reinterpret_cast<uint8_t*>(p.out + (static_cast<int64_t>(now.row0) + warp * 32) * p.Lkv + dv0);
+            uint8_t* part = reinterpret_cast<uint8_t*>(p.part_o + (now.part + warp * 32) * p.Lkv + dv0);
 #pragma unroll 1
             for (int d = 0; d < dv; d += 64) {
                 uint32_t o[64];  // (what lies behind dv is not stored)
@@ -543,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (mine && half == 0) {
                 const float lg = l == 0.f ? -INFINITY : ms + log2f(l);
-                if (!direct) p.part_lse[x.part + r] = lg;
+                if (!direct) p.part_lse[now.part + r] = lg;
                 else if (p.lse) p.lse[at] = lg * kLn2;
             }
             tc_fence_before();
@@ -552,99 +564,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---------------------------------------------------------------- MMA
         if (elect_one()) {
             const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
-            const uint32_t idesc_o = idesc_bf16_f32(kRows, dv) | kIdescBMnMajor;
+            const uint32_t x_full = smem_u32(&sh->x_full[0]), x_empty = smem_u32(&sh->x_empty[0]);
+            const uint32_t y_full = smem_u32(&sh->y_full[0]), y_empty = smem_u32(&sh->y_empty[0]);
             constexpr uint32_t kSlotStep = kSlotBytes >> 4, kQStep = kQBytes >> 4;
-            const uint32_t full0 = smem_u32(&sh->full[0][0]), empty0 = smem_u32(&sh->empty[0][0]);
             const uint64_t dq = smem_desc_sw128(sm_q), dp = smem_desc_sw128(sm_p);
+            const uint64_t dx = smem_desc_sw128(sm_x), dy = smem_desc_sw128(sm_y);
+            const uint64_t dvals = smem_desc_sw128_mn(sm_y, kSlotBytes);
             const uint32_t tq = tmem + kColQ, ts = tmem + kColS, to = tmem + kColO;
             const bool widest = p.C == 64 * kMaxChunks;
-            auto wait_group = [&](int g, int st) {
-                ok = ok && mbar_wait_lean(full0 + 8 * ((st & 1) * kMaxGroups + g), (st >> 1) & 1, kTimeoutNs, abort_flag);
+            auto look = [&](uint32_t bar, uint32_t parity) {
+                ok = ok && mbar_wait_lean(bar, parity, kTimeoutNs, abort_flag);
                 tc_fence_after();
+                return ok;
             };
-            auto free_group = [&](int g, int st) { mma_commit(empty0 + 8 * ((st & 1) * kMaxGroups + g)); };
-            // S (+)= Q K^T over the chunks of one group of any width
-            auto group_mma = [&](int g, uint64_t stage, bool first) {
-                const int nc = group_chunks(g);
-    #pragma unroll 1
-                for (int k = 0; k < nc; ++k) {
-                    const int ck = g * kGroup + k, place = q_place(ck), ks = min(4, p.C / 16 - ck * 4);
-                    const uint64_t b = stage + ck * kSlotStep;
-    #pragma unroll 1
-                    for (int e = 0; e < ks; ++e) {
-                        const uint32_t acc = !(first && k == 0 && e == 0);
-                        if (place < kTmemChunks) mma_bf16_ts(ts, tq + place * 32 + e * 8, b + 2 * e, idesc_s, acc);
-                        else mma_bf16(ts, dq + (place - kTmemChunks) * kQStep + 2 * e, b + 2 * e, idesc_s, acc);
-                    }
+            // S (+)= Q K^T over one chunk of any width
+            auto chunk_mma = [&](int ck, uint64_t b, bool first) {
+                const int place = q_place(ck), ks = min(4, p.C / 16 - ck * 4);
+#pragma unroll 1
+                for (int e = 0; e < ks; ++e) {
+                    const uint32_t acc = !(first && e == 0);
+                    if (place < kTmemChunks) mma_bf16_ts(ts, tq + place * 32 + e * 8, b + 2 * e, idesc_s, acc);
+                    else mma_bf16(ts, dq + (place - kTmemChunks) * kQStep + 2 * e, b + 2 * e, idesc_s, acc);
                 }
             };
+            int y = 0;  // ring place and parity of the next pair of value chunks
+            uint32_t yp = 0;
+            int at[2] = {0, 0}, was[2] = {0, 0};  // places of this step's and the step before's pairs
+            const uint32_t id[2] = {idesc_bf16_f32(kRows, min(dv, 128)) | kIdescBMnMajor,
+                                    idesc_bf16_f32(kRows, dv > 128 ? dv - 128 : 16) | kIdescBMnMajor};
             for (int piece = 0; walk.next(p, &x); ++piece) {
                 const int n = x.n;
-                ok = wait(&sh->q_full, piece);
-                tc_fence_after();
-                // Per round: the chunks of step t that only S needs; P V of step t - 1, whose softmax ran meanwhile;
-                // step t's value chunks.  In this order a step's value chunks leave the ring a whole step before the
-                // copy that refills their place is waited for.
-    #pragma unroll 1
+                look(smem_u32(&sh->q_full), piece & 1);
+                // Per round: the scores of step t, then P V of step t - 1, whose softmax ran meanwhile.
+#pragma unroll 1
                 for (int t = 0; t <= n && ok; ++t) {
                     const int st = step + t;
-                    const uint64_t stage = smem_desc_sw128(sm_ring + (st & 1) * chunks * kSlotBytes);
+                    was[0] = at[0], was[1] = at[1];
                     if (t < n) {
-                        if (st > 0) ok = wait(&sh->s_free, st - 1);
+                        if (st > 0 && !look(smem_u32(&sh->s_free), (st - 1) & 1)) break;
+                        if (nx && !look(x_full + 8 * (st & 1), (st >> 1) & 1)) break;
+                        const uint64_t b = dx + (st & 1) * (kOthers * kSlotStep);
                         if (widest) {
-                            const int g = half ^ 1;
-                            wait_group(g, st);
-                            if (!ok) break;
-                            const uint64_t b = stage + g * kGroup * kSlotStep, b8 = stage + 2 * kGroup * kSlotStep;
-    #pragma unroll
+#pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 mma_bf16_ts(ts, tq + 128 + k * 8, b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, k > 0);
-    #pragma unroll
-                            for (int k = 8; k < 16; ++k)
+#pragma unroll
+                            for (int k = 8; k < 20; ++k)
                                 mma_bf16(ts, dq + ((k >> 2) - 2) * kQStep + 2 * (k & 3),
-                                            b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, 1);
-                            free_group(g, st);
-                            wait_group(2, st);
-                            if (!ok) break;
-    #pragma unroll
-                            for (int k = 0; k < 4; ++k) mma_bf16(ts, dq + 2 * kQStep + 2 * k, b8 + 2 * k, idesc_s, 1);
-                            free_group(2, st);
+                                         b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, 1);
                         } else {
-    #pragma unroll 1
-                            for (int i = 0; i + 1 < groups && ok; ++i) {
-                                const int g = group_at(i);
-                                wait_group(g, st);
-                                if (!ok) break;
-                                group_mma(g, stage, i == 0);
-                                free_group(g, st);
-                            }
+                            for (int i = 0; i < nx; ++i) chunk_mma(other(i), b + i * kSlotStep, i == 0);
                         }
+                        if (nx) mma_commit(x_empty + 8 * (st & 1));
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (e >= pairs) break;
+                            if (!look(y_full + 8 * y, yp)) break;
+                            const uint64_t v = dy + y * (2 * kSlotStep);
+                            if (widest) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_bf16_ts(ts, tq + e * 64 + k * 8, v + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, 1);
+                            } else {
+                                for (int i = 0; i < 2 && 2 * e + i < nvc; ++i)
+                                    chunk_mma(v0 + 2 * e + i, v + i * kSlotStep, nx == 0 && e == 0 && i == 0);
+                            }
+                            at[e] = y;
+                            if (++y == kPairs) y = 0, yp ^= 1u;
+                        }
+                        if (!ok) break;
+                        mma_commit(smem_u32(&sh->s_full));
                     }
                     if (t > 0) {
-                        const int pv = st - 1;
-                        ok = ok && wait(&sh->p_full, pv);
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t b =
-                            smem_desc_sw128_mn(sm_ring + ((pv & 1) * chunks + half * kGroup) * kSlotBytes, kSlotBytes);
-    #pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            mma_bf16(to, dp + 2 * k, b + k * (2048 >> 4), idesc_o, t > 1 || k > 0);
-                        mma_commit(smem_u32(&sh->pv_done));
-                        free_group(half, pv);
-                    }
-                    if (t < n) {
-                        wait_group(half, st);
-                        if (!ok) break;
-                        if (widest) {
-                            const uint64_t b = stage + half * kGroup * kSlotStep;
-    #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                mma_bf16_ts(ts, tq + k * 8, b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, 1);
-                        } else {
-                            group_mma(half, stage, groups == 1);
+                        if (!look(smem_u32(&sh->p_full), (st - 1) & 1)) break;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            if (e >= pairs) break;
+                            if (e * 128 < dv) {  // (a pair may hold no value column)
+                                const uint64_t v = dvals + was[e] * (2 * kSlotStep);
+#pragma unroll
+                                for (int k = 0; k < kKeys / 16; ++k)
+                                    mma_bf16(to + e * 128, dp + 2 * k, v + k * (2048 >> 4), id[e], t > 1 || k > 0);
+                            }
+                            mma_commit(y_empty + 8 * was[e]);
                         }
-                        mma_commit(smem_u32(&sh->s_full));
+                        mma_commit(smem_u32(&sh->pv_done));
                     }
                 }
                 if (!ok) break;
@@ -660,10 +664,22 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The lanes look up the rows of 32 boxes at a time; one thread issues the copies.
         const int per = kKeys / p.box, batch = 32 / per;  // boxes per step, steps per lookup
         const bool lead = elect_one();
-        const uint32_t full0 = smem_u32(&sh->full[0][0]), empty0 = smem_u32(&sh->empty[0][0]);
+        const uint32_t x_full = smem_u32(&sh->x_full[0]), x_empty = smem_u32(&sh->x_empty[0]);
+        const uint32_t y_full = smem_u32(&sh->y_full[0]), y_empty = smem_u32(&sh->y_empty[0]);
         const uint32_t box_bytes = p.box * 128;
-        const bool single = per == 1;
-        int bits = 0, loaded = 0;  // loaded: copies' barriers armed, in the order of group_at
+        const bool whole = per == 1 && p.C == 64 * kMaxChunks;
+        int bits = 0, y = 0, xs = 0, ys = 0;  // xs, ys: barriers armed
+        uint32_t yp = 1;
+        // `count` chunks from chunk `ck` on to `dst`, box by box
+        auto copy = [&](uint32_t dst, uint32_t bar, int ck, int count, int rows, int box0) {
+#pragma unroll 1
+            for (int e = 0; e < per; ++e) {
+                const int row = __shfl_sync(~0u, rows, box0 + e);
+                if (lead)
+                    for (int c = 0; c < count; ++c)
+                        tma_load_3d(dst + e * box_bytes + c * kSlotBytes, &tm_c, bar, (ck + c) * 64, 0, row);
+            }
+        };
         while (ok && walk.next(p, &x)) {
             const int n = x.n, key0 = x.key0, end = x.end;
             const int32_t* row_table = p.table + static_cast<int64_t>(x.page_row) * p.max_pages;
@@ -680,42 +696,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int j = 0; j < steps && ok; ++j, ++step) {
                     const int st = step & 1;
-                    const uint32_t parity = ((step >> 1) & 1) ^ 1;
-                    const uint32_t ring = sm_ring + st * chunks * kSlotBytes;
                     const int row0 = __shfl_sync(~0u, rows, j * per);
-#pragma unroll 1
-                    for (int k = 0; k < groups; ++k) {
-                        const int g = group_at(k), nc = group_chunks(g);
-                        const uint32_t bar = full0 + 8 * (st * kMaxGroups + g), dst = ring + g * kGroup * kSlotBytes;
-                        const bool whole = single && (g + 1) * kGroup * 64 <= p.C;
+                    if (nx) {
+                        const uint32_t bar = x_full + 8 * st, dst = sm_x + st * kOthers * kSlotBytes;
                         if (lead) {
-                            ok = mbar_wait_lean(empty0 + 8 * (st * kMaxGroups + g), parity, kTimeoutNs, abort_flag);
+                            ok = mbar_wait_lean(x_empty + 8 * st, ((step >> 1) & 1) ^ 1, kTimeoutNs, abort_flag);
                             if (ok) {
-                                mbar_arrive_expect_tx(bar, nc * kSlotBytes);
-                                ++loaded;
-                                if (whole) tma_load_3d(dst, &tm_g, bar, 0, row0, g * kGroup);
+                                mbar_arrive_expect_tx(bar, nx * kSlotBytes);
+                                ++xs;
+                                if (whole) {
+                                    tma_load_3d(dst, &tm_4, bar, 0, row0, v0 ^ kGroup);
+                                    tma_load_3d(dst + kGroup * kSlotBytes, &tm_c, bar, 2 * kGroup * 64, 0, row0);
+                                }
                             }
                         }
                         ok = __all_sync(~0u, ok);
                         if (!ok) break;
                         if (!whole) {
+                            copy(dst, bar, other(0), min(nx, v0 ? v0 : nx), rows, j * per);
+                            if (v0 && nx > v0) copy(dst + v0 * kSlotBytes, bar, other(v0), nx - v0, rows, j * per);
+                        }
+                    }
 #pragma unroll 1
-                            for (int e = 0; e < per; ++e) {
-                                const int row = __shfl_sync(~0u, rows, j * per + e);
-                                if (lead)
-                                    for (int c = 0; c < nc; ++c)
-                                        tma_load_3d(dst + e * box_bytes + c * kSlotBytes, &tm_c, bar, (g * kGroup + c) * 64, 0, row);
+                    for (int e = 0; e < pairs; ++e) {
+                        const uint32_t bar = y_full + 8 * y, dst = sm_y + y * 2 * kSlotBytes;
+                        const int count = min(2, nvc - 2 * e);
+                        if (lead) {
+                            ok = mbar_wait_lean(y_empty + 8 * y, yp, kTimeoutNs, abort_flag);
+                            if (ok) {
+                                mbar_arrive_expect_tx(bar, count * kSlotBytes);
+                                ++ys;
+                                if (whole) tma_load_3d(dst, &tm_2, bar, 0, row0, v0 + 2 * e);
                             }
                         }
+                        ok = __all_sync(~0u, ok);
+                        if (!ok) break;
+                        if (!whole) copy(dst, bar, v0 + 2 * e, count, rows, j * per);
+                        if (++y == kPairs) y = 0, yp ^= 1u;
                     }
                 }
             }
         }
         // no copy may still be landing when the CTA leaves
-        if (lead)
-            for (int u = max(loaded - 2 * groups, 0); u < loaded; ++u)
-                mbar_wait(full0 + 8 * ((u / groups & 1) * kMaxGroups + group_at(u % groups)), (u / groups >> 1) & 1,
-                          kTimeoutNs, nullptr);
+        if (lead) {
+            for (int u = max(xs - 2, 0); u < xs; ++u) mbar_wait(x_full + 8 * (u & 1), (u >> 1) & 1, kTimeoutNs, nullptr);
+            for (int u = max(ys - kPairs, 0); u < ys; ++u)
+                mbar_wait(y_full + 8 * (u % kPairs), (u / kPairs) & 1, kTimeoutNs, nullptr);
+        }
         if (bits) raise_status(p.status, bits);
     }
     if (!ok) {
@@ -867,14 +894,17 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     if (workspace_bytes < y.bytes) return MLA_ERR_INVALID_ARG;
     const int C = d->kv_lora_rank + d->rope_dim, box = gcd(d->page_size, kKeys);
     const int64_t rows = d->num_pages * d->page_size;
-    CUtensorMap tm, tm_group;
+    CUtensorMap tm, tm4, tm2;
     // an empty cache has no valid page: every read is outside the map, which then only needs a valid address
-    if (!encode_bf16_3d(&tm, rows ? kv_cache : q, C, 1, rows ? rows : 1, 1, box))
-        return report_cuda(cudaErrorInvalidValue, "tensor map of attend_cache");
-    // the same rows by whole chunks, [chunk][row][64]: a copy of kGroup chunks lands chunk after chunk
-    if (C >= 64 * kGroup ? !encode_bf16_chunks(&tm_group, rows ? kv_cache : q, C, rows ? rows : 1, box, kGroup)
-                         : (tm_group = tm, false))
-        return report_cuda(cudaErrorInvalidValue, "tensor map of attend_cache");
+    const void* base = rows ? kv_cache : q;
+    bool good = encode_bf16_3d(&tm, base, C, 1, rows ? rows : 1, 1, box);
+    // the same rows by whole chunks, [chunk][row][64], four or two of them in one copy
+    const bool widest = C == 64 * kMaxChunks;
+    tm4 = tm2 = tm;
+    if (widest)
+        good = good && encode_bf16_chunks(&tm4, base, C, rows ? rows : 1, box, 4) &&
+               encode_bf16_chunks(&tm2, base, C, rows ? rows : 1, box, 2);
+    if (!good) return report_cuda(cudaErrorInvalidValue, "tensor maps of attend_cache");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     CacheParams p{static_cast<const uint16_t*>(q), page_table, seq_lens, seqs, shared_len, static_cast<uint16_t*>(out),
                   lse, status, reinterpret_cast<Cut*>(ws), reinterpret_cast<int64_t*>(ws + y.bases),
@@ -885,7 +915,7 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaFuncSetAttribute(mla_attend_cache_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return report_cuda(e, "mla_attend_cache_kernel attributes");
-    mla_attend_cache_kernel<<<y.units * y.halves, kThreads, kSmem, st>>>(tm, tm_group, p);
+    mla_attend_cache_kernel<<<y.units * y.halves, kThreads, kSmem, st>>>(tm, tm4, tm2, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
     const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
     mla_attend_join_kernel<<<static_cast<unsigned>(blocks), 128, 0, st>>>(p);
