@@ -167,6 +167,10 @@ def _stream_ptr(stream: Optional[torch.cuda.Stream]) -> Optional[int]:
 def _ptr(t: Optional[torch.Tensor], name: str, dtype, shape: Sequence[int], device) -> Optional[int]:
     if t is None:
         return None
+    # the usual case first: a call of a small operator takes a few microseconds in all
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == device.index and \
+            t.shape == shape and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.device != device:
@@ -377,10 +381,23 @@ def _on(t: torch.Tensor, name: str, dims: int) -> torch.device:
 
 
 def _stream_on(device, stream: Optional[torch.cuda.Stream]) -> Optional[int]:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    if s.device != device:
-        raise ValueError(f"the stream is on {s.device}, the tensors on {device}")
-    return s.cuda_stream or None
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device.index) or None
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
+    return stream.cuda_stream or None
+
+
+def _run(name: str, device, *args) -> None:
+    """Calls an entry point with `device` as the current one."""
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = f(*args)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args)
+    if rc != MLA_OK:
+        raise MlaPrologError(rc, name)
 
 
 def attend_prompt(q, k, v, cu_q, cu_k, out, lse=None, *, scale: float, causal: bool = True, q_scale=None,
@@ -408,9 +425,7 @@ def attend_prompt(q, k, v, cu_q, cu_k, out, lse=None, *, scale: float, causal: b
             _ptr(v, "v", bf, (Tk, Hk, Dv), dev), _ptr(cu_q, "cu_q", i32, (n + 1,), dev),
             _ptr(cu_k, "cu_k", i32, (n + 1,), dev), _ptr(out, "out", bf, (Tq, H, Dv), dev),
             _ptr(lse, "lse", f32, (Tq, H), dev), _ptr(status, "status", i32, (1,), dev)]
-    with torch.cuda.device(dev):
-        _check(lib().mla_prolog_attend_prompt(ctypes.byref(d), *args, _stream_on(dev, stream)),
-               "mla_prolog_attend_prompt")
+    _run("mla_prolog_attend_prompt", dev, ctypes.byref(d), *args, _stream_on(dev, stream))
 
 
 def attend_cache_workspace_bytes(batch: int, num_heads: int, kv_lora_rank: int, rope_dim: int) -> int:
@@ -441,8 +456,7 @@ def attend_cache(q, kv_cache, page_table, seq_lens, out, lse, workspace, *, scal
             _ptr(out, "out", bf, (B, H, Lkv), dev), _ptr(lse, "lse", torch.float32, (B, H), dev),
             _ptr(workspace, "workspace", torch.uint8, tuple(workspace.shape), dev), workspace.numel(),
             _ptr(status, "status", i32, (1,), dev)]
-    with torch.cuda.device(dev):
-        _check(lib().mla_prolog_attend_cache(ctypes.byref(d), *args, _stream_on(dev, stream)), "mla_prolog_attend_cache")
+    _run("mla_prolog_attend_cache", dev, ctypes.byref(d), *args, _stream_on(dev, stream))
 
 
 class PagePool:
@@ -464,8 +478,7 @@ class PagePool:
         return _ptr(t, name, torch.int32, (n,), self.device)
 
     def _call(self, name, *args, stream):
-        with torch.cuda.device(self.device):
-            _check(getattr(lib(), name)(ctypes.byref(self._pool), *args, _stream_on(self.device, stream)), name)
+        _run(name, self.device, ctypes.byref(self._pool), *args, _stream_on(self.device, stream))
 
     def extend(self, seqs, counts, slot_mapping=None, positions=None, stream=None) -> None:
         """Grows sequence seqs[i] by counts[i] tokens; slot_mapping and
@@ -508,5 +521,4 @@ def copy_pages(cache, src, dst, status=None, stream=None) -> None:
     args = [_ptr(cache, "cache", torch.bfloat16, tuple(cache.shape), dev), shape[0], shape[1] * page_bytes, shape[1],
             page_bytes, _ptr(src, "src", torch.int32, (n,), dev), _ptr(dst, "dst", torch.int32, (n,), dev), n,
             _ptr(status, "status", torch.int32, (1,), dev)]
-    with torch.cuda.device(dev):
-        _check(lib().mla_prolog_copy_pages(*args, _stream_on(dev, stream)), "mla_prolog_copy_pages")
+    _run("mla_prolog_copy_pages", dev, *args, _stream_on(dev, stream))

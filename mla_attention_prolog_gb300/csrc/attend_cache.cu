@@ -50,6 +50,9 @@ constexpr uint32_t kColO = 0, kColQ = 256, kColS = 448;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;             // log2 of the largest P
+// Own pages are asked of L2 this many steps before their copies: the ring holds two steps, which cover the
+// latency of L2 but not that of HBM.
+constexpr int kFetch = 2;
 constexpr int kOverhead = 7;              // a tile's start and end, in key steps
 constexpr int kMinRun = 8;                // shortest run worth a CTA pair, in key steps
 
@@ -63,6 +66,7 @@ struct Cut {
 
 struct CacheParams {
     const uint16_t* q;
+    const uint16_t* cache;
     const int32_t* table;
     const int32_t* lens;
     const int32_t* seqs;
@@ -683,20 +687,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && walk.next(p, &x)) {
             const int n = x.n, key0 = x.key0, end = x.end;
             const int32_t* row_table = p.table + static_cast<int64_t>(x.page_row) * p.max_pages;
+            // first row of box `lane` of the batch that starts at step j; a row outside the cache reads as zeros
+            auto look_up = [&](int j) {
+                const int key = key0 + (j * per + lane) * p.box;
+                if (j * per + lane >= n * per || key >= end) return p.num_rows;
+                const int page = row_table[key / p.page_size];
+                if (page >= 0 && page < p.num_pages) return page * p.page_size + key % p.page_size;
+                bits |= kStatusPageRange;
+                return p.num_rows;
+            };
+            // Asks L2 for this lane's box of cache rows, which lie in one piece of memory.
+            auto fetch = [&](int row) {
+                if (row < p.num_rows) bulk_prefetch_l2(p.cache + static_cast<int64_t>(row) * p.C, p.box * p.C * 2);
+            };
+            int rows = look_up(0), ahead = batch < n ? look_up(batch) : p.num_rows;
+            const bool far = !x.prefix && lane / per < batch;
+            if (far && lane / per < kFetch && (lane / per & (p.halves - 1)) == half) fetch(rows);
 #pragma unroll 1
             for (int j0 = 0; j0 < n && ok; j0 += batch) {
-                const int key = key0 + (j0 * per + lane) * p.box;
-                int rows = p.num_rows;  // outside the cache: reads as zeros
-                if (key < end) {
-                    const int page = row_table[key / p.page_size];
-                    if (page >= 0 && page < p.num_pages) rows = page * p.page_size + key % p.page_size;
-                    else if (j0 * per + lane < n * per) bits |= kStatusPageRange;
+                if (j0) {
+                    rows = ahead;
+                    ahead = j0 + batch < n ? look_up(j0 + batch) : p.num_rows;
                 }
                 const int steps = min(batch, n - j0);
 #pragma unroll 1
                 for (int j = 0; j < steps && ok; ++j, ++step) {
                     const int st = step & 1;
                     const int row0 = __shfl_sync(~0u, rows, j * per);
+                    // step j + kFetch of the run, alternately by the two CTAs
+                    if (far && lane / per == (j + kFetch) % batch && (j & (p.halves - 1)) == half)
+                        fetch(j + kFetch < batch ? rows : ahead);
                     if (nx) {
                         const uint32_t bar = x_full + 8 * st, dst = sm_x + st * kOthers * kSlotBytes;
                         if (lead) {
@@ -906,7 +926,7 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
                encode_bf16_chunks(&tm2, base, C, rows ? rows : 1, box, 2);
     if (!good) return report_cuda(cudaErrorInvalidValue, "tensor maps of attend_cache");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    CacheParams p{static_cast<const uint16_t*>(q), page_table, seq_lens, seqs, shared_len, static_cast<uint16_t*>(out),
+    CacheParams p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(kv_cache), page_table, seq_lens, seqs, shared_len, static_cast<uint16_t*>(out),
                   lse, status, reinterpret_cast<Cut*>(ws), reinterpret_cast<int64_t*>(ws + y.bases),
                   reinterpret_cast<float*>(ws + y.part_o), reinterpret_cast<float*>(ws + y.part_lse), d->batch,
                   d->num_heads, d->kv_lora_rank, C, d->page_size, d->table_rows, d->max_pages,

@@ -17,7 +17,6 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxList = 1024;
 constexpr int kPer = kMaxList / kThreads;  // list entries per thread
-constexpr int kSpan = kThreads * 32;       // pages per pass over refs
 
 struct Pool {
     int32_t sequences, max_pages, page_size, num_pages;
@@ -61,14 +60,29 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* total) {
     return x - v + (warp ? before : 0);
 }
 
-// Free pages among base + 32 * threadIdx.x .. + 31, one bit each.  The warp
-// reads its 1024 counts in 32 coalesced rows and each lane keeps one ballot.
-__device__ __forceinline__ uint32_t free_mask(const Pool& p, int64_t base) {
+// One pass over refs covers kWarps x words x 32 pages: warp w the words * 32
+// pages from base + w * words * 32 on, whose bits lane k < words keeps for the
+// k-th 32 of them.  Few pages are spread over all warps, many go in several
+// passes of the largest size.
+struct Span {
+    int words;
+    int64_t pages;
+};
+__device__ __forceinline__ Span span_of(const Pool& p) {
+    const int w = ceil_div(p.num_pages, kThreads);
+    const int words = w < 1 ? 1 : w > 32 ? 32 : w;
+    return Span{words, static_cast<int64_t>(words) * kThreads};
+}
+__device__ __forceinline__ int64_t warp_base(const Span& sp, int64_t base) {
+    return base + static_cast<int64_t>(threadIdx.x >> 5) * sp.words * 32;
+}
+
+__device__ __forceinline__ uint32_t free_mask(const Pool& p, const Span& sp, int64_t base) {
     const int lane = threadIdx.x & 31;
-    const int64_t at = base + (threadIdx.x >> 5) * 1024;
+    const int64_t at = warp_base(sp, base);
     uint32_t mine = 0;
 #pragma unroll 8
-    for (int k = 0; k < 32; ++k) {
+    for (int k = 0; k < sp.words; ++k) {
         const int64_t q = at + k * 32 + lane;
         const uint32_t m = __ballot_sync(~0u, q < p.num_pages && p.refs[q] == 0);
         if (lane == k) mine = m;
@@ -76,19 +90,38 @@ __device__ __forceinline__ uint32_t free_mask(const Pool& p, int64_t base) {
     return mine;
 }
 
-__device__ __forceinline__ uint32_t live_mask(const Pool& p, int64_t base, uint32_t free) {
-    const int64_t first = base + static_cast<int64_t>(threadIdx.x) * 32;
-    const int64_t n = p.num_pages - first;
-    const uint32_t in = n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u;
-    return in & ~free;
+// Bits of this lane's 32 pages that lie in [from, to).
+__device__ __forceinline__ uint32_t range_mask(const Span& sp, int64_t base, int64_t from, int64_t to) {
+    const int lane = threadIdx.x & 31;
+    if (lane >= sp.words) return 0;
+    const int64_t first = warp_base(sp, base) + lane * 32, a = from - first, b = to - first;
+    const uint32_t below = b >= 32 ? ~0u : b <= 0 ? 0u : (1u << b) - 1u;
+    return a >= 32 ? 0u : a <= 0 ? below : below & ~((1u << a) - 1u);
 }
 
-// Whether entry i is the first of its value in list[0 .. i).
-__device__ __forceinline__ bool first_listing(const int32_t* list, int i) {
-    const int v = list[i];
-    for (int j = 0; j < i; ++j)
-        if (list[j] == v) return false;
-    return true;
+// Runs f(page, whether its bit is set, its rank) with a lane per page; `rank`
+// is the rank of the lane's first bit.
+template <class F>
+__device__ __forceinline__ void for_pages(const Pool& p, const Span& sp, int64_t base, uint32_t bits, int64_t rank, F f) {
+    const int lane = threadIdx.x & 31;
+    const int64_t at = warp_base(sp, base);
+    for (int k = 0; k < sp.words && at + k * 32 < p.num_pages; ++k) {
+        const uint32_t m = __shfl_sync(~0u, bits, k);
+        const int64_t r = __shfl_sync(~0u, rank, k) + __popc(m & ((1u << lane) - 1u));
+        const int64_t page = at + k * 32 + lane;
+        if (page < p.num_pages) f(static_cast<int32_t>(page), (m >> lane & 1u) != 0, r);
+    }
+}
+
+// Sets again[i] for entries that repeat one before them.  A warp per entry.
+__device__ __forceinline__ void find_repeats(const int32_t* list, int n, uint8_t* again) {
+    for (int e = threadIdx.x >> 5; e < n; e += kWarps) {
+        bool hit = false;
+        const int v = list[e];
+        for (int j = threadIdx.x & 31; j < e; j += 32) hit |= list[j] == v;
+        if (__any_sync(~0u, hit)) hit = true;
+        if ((threadIdx.x & 31) == 0) again[e] = hit;
+    }
 }
 
 // The last entry e of the ascending first[0 .. n) with first[e] <= r.
@@ -109,30 +142,31 @@ __device__ __forceinline__ int find_entry(const int64_t* first, int n, int64_t r
 template <class Fits, class Place>
 __device__ __forceinline__ void deal_pages(const Pool& p, const int64_t* first, const int32_t* need, int n,
                                            int64_t want, Fits fits, Place place) {
-    int64_t have = 0;
+    const Span sp = span_of(p);
+    int64_t have = 0, rank = 0, sum, at = -1;
     uint32_t mask = 0;
-    int64_t at = -1;
-    for (int64_t base = 0; base < p.num_pages && have < want; base += kSpan) {
-        mask = free_mask(p, base);
+    for (int64_t base = 0; base < p.num_pages && have < want; base += sp.pages) {
+        mask = free_mask(p, sp, base);
         at = base;
-        int64_t sum;
-        block_scan(__popc(mask), &sum);
+        rank = block_scan(__popc(mask), &sum);
         have += sum;
     }
     for (int e = threadIdx.x; e < n; e += kThreads) fits(e, first[e] + need[e] <= have);
-    if (want == 0 || have == 0) return;
-    int64_t rank0 = 0;
-    for (int64_t base = 0; base < p.num_pages && rank0 < want; base += kSpan) {
-        if (base != at) mask = free_mask(p, base), at = base;
-        int64_t sum;
-        int64_t r = rank0 + block_scan(__popc(mask), &sum);
-        for (uint32_t m = mask; m && r < want; m &= m - 1, ++r) {
-            // entries that need nothing share their first rank with the next one: find the taker
-            int e = find_entry(first, n, r);
-            if (first[e] + need[e] <= have) place(e, static_cast<int>(r - first[e]),
-                                                  static_cast<int32_t>(base + threadIdx.x * 32 + __ffs(m) - 1));
+    int64_t before = 0;
+    for (int64_t base = 0; base < p.num_pages && before < want; base += sp.pages) {
+        if (base != at) {
+            mask = free_mask(p, sp, base);
+            at = base;
+            rank = block_scan(__popc(mask), &sum);
+        } else if (base) {
+            rank = block_scan(__popc(mask), &sum);
         }
-        rank0 += sum;
+        for_pages(p, sp, base, mask, before + rank, [&](int32_t page, bool set, int64_t r) {
+            if (!set || r >= want) return;
+            const int e = find_entry(first, n, r);  // (an entry that needs nothing is never the last at or below r)
+            if (first[e] + need[e] <= have) place(e, static_cast<int>(r - first[e]), page);
+        });
+        before += sum;
     }
 }
 
@@ -142,10 +176,12 @@ __global__ void __launch_bounds__(kThreads) mla_pages_extend_kernel(Pool p, cons
                                                                     int32_t* __restrict__ positions, int total) {
     __shared__ int32_t seq[kMaxList], need[kMaxList], old[kMaxList];
     __shared__ int64_t first[kMaxList], tok[kMaxList];
-    __shared__ uint8_t ok[kMaxList];
+    __shared__ uint8_t ok[kMaxList], again[kMaxList];
     const int t = threadIdx.x;
     const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
     for (int i = t; i < n; i += kThreads) seq[i] = seqs[i];
+    __syncthreads();
+    find_repeats(seq, n, again);
     __syncthreads();
     int64_t sum_need = 0, sum_tok = 0;
     int64_t cnt[kPer];
@@ -160,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_extend_kernel(Pool p, cons
         cnt[k] = c > 0 ? c : 0;
         int nd = 0, len = 0;
         uint8_t good = 0;
-        if (s < 0 || s >= p.sequences || c < 0 || !first_listing(seq, i)) {
+        if (s < 0 || s >= p.sequences || c < 0 || again[i]) {
             bits |= kStatusSeqRange;
         } else {
             len = seq_len(p, s);
@@ -233,9 +269,11 @@ __global__ void __launch_bounds__(kThreads) mla_pages_fork_kernel(Pool p, const 
                                                                   int32_t* __restrict__ dst) {
     __shared__ int32_t par[kMaxList], child[kMaxList], need[kMaxList], len[kMaxList];
     __shared__ int64_t first[kMaxList];
-    __shared__ uint8_t ok[kMaxList];
+    __shared__ uint8_t ok[kMaxList], again[kMaxList];
     const int t = threadIdx.x;
     for (int i = t; i < n; i += kThreads) par[i] = parents[i], child[i] = children[i];
+    __syncthreads();
+    find_repeats(child, n, again);
     __syncthreads();
     int64_t sum_need = 0;
     int bits = 0;
@@ -244,8 +282,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_fork_kernel(Pool p, const 
         const int i = t * kPer + k;
         if (i >= n) continue;
         const int a = par[i], c = child[i];
-        const bool good = a >= 0 && a < p.sequences && c >= 0 && c < p.sequences && p.lens[c] == 0 &&
-                          first_listing(child, i);
+        const bool good = a >= 0 && a < p.sequences && c >= 0 && c < p.sequences && p.lens[c] == 0 && !again[i];
         if (!good) bits |= kStatusSeqRange;
         len[i] = good ? seq_len(p, a) : 0;
         need[i] = len[i] % p.page_size != 0;
@@ -327,60 +364,54 @@ __global__ void __launch_bounds__(kThreads) mla_pages_release_kernel(Pool p, con
     raise_status(p.status, bits);
 }
 
-// Where each live page goes.  A mover of rank j (the j-th live page at or
-// above L) lies at L + j or later, so the hole of rank j is parked in
-// moved_to[L + j] first; going through the spans from the highest down, and
-// reading a span's parked holes before its places are written, every hole is
-// read before it is overwritten.
+// Where each live page goes.  The holes (free pages below L) are listed in
+// moved_to[0 ..) first: a mover's rank is below L and its own place at or
+// above, so reading the list and writing the movers' places do not meet; the
+// places below L are written last.
 __global__ void __launch_bounds__(kThreads) mla_pages_compact_kernel(Pool p, int32_t* __restrict__ moved_to,
                                                                      int32_t* __restrict__ live_out) {
     const int t = threadIdx.x;
-    int64_t live = 0, sum;
+    const Span sp = span_of(p);
+    int64_t live = 0, sum, at = -1;
     uint32_t mask = 0;
-    int64_t at = -1;
-    for (int64_t base = 0; base < p.num_pages; base += kSpan) {
-        mask = free_mask(p, base), at = base;
-        block_scan(__popc(live_mask(p, base, mask)), &sum);
+    auto load = [&](int64_t base) {
+        if (base != at) mask = free_mask(p, sp, base), at = base;
+    };
+    for (int64_t base = 0; base < p.num_pages; base += sp.pages) {
+        load(base);
+        block_scan(__popc(range_mask(sp, base, 0, p.num_pages) & ~mask), &sum);
         live += sum;
     }
     if (t == 0 && live_out) *live_out = static_cast<int32_t>(live);
-    int64_t rank0 = 0;
-    for (int64_t base = 0; base < live; base += kSpan) {
-        if (base != at) mask = free_mask(p, base), at = base;
-        const int64_t own = base + t * 32;
-        uint32_t holes = mask;
-        if (own + 32 > live) holes = own >= live ? 0u : mask & ((1u << (live - own)) - 1u);
-        int64_t r = rank0 + block_scan(__popc(holes), &sum);
-        for (uint32_t m = holes; m; m &= m - 1, ++r) moved_to[live + r] = static_cast<int32_t>(own + __ffs(m) - 1);
-        rank0 += sum;
+    int64_t before = 0;
+    for (int64_t base = 0; base < live; base += sp.pages) {
+        load(base);
+        const uint32_t holes = mask & range_mask(sp, base, 0, live);
+        const int64_t rank = before + block_scan(__popc(holes), &sum);
+        for_pages(p, sp, base, holes, rank, [&](int32_t page, bool set, int64_t r) {
+            if (set) moved_to[r] = page;
+        });
+        before += sum;
     }
-    const int64_t movers = rank0;  // as many live pages lie at or above L as holes below it
-    int64_t above = movers;
-    const int64_t spans = (p.num_pages + kSpan - 1) / kSpan;
-    for (int64_t sp = spans - 1; sp >= 0; --sp) {
-        const int64_t base = sp * kSpan, own = base + t * 32;
-        if (base != at) mask = free_mask(p, base), at = base;
-        const uint32_t lv = live_mask(p, base, mask);
-        uint32_t go = lv;
-        if (own < live) go = own + 32 <= live ? 0u : lv & ~((1u << (live - own)) - 1u);
-        int64_t r = block_scan(__popc(go), &sum);  // a barrier: parked holes and earlier reads are done
-        above -= sum;
-        r += above;
-        int32_t to[32];
-        int k = 0;
-#pragma unroll 1
-        for (uint32_t m = go; m; m &= m - 1) to[k++] = moved_to[live + r++];
-        __syncthreads();
-        k = 0;
-#pragma unroll 1
-        for (int b = 0; b < 32 && own + b < p.num_pages; ++b) {
-            const int32_t page = static_cast<int32_t>(own + b);
-            int32_t place = (lv >> b & 1u) ? page : -1;
-            if (go >> b & 1u) place = to[k++];
-            moved_to[page] = place;
-        }
-        __syncthreads();
+    __syncthreads();
+    before = 0;
+    for (int64_t base = live / sp.pages * sp.pages; base < p.num_pages; base += sp.pages) {
+        load(base);
+        const uint32_t go = range_mask(sp, base, live, p.num_pages) & ~mask;
+        const int64_t rank = before + block_scan(__popc(go), &sum);
+        for_pages(p, sp, base, go, rank, [&](int32_t page, bool set, int64_t r) {
+            if (page >= live) moved_to[page] = set ? moved_to[r] : -1;
+        });
+        before += sum;
     }
+    __syncthreads();
+    for (int64_t base = 0; base < live; base += sp.pages) {
+        load(base);
+        for_pages(p, sp, base, mask, 0, [&](int32_t page, bool free, int64_t) {
+            if (page < live) moved_to[page] = free ? -1 : page;
+        });
+    }
+    __syncthreads();
     for (int64_t page = live + t; page < p.num_pages; page += kThreads) {
         const int32_t place = moved_to[page];
         if (place < 0) continue;
@@ -405,22 +436,45 @@ __global__ void __launch_bounds__(256) mla_pages_retable_kernel(Pool p, const in
     raise_status(p.status, bits);
 }
 
-__global__ void __launch_bounds__(256) mla_copy_pages_kernel(uint8_t* __restrict__ cache, int64_t layer_stride,
-                                                             int64_t num_pages, int64_t page_bytes,
-                                                             const int32_t* __restrict__ src,
-                                                             const int32_t* __restrict__ dst, int32_t* status) {
-    const int i = blockIdx.x;
-    const int64_t a = src ? src[i] : i, b = dst[i];
-    if (a < 0 || b < 0 || a == b) return;
-    if (a >= num_pages || b >= num_pages) {
-        if (threadIdx.x == 0) raise_status(status, kStatusPageRange);
-        return;
-    }
+// A CTA copies `per` entries' pages of one layer, or one of `pieces` pieces of
+// one entry's page; each thread keeps 8 loads of 16 bytes in flight.
+constexpr int kCopyThreads = 256, kCopyLoads = 8, kCopyStep = kCopyThreads * kCopyLoads;
+
+__global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(uint8_t* __restrict__ cache, int64_t layer_stride,
+                                                                     int64_t num_pages, int64_t page_bytes,
+                                                                     const int32_t* __restrict__ src,
+                                                                     const int32_t* __restrict__ dst, int n, int per,
+                                                                     int pieces, int32_t* status) {
     uint8_t* layer = cache + blockIdx.y * layer_stride;
-    const uint4* from = reinterpret_cast<const uint4*>(layer + a * page_bytes);
-    uint4* to = reinterpret_cast<uint4*>(layer + b * page_bytes);
-    const int64_t n = page_bytes / 16;
-    for (int64_t j = threadIdx.x; j < n; j += 256) to[j] = from[j];
+    const int64_t words = page_bytes / 16;
+    const int64_t piece = (words + pieces - 1) / pieces, from_word = blockIdx.z * piece;
+    const int64_t to_word = from_word + piece < words ? from_word + piece : words;
+    // the entries' pages in one look (the first `per` lanes' answers)
+    const int lane = threadIdx.x & 31, i0 = blockIdx.x * per;
+    int a = -1, b = -1;
+    if (lane < per && i0 + lane < n) {
+        b = dst[i0 + lane];
+        a = src ? src[i0 + lane] : i0 + lane;
+    }
+    bool go = a >= 0 && b >= 0 && a != b;
+    if (go && (a >= num_pages || b >= num_pages)) {
+        go = false;
+        if (threadIdx.x < 32) raise_status(status, kStatusPageRange);
+    }
+    for (uint32_t todo = __ballot_sync(~0u, go); todo; todo &= todo - 1) {
+        const int e = __ffs(todo) - 1;
+        const uint4* from = reinterpret_cast<const uint4*>(layer + __shfl_sync(~0u, a, e) * page_bytes);
+        uint4* to = reinterpret_cast<uint4*>(layer + __shfl_sync(~0u, b, e) * page_bytes);
+        for (int64_t j = from_word + threadIdx.x; j < to_word; j += kCopyStep) {
+            uint4 v[kCopyLoads];
+#pragma unroll
+            for (int k = 0; k < kCopyLoads; ++k)
+                if (j + k * kCopyThreads < to_word) v[k] = __ldcs(from + j + k * kCopyThreads);
+#pragma unroll
+            for (int k = 0; k < kCopyLoads; ++k)
+                if (j + k * kCopyThreads < to_word) __stcs(to + j + k * kCopyThreads, v[k]);
+        }
+    }
 }
 
 int check_pool(const mla_prolog_pool* h, Pool* p) {
@@ -525,8 +579,15 @@ int mla_prolog_copy_pages(void* cache, int32_t layers, int64_t layer_stride, int
     int sms;
     const int rc = current_sm103(&sms);
     if (rc != MLA_OK) return rc;
-    mla_copy_pages_kernel<<<dim3(n, layers), 256, 0, static_cast<cudaStream_t>(stream)>>>(
-        static_cast<uint8_t*>(cache), layer_stride, num_pages, page_bytes, src, dst, status);
+    // Most entries of a long list are skipped (a compaction's): eight to a CTA then, so that the empty CTAs do not
+    // take longer than the copies; a short list is cut into pieces, so that few pages still fill the SMs.
+    const bool many = static_cast<int64_t>(n) * layers > 16 * sms;
+    const int per = many ? 8 : 1;
+    const int64_t step_bytes = kCopyStep * 16;
+    const int pieces = many ? 1 : static_cast<int>(std::min<int64_t>((page_bytes + step_bytes - 1) / step_bytes, 16));
+    mla_copy_pages_kernel<<<dim3((n + per - 1) / per, layers, pieces), kCopyThreads, 0,
+                            static_cast<cudaStream_t>(stream)>>>(static_cast<uint8_t*>(cache), layer_stride, num_pages,
+                                                                 page_bytes, src, dst, n, per, pieces, status);
     return launched("launch mla_copy_pages_kernel");
 }
 
