@@ -88,48 +88,38 @@ __device__ __forceinline__ bool seq_rows(const int32_t* cu, int s, int rows, int
     return x >= 0 && y >= x && y <= rows;
 }
 
-// The sequence and tile pair of index `t` in the order of the sequences (one
-// warp; -1: there are fewer).  `all`: look at every sequence for the status.
+// The t-th tile pair, counted from the last pair of the last sequence (the
+// last pairs of a causal sequence see the most keys: they start first).  One
+// warp; job[1] = 0: there are fewer.  `all`: look at every sequence.
 __device__ __forceinline__ void find_job(const PromptParams& p, int t, bool all, Shared* sh) {
     const int lane = threadIdx.x & 31;
-    int before = 0, found = 0, total = 0;
-    bool good = true;
-    if (all || p.B > 0) {
-        // tiles of all sequences: the heaviest (last) tiles come first
-        for (int pass = 0; pass < 2; ++pass) {
-            before = 0;
-            for (int s0 = 0; s0 < p.B; s0 += 32) {
-                const int s = s0 + lane;
-                int a = 0, n = 0, ka = 0, kn = 0;
-                if (s < p.B) {
-                    good &= seq_rows(p.cu_q, s, p.Tq, &a, &n);
-                    good &= seq_rows(p.cu_k, s, p.Tk, &ka, &kn);
-                }
-                const int tiles = (n + 2 * kTile - 1) / (2 * kTile);
-                int inc = tiles;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(~0u, inc, o);
-                    if (lane >= o) inc += y;
-                }
-                const int end = before + inc;
-                if (pass == 1 && t >= end - tiles && t < end) {
-                    sh->job[0] = a;
-                    sh->job[1] = n;
-                    sh->job[2] = ka;
-                    sh->job[3] = kn;
-                    sh->job[4] = (t - (end - tiles)) * 2 * kTile;
-                    found = 1;
-                }
-                before = __shfl_sync(~0u, end, 31);
-                if (pass == 1 && __any_sync(~0u, found)) break;
-            }
-            if (pass == 0) {
-                total = before;
-                t = total - 1 - t;
-                if (t < 0) break;
-            }
+    int before = 0;
+    bool good = true, found = false;
+    for (int s0 = p.B - 1; s0 >= 0; s0 -= 32) {
+        const int s = s0 - lane;
+        int a = 0, n = 0, ka = 0, kn = 0;
+        if (s >= 0) {
+            good &= seq_rows(p.cu_q, s, p.Tq, &a, &n);
+            good &= seq_rows(p.cu_k, s, p.Tk, &ka, &kn);
         }
+        const int tiles = (n + 2 * kTile - 1) / (2 * kTile);
+        int end = tiles;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(~0u, end, o);
+            if (lane >= o) end += y;
+        }
+        end += before;
+        if (t >= end - tiles && t < end) {
+            sh->job[0] = a;
+            sh->job[1] = n;
+            sh->job[2] = ka;
+            sh->job[3] = kn;
+            sh->job[4] = (end - 1 - t) * 2 * kTile;
+            found = true;
+        }
+        before = __shfl_sync(~0u, end, 31);
+        if (!all && before > t) break;
     }
     if (!__any_sync(~0u, found) && lane == 0) sh->job[1] = 0;
     if (all && !__all_sync(~0u, good) && lane == 0) raise_status(p.status, kStatusSeqRange);
@@ -209,10 +199,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         sh->abort_flag = 0;
         for (int i = 0; i < 12; ++i) sh->bad[i] = 0;
         fence_barrier_init();
+        if (!p.q8) prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
     }
-    __syncthreads();
-    const Job jb{sh->job[0], sh->job[1], sh->job[2], sh->job[3], sh->job[4]};
-    if (jb.nq == 0) return;
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(&sh->tmem), 512);
         tmem_relinquish();
@@ -221,6 +211,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
+    const Job jb{sh->job[0], sh->job[1], sh->job[2], sh->job[3], sh->job[4]};
+    if (jb.nq == 0) {
+        if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+        return;
+    }
 
     // Keys that row r of the sequence sees: [0, limit(r)).
     const int off = jb.nk - jb.nq;
@@ -251,22 +246,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float qs = mine ? p.q_scale[p.q_per_head ? at : jb.q0 + row] : 0.f;
             c *= fabsf(qs);  // a negative scale turns the codes' sign, so that c > 0 keeps the order of the scores
             if (c < 1e-30f) c = 1e-30f;  // a zero row: its scores are 0 (hidden ones stay -inf)
-            const uint32_t qt = sm_q + t * nqk * kSlotBytes + r * 128;
-            for (int d = 0; d < p.Dqk; d += 16) {
-                uint4 w = mine ? *reinterpret_cast<const uint4*>(p.q8 + at * p.Dqk + d) : make_uint4(0, 0, 0, 0);
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                uint32_t y[8];
+            // The warp's 32 rows of codes in pieces of 16, four pieces a lane at a time: neighbouring lanes read
+            // neighbouring pieces of a row.
+            const int8_t* rows8 = p.q8 + (at - static_cast<int64_t>(r & 31) * p.H) * p.Dqk;
+            const int pieces = p.Dqk / 16, wrow = (warp & 3) * 32, wrows = clampi(rows - wrow, 0, 32);
+            const uint32_t negative = __ballot_sync(~0u, qs < 0.f);
+            for (int i0 = 0; i0 < pieces * 32; i0 += 128) {
+                uint4 w[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const uint32_t two = x[i >> 1] >> ((i & 1) * 16);
-                    float a = static_cast<float>(static_cast<int8_t>(two)), b = static_cast<float>(static_cast<int8_t>(two >> 8));
-                    if (qs < 0.f) a = -a, b = -b;
-                    y[i] = pack_bf16x2(a, b);
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + k * 32 + lane, row = i / pieces, piece = i - row * pieces;
+                    w[k] = row < wrows ? *reinterpret_cast<const uint4*>(rows8 + static_cast<int64_t>(row) * p.H * p.Dqk + piece * 16)
+                                       : make_uint4(0, 0, 0, 0);
                 }
-                const uint32_t dst = qt + (d >> 6) * kSlotBytes;
-                const uint32_t j = (d & 63) >> 3;
-                st_shared_v4(dst + ((j ^ (r & 7)) << 4), y[0], y[1], y[2], y[3]);
-                st_shared_v4(dst + (((j + 1) ^ (r & 7)) << 4), y[4], y[5], y[6], y[7]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int i = i0 + k * 32 + lane, row = i / pieces, piece = i - row * pieces;
+                    if (i >= pieces * 32) continue;
+                    const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                    const bool turn = negative >> row & 1u;
+                    uint32_t y[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const uint32_t two = x[e >> 1] >> ((e & 1) * 16);
+                        float u = static_cast<float>(static_cast<int8_t>(two)), v = static_cast<float>(static_cast<int8_t>(two >> 8));
+                        if (turn) u = -u, v = -v;
+                        y[e] = pack_bf16x2(u, v);
+                    }
+                    const uint32_t dst = sm_q + (t * nqk + (piece >> 2)) * kSlotBytes + (wrow + row) * 128;
+                    const uint32_t c16 = (piece & 3) * 2;
+                    st_shared_v4(dst + ((c16 ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
+                    st_shared_v4(dst + (((c16 + 1) ^ (row & 7)) << 4), y[4], y[5], y[6], y[7]);
+                }
             }
             fence_proxy_async_shared();
             mbar_arrive(smem_u32(&sh->q_full[t]));
@@ -373,35 +384,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 12; ++i) any_bad |= *const_cast<volatile uint32_t*>(sh->bad + i);
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                // A warp's rows pass through its part of the tile's Q (no score is left to make), 64 columns at a
+                // time, so that it stores four rows' whole lines at once.
+                const uint32_t stage = sm_q + t * nqk * kSlotBytes + (warp & 3) * 32 * 128;
+                const int64_t row_bytes = static_cast<int64_t>(p.H) * p.Dv * 2;
+                uint8_t* rows_out = reinterpret_cast<uint8_t*>(p.out + (at - static_cast<int64_t>(lane) * p.H) * p.Dv);
+                const int wrows = clampi(rows - (warp & 3) * 32, 0, 32);
 #pragma unroll 1
-                for (int d = 0; d < p.Dv; d += 16) {
-                    float o[16];
-                    if (n) tmem_ld16(to + d, o);
+                for (int d = 0; d < p.Dv; d += 64) {
+                    float o[64];  // (what lies behind v_dim is not stored)
+                    if (n) {
+                        uint32_t raw_o[64];
+                        tmem_ld64_raw(to + d, raw_o);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = l == 0.f ? 0.f : o[i] * inv;
+                        for (int i = 0; i < 64; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(raw_o[i]) * inv;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 64; ++i) o[i] = 0.f;
+                    }
                     if (any_bad) {
                         for (int w = 0; w < 12; ++w)
                             for (uint32_t bits = *const_cast<volatile uint32_t*>(sh->bad + w); bits; bits &= bits - 1) {
                                 const int key = (first_masked + w / 4) * kTile + (w & 3) * 32 + __ffs(bits) - 1;
                                 if (key >= lim) continue;
                                 const uint16_t* v = p.v + ((static_cast<int64_t>(jb.k0) + key) * p.Hk + hk) * p.Dv + d;
-#pragma unroll 1
-                                for (int i = 0; i < 16; ++i)
-                                    if ((v[i] & 0x7F80) == 0x7F80) {
-                                        const float x = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
 #pragma unroll
-                                        for (int k = 0; k < 16; ++k)
-                                            if (k == i) o[k] += x;
-                                    }
+                                for (int i = 0; i < 64; ++i)
+                                    if (d + i < p.Dv && (v[i] & 0x7F80) == 0x7F80)
+                                        o[i] += __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
                             }
                     }
-                    if (mine) {
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + at * p.Dv + d);
-                        dst[0] = make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]), pack_bf16x2(o[4], o[5]),
-                                            pack_bf16x2(o[6], o[7]));
-                        dst[1] = make_uint4(pack_bf16x2(o[8], o[9]), pack_bf16x2(o[10], o[11]),
-                                            pack_bf16x2(o[12], o[13]), pack_bf16x2(o[14], o[15]));
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_shared_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                                     pack_bf16x2(o[8 * i + 2], o[8 * i + 3]), pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                                     pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int row2 = i * 4 + (lane >> 3), col = d + (lane & 7) * 8;
+                        uint4 v;
+                        ld_shared_v4(stage + row2 * 128 + (((lane & 7) ^ (row2 & 7)) << 4), v.x, v.y, v.z, v.w);
+                        if (row2 < wrows && col < p.Dv) *reinterpret_cast<uint4*>(rows_out + row2 * row_bytes + col * 2) = v;
                     }
+                    __syncwarp();
                 }
                 if (mine && p.lse) p.lse[at] = l == 0.f ? -INFINITY : ms * kLn2 + logf(l);
             }
