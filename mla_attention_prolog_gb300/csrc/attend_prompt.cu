@@ -125,6 +125,17 @@ __device__ __forceinline__ void find_job(const PromptParams& p, int t, bool all,
     if (all && !__all_sync(~0u, good) && lane == 0) raise_status(p.status, kStatusSeqRange);
 }
 
+// Two INT8 codes (bytes of `four`, named by the byte selector 0x4b4a) as BF16:
+// with the low seven bits of a code as the fraction of 128 and its sign bit
+// turning 128 into 256, code = (128 + low) - (128 or 256) exactly.
+__device__ __forceinline__ uint32_t codes_bf16x2(uint32_t four, uint32_t selector) {
+    const uint32_t two = __byte_perm(four, 0, selector);
+    const uint32_t a = (two & 0x007F007Fu) | 0x43004300u, b = (two & 0x00800080u) | 0x43004300u;
+    uint32_t r;
+    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Zeroes what no row may multiply: v rows behind the sequence's end, and NaN
 // or infinite elements of v (in tiles where the mask hides keys from some
 // rows); their keys are noted, and the rows that do see them add them in the
@@ -246,37 +257,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float qs = mine ? p.q_scale[p.q_per_head ? at : jb.q0 + row] : 0.f;
             c *= fabsf(qs);  // a negative scale turns the codes' sign, so that c > 0 keeps the order of the scores
             if (c < 1e-30f) c = 1e-30f;  // a zero row: its scores are 0 (hidden ones stay -inf)
-            // The warp's 32 rows of codes in pieces of 16, four pieces a lane at a time: neighbouring lanes read
-            // neighbouring pieces of a row.
+            // The warp's 32 rows of codes in pieces of 16, a lane's pieces 32 apart: neighbouring lanes read
+            // neighbouring pieces of a row.  Up to 12 loads (Dqk = 192) are in flight.
             const int8_t* rows8 = p.q8 + (at - static_cast<int64_t>(r & 31) * p.H) * p.Dqk;
+            const int64_t row_pitch = static_cast<int64_t>(p.H) * p.Dqk;
             const int pieces = p.Dqk / 16, wrow = (warp & 3) * 32, wrows = clampi(rows - wrow, 0, 32);
+            const int row_step = 32 / pieces, piece_step = 32 % pieces;
             const uint32_t negative = __ballot_sync(~0u, qs < 0.f);
-            for (int i0 = 0; i0 < pieces * 32; i0 += 128) {
-                uint4 w[4];
+            int row0 = lane / pieces, piece0 = lane % pieces;  // of this lane's next load
+            int row1 = row0, piece1 = piece0;                  // of its next store
+            auto advance = [&](int& row, int& piece) {
+                row += row_step;
+                piece += piece_step;
+                if (piece >= pieces) piece -= pieces, ++row;
+            };
+#pragma unroll 1
+            for (int k0 = 0; k0 < pieces; k0 += 12) {
+                uint4 w[12];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = i0 + k * 32 + lane, row = i / pieces, piece = i - row * pieces;
-                    w[k] = row < wrows ? *reinterpret_cast<const uint4*>(rows8 + static_cast<int64_t>(row) * p.H * p.Dqk + piece * 16)
-                                       : make_uint4(0, 0, 0, 0);
+                for (int k = 0; k < 12; ++k) {
+                    w[k] = k0 + k < pieces && row0 < wrows
+                               ? *reinterpret_cast<const uint4*>(rows8 + row0 * row_pitch + piece0 * 16)
+                               : make_uint4(0, 0, 0, 0);
+                    advance(row0, piece0);
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int i = i0 + k * 32 + lane, row = i / pieces, piece = i - row * pieces;
-                    if (i >= pieces * 32) continue;
-                    const uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-                    const bool turn = negative >> row & 1u;
-                    uint32_t y[8];
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const uint32_t two = x[e >> 1] >> ((e & 1) * 16);
-                        float u = static_cast<float>(static_cast<int8_t>(two)), v = static_cast<float>(static_cast<int8_t>(two >> 8));
-                        if (turn) u = -u, v = -v;
-                        y[e] = pack_bf16x2(u, v);
-                    }
-                    const uint32_t dst = sm_q + (t * nqk + (piece >> 2)) * kSlotBytes + (wrow + row) * 128;
-                    const uint32_t c16 = (piece & 3) * 2;
-                    st_shared_v4(dst + ((c16 ^ (row & 7)) << 4), y[0], y[1], y[2], y[3]);
-                    st_shared_v4(dst + (((c16 + 1) ^ (row & 7)) << 4), y[4], y[5], y[6], y[7]);
+                for (int k = 0; k < 12; ++k) {
+                    if (k0 + k >= pieces) break;
+                    const uint32_t turn = (negative >> row1 & 1u) ? 0x80008000u : 0u;
+                    const uint32_t dst = sm_q + (t * nqk + (piece1 >> 2)) * kSlotBytes + (wrow + row1) * 128;
+                    const uint32_t c16 = (piece1 & 3) * 2;
+                    st_shared_v4(dst + ((c16 ^ (row1 & 7)) << 4), codes_bf16x2(w[k].x, 0x4140) ^ turn,
+                                 codes_bf16x2(w[k].x, 0x4342) ^ turn, codes_bf16x2(w[k].y, 0x4140) ^ turn,
+                                 codes_bf16x2(w[k].y, 0x4342) ^ turn);
+                    st_shared_v4(dst + (((c16 + 1) ^ (row1 & 7)) << 4), codes_bf16x2(w[k].z, 0x4140) ^ turn,
+                                 codes_bf16x2(w[k].z, 0x4342) ^ turn, codes_bf16x2(w[k].w, 0x4140) ^ turn,
+                                 codes_bf16x2(w[k].w, 0x4342) ^ turn);
+                    advance(row1, piece1);
                 }
             }
             fence_proxy_async_shared();
