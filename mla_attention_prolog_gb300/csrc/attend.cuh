@@ -1,6 +1,7 @@
 // What the entry points of the attention and page operators share.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -29,6 +30,20 @@ inline int current_sm103(int* sms) {
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return report_cuda(e, "device query");
     return major == 10 && minor == 3 ? MLA_OK : MLA_ERR_DEVICE;
+}
+
+// Lets `kernel` use `bytes` of dynamic shared memory on the current device;
+// `ready` (one bit per device) remembers for which that was done.
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes, std::atomic<uint64_t>* ready) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+    if (ready->load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) ready->fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 inline bool encode_bf16_dims(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[3],

@@ -227,7 +227,13 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* scratch, int64
 // workspace for the join.  False: the unit has no run.
 __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared* sh, Walk* w) {
     const bool writer = blockIdx.x == 0;
-    int bits = 0, row;
+    int bits = 0, row, first_row = -1;
+    // this thread's row of the first kThreads: read once, beside the shared length
+    const int first_len = threadIdx.x < p.B ? batch_len(p, threadIdx.x, &first_row, &bits) : 0;
+    auto len_of = [&](int b) {
+        if (b == static_cast<int>(threadIdx.x)) return first_len;
+        return b < p.B ? batch_len(p, b, &row, &bits) : 0;
+    };
     // who shares the prefix
     int shared = p.shared_len ? *p.shared_len : 0;
     const int cap = p.max_pages * p.page_size;
@@ -237,7 +243,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
     if (shared > 0) {
         int count = 0, first = p.B;
         for (int b = threadIdx.x; b < p.B; b += kThreads)
-            if (batch_len(p, b, &row, &bits) >= shared) ++count, first = min(first, b);
+            if (len_of(b) >= shared) ++count, first = min(first, b);
         if (count) {
             atomicAdd(&sh->sharers, count);
             atomicMin(&sh->source, first);
@@ -250,7 +256,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
     int64_t total = prefix, sum;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
-        const int len = b < p.B ? batch_len(p, b, &row, &bits) : 0;
+        const int len = len_of(b);
         const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
         const int64_t before = total + block_scan(mine, sh->scan, &sum);
         if (writer && b < p.B) p.bases[b] = before;
@@ -276,7 +282,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
     if (w->at >= prefix) {  // the batch row that holds `at`
         if (p.B <= kThreads) {
             const int b = threadIdx.x;
-            const int len = b < p.B ? batch_len(p, b, &row, &bits) : 0;
+            const int len = len_of(b);
             const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
             const int64_t before = prefix + block_scan(mine, sh->scan, &sum);
             if (mine && w->at >= before && w->at < before + mine) sh->first_b = b, sh->first_base = before;
@@ -284,7 +290,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
             int64_t base = prefix;
             for (int b0 = 0; b0 < p.B; b0 += kThreads) {
                 const int b = b0 + threadIdx.x;
-                const int len = b < p.B ? batch_len(p, b, &row, &bits) : 0;
+                const int len = len_of(b);
                 const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
                 const int64_t before = base + block_scan(mine, sh->scan, &sum);
                 if (mine && w->at >= before && w->at < before + mine) sh->first_b = b, sh->first_base = before;
@@ -784,6 +790,7 @@ __global__ void __launch_bounds__(128) mla_attend_join_kernel(const CacheParams 
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     if (row >= static_cast<int64_t>(p.B) * p.H) return;
+    pdl_wait();
     const Cut cut = *p.cut;
     const int b = static_cast<int>(row / p.H), h = static_cast<int>(row % p.H);
     int trow, bits = 0;
@@ -933,13 +940,22 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
                   static_cast<int>(rows ? rows : 1), static_cast<int>(d->num_pages), box, y.row_tiles, y.head_tiles,
                   y.halves, y.units, d->scale};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaFuncSetAttribute(mla_attend_cache_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_smem(&mla_attend_cache_kernel, kSmem, &ready);
     if (e != cudaSuccess) return report_cuda(e, "mla_attend_cache_kernel attributes");
     mla_attend_cache_kernel<<<y.units * y.halves, kThreads, kSmem, st>>>(tm, tm4, tm2, p);
     if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
     const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
-    mla_attend_join_kernel<<<static_cast<unsigned>(blocks), 128, 0, st>>>(p);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, mla_attend_join_kernel, p);
     return e == cudaSuccess ? MLA_OK : report_cuda(e, "launch mla_attend_join_kernel");
 }
 

@@ -657,7 +657,8 @@ extern "C" int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* d, const v
                    static_cast<uint16_t*>(out), lse, status, d->Tq, d->Tk, d->sequences, d->num_heads, d->kv_heads,
                    d->qk_dim, d->v_dim, d->scale, (d->flags & MLA_PROMPT_CAUSAL) != 0, per_head, slots,
                    static_cast<int>(tiles), static_cast<int>(group)};
-    cudaError_t e = cudaFuncSetAttribute(mla_attend_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = allow_smem(&mla_attend_prompt_kernel, kSmemMax, &ready);
     if (e != cudaSuccess) return report_cuda(e, "mla_attend_prompt_kernel attributes");
     mla_attend_prompt_kernel<<<static_cast<unsigned>(tiles * d->num_heads), kThreads, smem,
                                static_cast<cudaStream_t>(stream)>>>(tq, tk, tv, p);
