@@ -713,9 +713,9 @@ typedef struct mla_prolog_pool {
  * of the entries up to it (those that fit the columns) sum to more than the
  * free pages.
  * A sequence listed twice, or outside [0, sequences), or a negative count, is
- * left out with MLA_STATUS_SEQ_RANGE (the first listing counts).  Tokens
+ * left out with MLA_STATUS_SEQ_RANGE (the first listing counts).
+ * slot_mapping and positions may each be NULL; where one is given, tokens
  * beyond `total` get a page but no slot, and set MLA_STATUS_SLOT_RANGE.
- * slot_mapping and positions may each be NULL.
  */
 int mla_prolog_pages_extend(const mla_prolog_pool* pool, const int32_t* seqs, const int32_t* counts, int32_t n,
                             int32_t* slot_mapping, int32_t* positions, int32_t total, void* stream);

@@ -421,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!ok) break;
                 tc_fence_after();
                 uint32_t s[kKeys];
-                tmem_ld64_raw(tmem + lanes + kColS, s);
+                float mt = tmem_ld64_max(tmem + lanes + kColS, s);  // of the row
                 tc_fence_before();
                 mbar_arrive(smem_u32(&sh->s_free));
                 const int left = now.end - now.key0 - j * kKeys;
@@ -429,14 +429,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < kKeys; ++i)
                         if (i >= left) s[i] = 0xFF800000u;
+                    mt = -INFINITY;
+#pragma unroll
+                    for (int i = 0; i < kKeys; ++i) mt = fmaxf(mt, __uint_as_float(s[i]));
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < kKeys; i += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[i + k])), __uint_as_float(s[i + 4 + k]));
-                const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool grow = mt > m && (m == -INFINITY || mt * c > ms + kSlack);
                 float alpha = 1.f;
                 if (__any_sync(~0u, grow)) {

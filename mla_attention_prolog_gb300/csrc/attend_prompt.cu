@@ -211,8 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 12; ++i) sh->bad[i] = 0;
         fence_barrier_init();
         if (!p.q8) prefetch_tensormap(&tm_q);
-        prefetch_tensormap(&tm_k);
-        prefetch_tensormap(&tm_v);
+        if (p.Tk) prefetch_tensormap(&tm_k), prefetch_tensormap(&tm_v);
     }
     if (warp == kMmaWarp) {
         tmem_alloc(smem_u32(&sh->tmem), 512);
@@ -310,21 +309,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             tc_fence_after();
             uint32_t s[kTile];
-            tmem_ld128_raw(ts, s);
+            float mt = tmem_ld128_max(ts, s);  // of the row
             const bool masked = (j + 1) * kTile > lim0;
             if (masked) {
                 const int left = lim - j * kTile;
 #pragma unroll
                 for (int i = 0; i < kTile; ++i)
                     if (i >= left) s[i] = 0xFF800000u;
+                mt = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < kTile; ++i) mt = fmaxf(mt, __uint_as_float(s[i]));
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int i = 0; i < kTile; i += 8)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mx[k] = fmaxf(fmaxf(mx[k], __uint_as_float(s[i + k])), __uint_as_float(s[i + 4 + k]));
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
             // rows that have no maximum yet take this tile's; the others only one that has grown by the slack
             const bool grow = mt > m && (m == -INFINITY || mt * c > ms + kSlack);
             if (__any_sync(~0u, grow)) {

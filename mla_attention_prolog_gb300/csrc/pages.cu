@@ -239,8 +239,8 @@ __global__ void __launch_bounds__(kThreads) mla_pages_extend_kernel(Pool p, cons
             p.refs[page] = 1;
         });
     __syncthreads();
-    if (tokens > total) bits |= kStatusSlotRange;
     if (slots || positions) {
+        if (tokens > total) bits |= kStatusSlotRange;
         for (int j = t; j < total; j += kThreads) {
             int slot = -1, pos = 0;
             if (j < tokens) {

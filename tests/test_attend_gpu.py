@@ -358,6 +358,69 @@ def test_cache_behind_32_bit_offsets():
     check_cache(c, out, lse)
 
 
+@pytest.mark.parametrize("shared", [0, 192])
+def test_cache_large_batch(shared):
+    """More sequences than a CTA has threads, some empty, some shorter than the prefix."""
+    g = torch.Generator().manual_seed(11)
+    own = torch.randint(0, 150, (450,), generator=g).tolist()
+    lens = [shared + n if i % 7 else n for i, n in enumerate(own)]
+    lens[0] = shared + 1
+    c = cache_case(11, lens, 4, 512, 64, 64, shared)
+    out, lse, status = run_cache(c)
+    assert status == 0
+    check_cache(c, out, lse)
+
+
+def test_cache_shared_prefix_seen_first_by_a_later_row():
+    """The first sequence is shorter than the prefix; one sequence alone shares nothing."""
+    c = cache_case(12, [500, 10, 470, 0], 16, 512, 64, 64, 448)
+    for rows in ([1, 0, 2], [1, 3, 0], [3, 1, 1]):
+        seqs = torch.tensor(rows, dtype=torch.int32, device=DEV)
+        d = {**c, "q": c["q"][:3].contiguous()}
+        out, lse, status = run_cache(d, seqs=seqs)
+        assert status == 0
+        check_cache(d, out, lse, rows)
+
+
+def test_cache_without_pages():
+    c = cache_case(13, [0, 0, 0], 16, 512, 64, 64, spare=0)
+    assert c["cache"].shape[0] == 0
+    out, lse, status = run_cache(c)
+    assert status == 0 and (out == 0).all() and torch.isneginf(lse).all()
+    c["lens"][1] = 70   # and no page to hold them: rows of zeros
+    c["table"] = torch.zeros((3, 2), dtype=torch.int32, device=DEV)
+    out, lse, status = run_cache(c)
+    assert status == binding.STATUS_PAGE_RANGE and (out == 0).all()
+    assert (lse[1] - math.log(70)).abs().max() <= 1e-5
+
+
+def test_cache_refuses_a_small_workspace():
+    c = cache_case(14, [100, 40], 16, 512, 64, 64)
+    n = binding.attend_cache_workspace_bytes(2, 16, 512, 64)
+    out, lse = torch.zeros((2, 16, 512), dtype=torch.bfloat16, device=DEV), torch.zeros((2, 16), device=DEV)
+    for ws in (torch.empty(n - 1, dtype=torch.uint8, device=DEV), torch.empty(n + 8, dtype=torch.uint8, device=DEV)[8:]):
+        with pytest.raises(binding.MlaPrologError):
+            binding.attend_cache(c["q"], c["cache"], c["table"], c["lens"], out, lse, ws, scale=1.0)
+
+
+def test_binding_refusals():
+    """Shapes, types and layouts that do not belong together, before any launch."""
+    c = prompt_case(15, [20], [20], 2, 2, 64, 64, pad=0)
+    out = torch.zeros((20, 2, 64), dtype=torch.bfloat16, device=DEV)
+    call = lambda **kw: binding.attend_prompt(*{**dict(q=c["q"], k=c["k"], v=c["v"], cu_q=c["cu_q"], cu_k=c["cu_k"],  # noqa: E731
+                                                        out=out), **kw}.values(), scale=1.0)
+    call()
+    for kw, err in ((dict(q=c["q"].float()), TypeError), (dict(k=c["k"][:, :, :32]), ValueError), (dict(cu_k=c["cu_k"][:1]), ValueError),
+                    (dict(cu_q=c["cu_q"].long()), TypeError), (dict(v=c["v"].transpose(0, 1)), ValueError),
+                    (dict(out=out.transpose(0, 1)), ValueError), (dict(q=c["q"].cpu()), TypeError),
+                    (dict(k=c["k"].cpu()), TypeError)):
+        with pytest.raises(err):
+            call(**kw)
+    with pytest.raises(binding.MlaPrologError):   # 16-byte alignment
+        flat = torch.zeros(20 * 2 * 64 + 4, dtype=torch.bfloat16, device=DEV)
+        call(out=flat[4:].view(20, 2, 64))
+
+
 def test_cache_two_graphs_with_their_own_workspaces():
     """Two captured calls replayed at once on two streams, then again with
     other lengths."""

@@ -203,6 +203,30 @@ def test_extend_refusals_leave_the_rest():
     assert x.m.status & SLOT
 
 
+def test_extend_without_buffers():
+    """Growing sequences needs neither slots nor positions."""
+    x = Pair(3, 4, 9, 16)
+    x.pool.extend(i32(0, 2), i32(20, 3))
+    x.m.extend([0, 2], [20, 3], 23)
+    x.same()
+    positions = i32(*[9] * 7)
+    x.pool.extend(i32(2), i32(7), positions=positions)
+    assert positions.tolist() == x.m.extend([2], [7], 7)[1]
+    x.same()
+
+
+def test_lists_of_any_length():
+    """As many entries as a call takes, and repeats far apart."""
+    r = random.Random(9)
+    x = Pair(1200, 3, 2500, 16)
+    seqs = r.sample(range(1200), 1023)
+    x.extend(seqs + [seqs[5]], [r.randint(0, 20) for _ in range(1024)])
+    empty = [s for s in range(1200) if x.m.lens[s] == 0]
+    x.fork([r.randrange(1200) for _ in empty], empty)
+    x.release(seqs[:600] + seqs[:424])
+    x.compact()
+
+
 def test_fork_refusals_leave_the_rest():
     x = Pair(8, 4, 10, 16)
     x.extend([0, 1], [40, 32])
