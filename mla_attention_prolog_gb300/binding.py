@@ -373,11 +373,11 @@ def lpt(cost: Sequence[int], groups: int):
 
 def _on(t: torch.Tensor, name: str, dims: int) -> torch.device:
     """The device that the other tensors of a call have to be on."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == dims:
+        return t.device
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != dims:
-        raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
-    return t.device
+    raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
 
 
 def _stream_on(device, stream: Optional[torch.cuda.Stream]) -> Optional[int]:
@@ -390,8 +390,8 @@ def _stream_on(device, stream: Optional[torch.cuda.Stream]) -> Optional[int]:
 
 def _run(name: str, device, *args) -> None:
     """Calls an entry point with `device` as the current one."""
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() == device.index:
+    f = getattr(_lib or lib(), name)
+    if torch._C._cuda_getDevice() == device.index:
         rc = f(*args)
     else:
         with torch.cuda.device(device):
@@ -407,8 +407,8 @@ def attend_prompt(q, k, v, cu_q, cu_k, out, lse=None, *, scale: float, causal: b
     ``q_scale`` [Tq] or [Tq, H]; k [Tk, Hk, Dqk], v [Tk, Hk, Dv]; cu_q, cu_k
     int32 [sequences + 1]; out BF16 [Tq, H, Dv], lse FP32 [Tq, H]."""
     dev = _on(q, "q", 3)
-    (Tq, H, Dqk), _, _ = q.shape, _on(k, "k", 3), _on(v, "v", 3)
-    Tk, Hk, Dv, n = k.shape[0], k.shape[1], v.shape[2], cu_q.numel() - 1
+    _on(k, "k", 3), _on(v, "v", 3)
+    (Tq, H, Dqk), (Tk, Hk, _), Dv, n = q.shape, k.shape, v.shape[2], cu_q.numel() - 1
     if n < 0:
         raise ValueError("cu_q must have at least one entry")
     bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
@@ -445,9 +445,8 @@ def attend_cache(q, kv_cache, page_table, seq_lens, out, lse, workspace, *, scal
     out BF16 [B, H, Lkv]; lse FP32 [B, H] or None; workspace uint8 of at least
     ``attend_cache_workspace_bytes``."""
     dev = _on(q, "q", 3)
-    (B, H, C), _, _ = q.shape, _on(kv_cache, "kv_cache", 3), _on(page_table, "page_table", 2)
-    _on(out, "out", 3), _on(workspace, "workspace", 1)
-    pages, page_size, Lkv, (S, width) = kv_cache.shape[0], kv_cache.shape[1], out.shape[2], page_table.shape
+    _on(kv_cache, "kv_cache", 3), _on(page_table, "page_table", 2), _on(out, "out", 3), _on(workspace, "workspace", 1)
+    (B, H, C), (pages, page_size, _), Lkv, (S, width) = q.shape, kv_cache.shape, out.shape[2], page_table.shape
     bf, i32 = torch.bfloat16, torch.int32
     d = MlaPrologCacheDims(B, H, Lkv, C - Lkv, page_size, S, width, scale, pages)
     args = [_ptr(q, "q", bf, (B, H, C), dev), _ptr(kv_cache, "kv_cache", bf, (pages, page_size, C), dev),
@@ -474,18 +473,20 @@ class PagePool:
                                    _ptr(refs, "refs", i32, (refs.numel(),), self.device),
                                    _ptr(status, "status", i32, (1,), self.device))
 
+        self._ref = ctypes.byref(self._pool)
+
     def _list(self, t, name, n):
         return _ptr(t, name, torch.int32, (n,), self.device)
 
     def _call(self, name, *args, stream):
-        _run(name, self.device, ctypes.byref(self._pool), *args, _stream_on(self.device, stream))
+        _run(name, self.device, self._ref, *args, _stream_on(self.device, stream))
 
     def extend(self, seqs, counts, slot_mapping=None, positions=None, stream=None) -> None:
         """Grows sequence seqs[i] by counts[i] tokens; slot_mapping and
         positions (int32 [total], as ``run_cached`` takes them) receive the new
         tokens' slots and places."""
         n = seqs.numel()
-        total = next((t.numel() for t in (slot_mapping, positions) if t is not None), 0)
+        total = slot_mapping.numel() if slot_mapping is not None else positions.numel() if positions is not None else 0
         self._call("mla_prolog_pages_extend", self._list(seqs, "seqs", n), self._list(counts, "counts", n), n,
                    self._list(slot_mapping, "slot_mapping", total), self._list(positions, "positions", total), total,
                    stream=stream)
@@ -494,9 +495,8 @@ class PagePool:
         """Makes children[i] a copy of parents[i]; (copy_src[i], copy_dst[i]) is
         the page that ``copy_pages`` has to copy in every cache (-1: none)."""
         n = parents.numel()
-        self._call("mla_prolog_pages_fork", *(self._list(t, name, n) for t, name in (
-            (parents, "parents"), (children, "children"))), n, self._list(copy_src, "copy_src", n),
-            self._list(copy_dst, "copy_dst", n), stream=stream)
+        self._call("mla_prolog_pages_fork", self._list(parents, "parents", n), self._list(children, "children", n), n,
+                   self._list(copy_src, "copy_src", n), self._list(copy_dst, "copy_dst", n), stream=stream)
 
     def release(self, seqs, stream=None) -> None:
         """Ends sequences: their pages lose a reference each."""
@@ -514,11 +514,12 @@ def copy_pages(cache, src, dst, status=None, stream=None) -> None:
     """Copies page src[i] to dst[i] (src None: page i; negative: skipped) in
     every layer of a BF16 cache [layers, num_pages, page_size, Lkv + R], or in
     one of [num_pages, page_size, Lkv + R]."""
-    dev = _on(cache, "cache", 3 if isinstance(cache, torch.Tensor) and cache.dim() == 3 else 4)
-    shape = tuple(cache.shape) if cache.dim() == 4 else (1,) + tuple(cache.shape)
+    one = isinstance(cache, torch.Tensor) and cache.dim() == 3
+    dev = _on(cache, "cache", 3 if one else 4)
+    shape = (1, *cache.shape) if one else cache.shape
     page_bytes = shape[2] * shape[3] * 2
     n = dst.numel()
-    args = [_ptr(cache, "cache", torch.bfloat16, tuple(cache.shape), dev), shape[0], shape[1] * page_bytes, shape[1],
+    args = [_ptr(cache, "cache", torch.bfloat16, cache.shape, dev), shape[0], shape[1] * page_bytes, shape[1],
             page_bytes, _ptr(src, "src", torch.int32, (n,), dev), _ptr(dst, "dst", torch.int32, (n,), dev), n,
             _ptr(status, "status", torch.int32, (1,), dev)]
     _run("mla_prolog_copy_pages", dev, *args, _stream_on(dev, stream))
