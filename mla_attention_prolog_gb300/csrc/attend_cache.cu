@@ -8,18 +8,19 @@
 //
 //   S = Q K^T   128 x 64 keys, 576 deep     O += P V   128 x Lkv, 64 deep
 //
-// O of 128 rows x 512 columns in FP32 would fill TMEM alone, so two CTAs share
-// a tile: each makes all of S and half of the columns of O (256 TMEM columns).
-// Doing S twice costs 1.5 times the products of a perfect split; halving the
-// rows instead would cost twice the key traffic into each SM for the same
-// products, and exchanging S or P between the CTAs a round trip per key tile.
-// Two thirds of Q stay in TMEM as well (192 columns, read as the A operand),
-// S takes the last 64; the rest of Q, two key tiles and P fill shared memory.
+// O of 128 rows x 512 columns in FP32 would fill the TMEM of an SM alone, so
+// a pair of CTAs works on a tile (cta_group::2, M = 128): each holds 64 of its
+// rows, and the tensor core spreads their columns over both halves of the
+// lanes, so that O takes 256 columns and S 32.  Each CTA brings half of the
+// operands that both multiply: for S half of the keys (all columns), for P V
+// half of the value columns (all keys).  A lane's row is shared by two
+// threads, 64 lanes apart, one for each half of the keys and of the value
+// columns.
 //
-// The work is cut into as many equal runs of key tiles as there are CTA pairs
-// (a tile costs its key tiles plus kOverhead for its start and end); a run
-// takes whole or partial tiles.  Partial results go to the workspace in FP32,
-// and a second kernel joins them.
+// The work is cut into as many equal runs of key steps as there are CTA pairs
+// (a tile costs its steps plus kOverhead for its start and end); a run takes
+// whole or partial tiles.  Partial results go to the workspace in FP32, and a
+// second kernel joins them.
 #include <cmath>
 #include <cstdint>
 
@@ -29,24 +30,24 @@
 namespace mlap {
 namespace {
 
-constexpr int kRows = 128;                // query rows per tile
+constexpr int kRows = 128;                // query rows per tile (64 per CTA)
 constexpr int kKeys = 64;                 // keys per step
-constexpr int kSlotBytes = kKeys * 128;   // 64 keys x 64 BF16 columns
-constexpr int kQBytes = kRows * 128;      // 128 rows x 64 BF16 columns
 constexpr int kMaxChunks = 9;             // 64-column chunks of a cache row
-constexpr int kGroup = 4;                 // value chunks of a CTA (its columns of O)
-constexpr int kOthers = kMaxChunks - kGroup;  // the chunks that only S needs, two steps of them in the ring
-constexpr int kPairs = 5;                 // pairs of value chunks in the ring: two and a half steps
-constexpr int kTmemChunks = 6;            // chunks of Q kept in TMEM
-constexpr int kHalf = 256;                // columns of O per CTA
+constexpr int kMaxValues = 4;             // 64-column chunks of a CTA's value columns
+constexpr int kQBytes = 64 * 128;         // a chunk of this CTA's rows of Q,
+constexpr int kKBytes = 32 * 128;         //   of its half of a step's keys,
+constexpr int kVBytes = kKeys * 128;      //   of its value columns of a step
+constexpr int kPBytes = 64 * 128;
+constexpr int kStageBytes = 4 * 32 * 128;  // where results pass through on their way out, and P of two steps
+static_assert(2 * kPBytes <= kStageBytes, "");
 constexpr int kThreads = 192;
 constexpr int kMmaWarp = 4, kLoadWarp = 5;
-constexpr int kMiscBytes = 1024;
-constexpr int kSmemQ = (kMaxChunks - kTmemChunks) * kQBytes, kSmemX = 2 * kOthers * kSlotBytes;
-constexpr int kSmemY = 2 * kPairs * kSlotBytes;
-constexpr int kSmem = 1024 + kMiscBytes + kSmemQ + kQBytes + kSmemX + kSmemY;
+constexpr int kMiscBytes = 1536;
+constexpr int kSmemQ = kMaxChunks * kQBytes, kSmemK = 2 * kMaxChunks * kKBytes, kSmemV = 2 * kMaxValues * kVBytes;
+constexpr int kSmem = 1024 + kMiscBytes + kSmemQ + kSmemK + kSmemV + kStageBytes;
 static_assert(kSmem <= 232448, "227 KB");
-constexpr uint32_t kColO = 0, kColQ = 256, kColS = 448;
+constexpr int kAhead = 4;                 // S of so many steps in TMEM
+constexpr uint32_t kColO = 0, kColS = 256;
 constexpr uint64_t kTimeoutNs = 1000000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;             // log2 of the largest P
@@ -79,7 +80,8 @@ struct CacheParams {
     float* part_o;      //   partial results [part rows][Lkv]
     float* part_lse;    //   and their log2-sum-exp [part rows]
     int B, H, Lkv, C, page_size, table_rows, max_pages, num_rows, num_pages, box;
-    int row_tiles, head_tiles, halves, units;
+    int row_tiles, head_tiles, units;
+    int dv_half;  // value columns of a CTA
     float scale;
 };
 
@@ -190,10 +192,12 @@ struct Walk {
 };
 
 struct Shared {
-    uint64_t x_full[2], x_empty[2], y_full[kPairs], y_empty[kPairs];  // other chunks by step, value chunks by pair
-    uint64_t q_full, s_full, s_free, p_full, pv_done, drain;
+    // full and free: K and V of step i at i % 2, Q of a piece; the even CTA's count for both
+    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full, q_free;
+    uint64_t s_full[kAhead], s_read[kAhead], p_full[2], pv_done[2], v_seen, drain;
     uint32_t tmem;
     int abort_flag;
+    float row_max[kRows], row_sum[kRows];  // what the two threads of a row tell each other
     int64_t scan[kThreads / 32];
     int64_t total, first_base;
     int first_b, sharers, source, shared;
@@ -307,49 +311,50 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_c, const __grid_constant__ CUtensorMap tm_4,
-                            const __grid_constant__ CUtensorMap tm_2, const CacheParams p) {
+    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
+                            const __grid_constant__ CUtensorMap tm_k4, const __grid_constant__ CUtensorMap tm_v4,
+                            const CacheParams p) {
     extern __shared__ uint8_t raw[];
     const uint32_t raw_at = smem_u32(raw);
-    const uint32_t pad = (1024u - (raw_at & 1023u)) & 1023u;
+    const uint32_t pad = (1024u - (raw_at & 1023u)) & 1023u;  // the same in both CTAs of a pair
     const int chunks = (p.C + 63) / 64;
-    const uint32_t sm_q = raw_at + pad, sm_p = sm_q + kSmemQ, sm_x = sm_p + kQBytes, sm_y = sm_x + kSmemX;
-    Shared* sh = reinterpret_cast<Shared*>(raw + pad + kSmemQ + kQBytes + kSmemX + kSmemY);
+    const uint32_t sm_q = raw_at + pad, sm_k = sm_q + kSmemQ, sm_v = sm_k + kSmemK, sm_p = sm_v + kSmemV;
+    Shared* sh = reinterpret_cast<Shared*>(raw + pad + kSmemQ + kSmemK + kSmemV + kStageBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int unit = blockIdx.x / p.halves, half = blockIdx.x % p.halves;
-    // This CTA's columns of O lie in value chunks 4 half .. + 3 of a cache row; the others only go into S.
-    const int dv0 = half * kHalf, dv = min(kHalf, p.Lkv - dv0);
-    const int v0 = half * kGroup, nvc = min(kGroup, chunks - v0), nx = chunks - nvc, pairs = (nvc + 1) / 2;
-    auto other = [&](int i) { return i < v0 ? i : i + nvc; };  // chunk of ring place i
-    // Place of a chunk of Q: 0-5 in TMEM, the value chunks first, 6-8 in shared memory.
-    auto q_place = [&](int ck) { return ck >= 2 * kGroup ? ck : (ck ^ v0); };
+    const int unit = blockIdx.x / 2, rank = blockIdx.x % 2;
+    const int v0 = rank * p.dv_half, nvc = (p.dv_half + 63) / 64;  // value columns that this CTA brings
 
     Walk walk;
     if (!make_cut(p, unit, sh, &walk)) return;
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&sh->x_full[i]), 1);
-            mbar_init(smem_u32(&sh->x_empty[i]), 1);
+            mbar_init(smem_u32(&sh->k_full[i]), 1);
+            mbar_init(smem_u32(&sh->k_free[i]), 1);
+            mbar_init(smem_u32(&sh->v_full[i]), 1);
+            mbar_init(smem_u32(&sh->v_free[i]), 1);
+            mbar_init(smem_u32(&sh->p_full[i]), 8);  // the softmax warps of both CTAs
+            mbar_init(smem_u32(&sh->pv_done[i]), 1);
         }
-        for (int i = 0; i < kPairs; ++i) {
-            mbar_init(smem_u32(&sh->y_full[i]), 1);
-            mbar_init(smem_u32(&sh->y_empty[i]), 1);
+        for (int i = 0; i < kAhead; ++i) {
+            mbar_init(smem_u32(&sh->s_full[i]), 1);
+            mbar_init(smem_u32(&sh->s_read[i]), 8);
         }
-        mbar_init(smem_u32(&sh->q_full), kRows);
-        mbar_init(smem_u32(&sh->s_full), 1);
-        mbar_init(smem_u32(&sh->s_free), kRows);
-        mbar_init(smem_u32(&sh->p_full), kRows);
-        mbar_init(smem_u32(&sh->pv_done), 1);
+        mbar_init(smem_u32(&sh->q_full), 1);
+        mbar_init(smem_u32(&sh->q_free), 1);
+        mbar_init(smem_u32(&sh->v_seen), 1);
         mbar_init(smem_u32(&sh->drain), 1);
         sh->abort_flag = 0;
         fence_barrier_init();
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_c);
     }
     if (warp == kMmaWarp) {
-        tmem_alloc(smem_u32(&sh->tmem), 512);
-        tmem_relinquish();
+        tmem_alloc_pair(smem_u32(&sh->tmem), 512);
+        tmem_relinquish_pair();
     }
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
     const volatile int* abort_flag = &sh->abort_flag;
@@ -362,80 +367,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp < 4) {
         // ------------------------------------------------------------ softmax
-        const int r = threadIdx.x;
+        const int r = (warp & 1) * 32 + lane, side = warp >> 1;  // row of this CTA; half of the keys, of the columns
+        const int tile_row = rank * 64 + r;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        const float c = p.scale * kLog2e;
-        auto load_q = [&](const Piece& y) {
-            // Q: places 0-5 to TMEM, by way of the warp's rows of the shared-memory places 6-8, and those then to
-            // shared memory in the swizzled layout of a TMA box.  A warp reads four rows of 128 bytes at a time.
-            const uint4* q = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(y.row0) + warp * 32) * p.C);
-            const int pitch = p.C / 8, wrows = y.rows - warp * 32;
-#pragma unroll 1
-            for (int place0 = 0; place0 < kMaxChunks; place0 += 3) {
-                uint4 w[24];
-#pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    const int ck = q_place(place0 + e);  // its own inverse
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = i * 4 + (lane >> 3), col = ck * 8 + (lane & 7);
-                        w[8 * e + i] = row < wrows && col < pitch ? q[row * pitch + col] : make_uint4(0, 0, 0, 0);
-                    }
-                }
-                const uint32_t base = sm_q + warp * 32 * 128;
-                __syncwarp();  // the round before has been read
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row = i * 4 + (lane >> 3);
-                        st_shared_v4(base + e * kQBytes + row * 128 + (((lane & 7) ^ (row & 7)) << 4), w[8 * e + i].x,
-                                     w[8 * e + i].y, w[8 * e + i].z, w[8 * e + i].w);
-                    }
-                if (place0 < kTmemChunks) {
-                    __syncwarp();
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) {
-                        uint32_t t[32];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            ld_shared_v4(base + e * kQBytes + lane * 128 + ((i ^ (lane & 7)) << 4), t[4 * i], t[4 * i + 1],
-                                         t[4 * i + 2], t[4 * i + 3]);
-                        tmem_st32_raw(tmem + lanes + kColQ + (place0 + e) * 32, t);
-                    }
-                }
-            }
-            tmem_wait_st();
-            fence_proxy_async_shared();
-            tc_fence_before();
-            mbar_arrive(smem_u32(&sh->q_full));
+        const uint32_t to = tmem + lanes + kColO, ts = tmem + lanes + kColS;
+        const uint32_t s_read = map_shared_rank(smem_u32(&sh->s_read[0]), 0), p_full = map_shared_rank(smem_u32(&sh->p_full[0]), 0);
+        auto arrive = [&](uint32_t bar) {  // one arrival per warp, at the even CTA
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(bar);
         };
-        bool more = walk.next(p, &x);
-        if (more) load_q(x);
-        while (more && ok) {
-            const Piece now = x;
-            const bool mine = r < now.rows;
-            float m = -INFINITY, ms = 0.f, l = 0.f;
-            for (int j = 0; j < now.n; ++j, ++step) {
-                ok = __all_sync(~0u, wait(&sh->s_full, step));
-                if (!ok) break;
+        const float c = p.scale * kLog2e;
+        int tails = 0;  // steps so far that ended inside
+        const int dv0 = side * p.dv_half, dv = min(p.dv_half, p.Lkv - dv0);  // value columns of this thread
+        while (ok && walk.next(p, &x)) {
+            const bool mine = tile_row < x.rows;
+            const int n = x.n, keys = x.end - x.key0;
+            float m = -INFINITY, ms = 0.f, l = 0.f;  // row maximum of S, ms = m c, sum of this thread's half of P
+            for (int j = 0; j < n; ++j, ++step) {
+                ok = __all_sync(~0u, wait(&sh->s_full[step % kAhead], step / kAhead));
+                // (a barrier of the whole group follows in every step: it leaves together)
+                uint32_t s[32];
                 tc_fence_after();
-                uint32_t s[kKeys];
-                float mt = tmem_ld64_max(tmem + lanes + kColS, s);  // of the row
+                float mt = tmem_ld32_max(ts + step % kAhead * 32, s);
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh->s_free));
-                const int left = now.end - now.key0 - j * kKeys;
-                if (left < kKeys) {
-#pragma unroll
-                    for (int i = 0; i < kKeys; ++i)
-                        if (i >= left) s[i] = 0xFF800000u;
+                arrive(s_read + 8 * (step % kAhead));
+                const int left = keys - j * kKeys - side * 32;
+                if (left < 32) {
                     mt = -INFINITY;
 #pragma unroll
-                    for (int i = 0; i < kKeys; ++i) mt = fmaxf(mt, __uint_as_float(s[i]));
+                    for (int i = 0; i < 32; ++i) {
+                        if (i >= left) s[i] = 0xFF800000u;
+                        mt = fmaxf(mt, __uint_as_float(s[i]));
+                    }
                 }
-                const bool grow = mt > m && (m == -INFINITY || mt * c > ms + kSlack);
+                bool grow = mt > m && (m == -INFINITY || mt * c > ms + kSlack);
                 float alpha = 1.f;
-                if (__any_sync(~0u, grow)) {
+                // rare after the first step: the row's two threads agree on a new scale
+                if (named_bar_or(1, 128, grow || !ok)) {
+                    sh->row_max[threadIdx.x] = mt;
+                    if (named_bar_or(1, 128, !ok)) {
+                        ok = false;
+                        break;
+                    }
+                    const float other = *const_cast<volatile float*>(&sh->row_max[threadIdx.x ^ 64]);
+                    mt = fmaxf(mt, other);
                     if (mt > m) {
                         const float next = mt * c;
                         if (m != -INFINITY) alpha = ex2(ms - next);
@@ -446,9 +421,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint64_t cc = pk2(c, c), mm = pk2(-ms, -ms);
                 uint64_t sum0 = 0, sum1 = 0;
-                uint32_t w[kKeys / 2];
+                uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < kKeys; i += 4) {
+                for (int i = 0; i < 32; i += 4) {
                     float e0, e1, e2, e3;
                     upk2(fma2(pk2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), cc, mm), e0, e1);
                     upk2(fma2(pk2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), cc, mm), e2, e3);
@@ -461,61 +436,62 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float a0, a1;
                 upk2(add2(sum0, sum1), a0, a1);
                 l += a0 + a1;
-                // the step before has read P, and O is at rest
-                if (step > 0) {
-                    ok = __all_sync(~0u, wait(&sh->pv_done, step - 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                }
+                // P of two steps before has been read; O is at rest where it has to be scaled
+                if (step > 1) ok = __all_sync(~0u, ok && wait(&sh->pv_done[step & 1], (step >> 1) - 1));
                 if (j > 0 && __any_sync(~0u, alpha != 1.f)) {
+                    ok = __all_sync(~0u, ok && wait(&sh->pv_done[(step - 1) & 1], (step - 1) >> 1));
+                    tc_fence_after();
 #pragma unroll 1
-                    for (int d = 0; d < dv; d += 16) {
+                    for (int d = 0; d < p.dv_half; d += 16) {
                         float o[16];
-                        tmem_ld16(tmem + lanes + kColO + d, o);
+                        tmem_ld16(to + d, o);
 #pragma unroll
                         for (int i = 0; i < 16; ++i) o[i] *= alpha;
-                        tmem_st16(tmem + lanes + kColO + d, o);
+                        tmem_st16(to + d, o);
                     }
                 }
-                const uint32_t dst = sm_p + r * 128;
+                const uint32_t dst = sm_p + (step & 1) * kPBytes + r * 128;
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    st_shared_v4(dst + ((i ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                if (left < kKeys) {
+                for (int i = 0; i < 4; ++i)
+                    st_shared_v4(dst + (((side * 4 + i) ^ (r & 7)) << 4), w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                const int rest = keys - j * kKeys;
+                if (rest < kKeys) {
                     // rows behind the end may hold anything: as values they have to be zero
-                    for (int k = r; k < (kKeys - left) * nvc * 8; k += kRows) {
-                        const int row = left + k / (nvc * 8), in = k % (nvc * 8), c2 = in / 8;
-                        const int slot = (step * pairs + c2 / 2) % kPairs * 2 + (c2 & 1);
-                        st_shared_v4(sm_y + slot * kSlotBytes + row * 128 + (in & 7) * 16, 0, 0, 0, 0);
+                    ok = __all_sync(~0u, ok && wait(&sh->v_seen, tails));
+                    ++tails;
+                    for (int k = threadIdx.x; k < (kKeys - rest) * nvc * 8; k += 128) {
+                        const int row = rest + k / (nvc * 8), in = k % (nvc * 8);
+                        st_shared_v4(sm_v + ((step & 1) * kMaxValues + in / 8) * kVBytes + row * 128 + (in & 7) * 16, 0, 0, 0, 0);
                     }
                 }
                 fence_proxy_async_shared();
                 tc_fence_before();
-                mbar_arrive(smem_u32(&sh->p_full));
+                arrive(p_full + 8 * (step & 1));
             }
-            if (!ok) break;
-            // every score of this piece is done: the next piece's Q can take Q's place while P V finishes
-            more = walk.next(p, &x);
-            if (more) load_q(x);
-            ok = __all_sync(~0u, wait(&sh->pv_done, step - 1));
-            if (!ok) break;
+            sh->row_sum[threadIdx.x] = l;
+            ok = __all_sync(~0u, ok && wait(&sh->pv_done[(step - 1) & 1], (step - 1) >> 1));
+            if (named_bar_or(1, 128, !ok)) {
+                ok = false;
+                break;
+            }
             tc_fence_after();
+            l = sh->row_sum[threadIdx.x & 63] + sh->row_sum[(threadIdx.x & 63) + 64];
             // A row whose keys this piece covers alone is finished; the others leave a partial result.
-            bool direct = now.whole;
-            const int b = (now.row0 + r) / p.H;
+            bool direct = x.whole;
+            const int b = (x.row0 + tile_row) / p.H;
             if (walk.shared && direct && mine) {
                 int trow, bits = 0;
                 const int len = batch_len(p, b, &trow, &bits);
-                direct = now.prefix ? len == walk.shared : len < walk.shared;
+                direct = x.prefix ? len == walk.shared : len < walk.shared;
             }
-            // A warp's rows pass through its part of P's buffer, 128 bytes of each at a time, so that it stores
-            // four rows' whole lines at once: 64 columns of finished rows, 32 of partial ones.
+            // A warp's rows pass through shared memory, 128 bytes of each at a time, so that it stores four rows'
+            // whole lines at once: 64 columns of finished rows, 32 of partial ones.
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const int64_t at = static_cast<int64_t>(now.row0) + r;
+            const int64_t at = static_cast<int64_t>(x.row0) + tile_row;
             const uint32_t direct_rows = __ballot_sync(~0u, direct && mine), part_rows = __ballot_sync(~0u, !direct && mine);
             const uint32_t stage = sm_p + warp * 32 * 128;
-            auto put = [&](int i, uint32_t a, uint32_t b, uint32_t c2, uint32_t d2) {
-                st_shared_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), a, b, c2, d2);
+            auto put = [&](int i, uint32_t a, uint32_t b2, uint32_t c2, uint32_t d2) {
+                st_shared_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), a, b2, c2, d2);
             };
             auto flush = [&](uint8_t* rows, int64_t row_bytes, uint32_t which, int bytes) {
                 __syncwarp();
@@ -528,12 +504,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 __syncwarp();
             };
-            uint8_t* out = reinterpret_cast<uint8_t*>(p.out + (static_cast<int64_t>(now.row0) + warp * 32) * p.Lkv + dv0);
-            uint8_t* part = reinterpret_cast<uint8_t*>(p.part_o + (now.part + warp * 32) * p.Lkv + dv0);
+            const int64_t row32 = rank * 64 + (warp & 1) * 32;  // the warp's first row of the tile
+            uint8_t* out = reinterpret_cast<uint8_t*>(p.out + (x.row0 + row32) * p.Lkv + dv0);
+            uint8_t* part = reinterpret_cast<uint8_t*>(p.part_o + (x.part + row32) * p.Lkv + dv0);
 #pragma unroll 1
             for (int d = 0; d < dv; d += 64) {
                 uint32_t o[64];  // (what lies behind dv is not stored)
-                tmem_ld64_raw(tmem + lanes + kColO + d, o);
+                tmem_ld64_raw(to + d, o);
 #pragma unroll
                 for (int i = 0; i < 64; ++i) o[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
                 const int left = dv - d;
@@ -559,136 +536,108 @@ __global__ void __launch_bounds__(kThreads, 1)
                     flush(out + d * 2, p.Lkv * 2, direct_rows, left * 2);
                 }
             }
-            if (mine && half == 0) {
+            if (mine && side == 0) {
                 const float lg = l == 0.f ? -INFINITY : ms + log2f(l);
-                if (!direct) p.part_lse[now.part + r] = lg;
+                if (!direct) p.part_lse[x.part + tile_row] = lg;
                 else if (p.lse) p.lse[at] = lg * kLn2;
             }
             tc_fence_before();
+            named_bar_sync(1, 128);  // the next piece's P takes the place that results pass through
         }
     } else if (warp == kMmaWarp) {
-        // ---------------------------------------------------------------- MMA
-        if (elect_one()) {
+        // ------------------------------------------ MMA (the even CTA's, for both)
+        if (rank == 0 && elect_one()) {
             const uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys);
-            const uint32_t x_full = smem_u32(&sh->x_full[0]), x_empty = smem_u32(&sh->x_empty[0]);
-            const uint32_t y_full = smem_u32(&sh->y_full[0]), y_empty = smem_u32(&sh->y_empty[0]);
-            constexpr uint32_t kSlotStep = kSlotBytes >> 4, kQStep = kQBytes >> 4;
-            const uint64_t dq = smem_desc_sw128(sm_q), dp = smem_desc_sw128(sm_p);
-            const uint64_t dx = smem_desc_sw128(sm_x), dy = smem_desc_sw128(sm_y);
-            const uint64_t dvals = smem_desc_sw128_mn(sm_y, kSlotBytes);
-            const uint32_t tq = tmem + kColQ, ts = tmem + kColS, to = tmem + kColO;
+            const uint64_t dq = smem_desc_sw128(sm_q), dk = smem_desc_sw128(sm_k), dp = smem_desc_sw128(sm_p);
+            const uint64_t dvals = smem_desc_sw128_mn(sm_v, kVBytes);
+            const uint32_t to = tmem + kColO;
             const bool widest = p.C == 64 * kMaxChunks;
-            auto look = [&](uint32_t bar, uint32_t parity) {
-                ok = ok && mbar_wait_lean(bar, parity, kTimeoutNs, abort_flag);
+            // value columns in products of up to 128 per CTA
+            const int first = min(p.dv_half, 128), second = p.dv_half - first;
+            const uint32_t id0 = idesc_bf16_f32(kRows, 2 * first) | kIdescBMnMajor;
+            const uint32_t id1 = idesc_bf16_f32(kRows, second ? 2 * second : 32) | kIdescBMnMajor;
+            auto look = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && wait(bar, parity);
                 tc_fence_after();
                 return ok;
             };
-            // S (+)= Q K^T over one chunk of any width
-            auto chunk_mma = [&](int ck, uint64_t b, bool first) {
-                const int place = q_place(ck), ks = min(4, p.C / 16 - ck * 4);
-#pragma unroll 1
-                for (int e = 0; e < ks; ++e) {
-                    const uint32_t acc = !(first && e == 0);
-                    if (place < kTmemChunks) mma_bf16_ts(ts, tq + place * 32 + e * 8, b + 2 * e, idesc_s, acc);
-                    else mma_bf16(ts, dq + (place - kTmemChunks) * kQStep + 2 * e, b + 2 * e, idesc_s, acc);
-                }
-            };
-            int y = 0;  // ring place and parity of the next pair of value chunks
-            uint32_t yp = 0;
-            int at[2] = {0, 0}, was[2] = {0, 0};  // places of this step's and the step before's pairs
-            const uint32_t id[2] = {idesc_bf16_f32(kRows, min(dv, 128)) | kIdescBMnMajor,
-                                    idesc_bf16_f32(kRows, dv > 128 ? dv - 128 : 16) | kIdescBMnMajor};
+            auto commit = [&](uint64_t* bar) { mma_commit_pair(smem_u32(bar), 0x3); };
             for (int piece = 0; walk.next(p, &x); ++piece) {
                 const int n = x.n;
-                look(smem_u32(&sh->q_full), piece & 1);
-                // Per round: the scores of step t, then P V of step t - 1, whose softmax ran meanwhile.
+                if (!look(&sh->q_full, piece)) break;
+                // Per round: the scores of step t, then P V of step t - 2, whose softmax ran meanwhile.
 #pragma unroll 1
-                for (int t = 0; t <= n && ok; ++t) {
-                    const int st = step + t;
-                    was[0] = at[0], was[1] = at[1];
+                for (int t = 0; t < n + 2 && ok; ++t) {
+                    const int st = step + t, e = st & 1, f4 = st % kAhead;
                     if (t < n) {
-                        if (st > 0 && !look(smem_u32(&sh->s_free), (st - 1) & 1)) break;
-                        if (nx && !look(x_full + 8 * (st & 1), (st >> 1) & 1)) break;
-                        const uint64_t b = dx + (st & 1) * (kOthers * kSlotStep);
+                        if (st >= kAhead && !look(&sh->s_read[f4], st / kAhead - 1)) break;
+                        if (!look(&sh->k_full[e], st >> 1)) break;
+                        const uint32_t d = tmem + kColS + f4 * 32;
+                        const uint64_t b = dk + e * (kMaxChunks * kKBytes >> 4);
                         if (widest) {
 #pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                mma_bf16_ts(ts, tq + 128 + k * 8, b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, k > 0);
-#pragma unroll
-                            for (int k = 8; k < 20; ++k)
-                                mma_bf16(ts, dq + ((k >> 2) - 2) * kQStep + 2 * (k & 3),
-                                         b + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, 1);
+                            for (int k = 0; k < 4 * kMaxChunks; ++k)
+                                mma_bf16_pair(d, dq + (k >> 2) * (kQBytes >> 4) + 2 * (k & 3),
+                                              b + (k >> 2) * (kKBytes >> 4) + 2 * (k & 3), idesc_s, k > 0);
                         } else {
-                            for (int i = 0; i < nx; ++i) chunk_mma(other(i), b + i * kSlotStep, i == 0);
+#pragma unroll 1
+                            for (int k = 0; k < p.C / 16; ++k)
+                                mma_bf16_pair(d, dq + (k >> 2) * (kQBytes >> 4) + 2 * (k & 3),
+                                              b + (k >> 2) * (kKBytes >> 4) + 2 * (k & 3), idesc_s, k > 0);
                         }
-                        if (nx) mma_commit(x_empty + 8 * (st & 1));
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if (e >= pairs) break;
-                            if (!look(y_full + 8 * y, yp)) break;
-                            const uint64_t v = dy + y * (2 * kSlotStep);
-                            if (widest) {
-#pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_bf16_ts(ts, tq + e * 64 + k * 8, v + (k >> 2) * kSlotStep + 2 * (k & 3), idesc_s, 1);
-                            } else {
-                                for (int i = 0; i < 2 && 2 * e + i < nvc; ++i)
-                                    chunk_mma(v0 + 2 * e + i, v + i * kSlotStep, nx == 0 && e == 0 && i == 0);
-                            }
-                            at[e] = y;
-                            if (++y == kPairs) y = 0, yp ^= 1u;
-                        }
-                        if (!ok) break;
-                        mma_commit(smem_u32(&sh->s_full));
+                        commit(&sh->s_full[f4]);
+                        commit(&sh->k_free[e]);
+                        if (t + 1 == n) commit(&sh->q_free);
                     }
-                    if (t > 0) {
-                        if (!look(smem_u32(&sh->p_full), (st - 1) & 1)) break;
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            if (e >= pairs) break;
-                            if (e * 128 < dv) {  // (a pair may hold no value column)
-                                const uint64_t v = dvals + was[e] * (2 * kSlotStep);
-#pragma unroll
-                                for (int k = 0; k < kKeys / 16; ++k)
-                                    mma_bf16(to + e * 128, dp + 2 * k, v + k * (2048 >> 4), id[e], t > 1 || k > 0);
-                            }
-                            mma_commit(y_empty + 8 * was[e]);
+                    if (t > 1) {
+                        const int pv = st - 2, f = pv & 1;
+                        if (!look(&sh->v_full[f], pv >> 1)) break;
+                        if (t == n + 1 && x.end - x.key0 < n * kKeys) {  // both CTAs clear the rows behind the end first
+                            mbar_arrive(smem_u32(&sh->v_seen));
+                            mbar_arrive_peer(map_shared_rank(smem_u32(&sh->v_seen), 1));
                         }
-                        mma_commit(smem_u32(&sh->pv_done));
+                        if (!look(&sh->p_full[f], pv >> 1)) break;
+                        const uint64_t b = dvals + f * (kMaxValues * kVBytes >> 4);
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k) {
+                            mma_bf16_pair(to, dp + f * (kPBytes >> 4) + 2 * k, b + k * (2048 >> 4), id0, t > 2 || k > 0);
+                            if (second) mma_bf16_pair(to + 128, dp + f * (kPBytes >> 4) + 2 * k, b + (2 * kVBytes >> 4) + k * (2048 >> 4), id1, t > 2 || k > 0);
+                        }
+                        commit(&sh->pv_done[f]);
+                        commit(&sh->v_free[f]);
                     }
                 }
                 if (!ok) break;
                 step += n;
             }
-            if (!ok) {  // no MMA may still run when the CTA leaves
-                mma_commit(smem_u32(&sh->drain));
+            if (!ok) {  // no MMA may still run when the CTAs leave
+                commit(&sh->drain);
                 mbar_wait(smem_u32(&sh->drain), 0, kTimeoutNs, nullptr);
             }
         }
     } else {
         // --------------------------------------------------------------- TMA
-        // The lanes look up the rows of 32 boxes at a time; one thread issues the copies.
+        // The lanes look up the rows of 32 boxes at a time; one thread issues the copies, each CTA its halves, which
+        // complete on the even CTA's barriers; the even CTA tells them how many bytes both bring.
         const int per = kKeys / p.box, batch = 32 / per;  // boxes per step, steps per lookup
         const bool lead = elect_one();
-        const uint32_t x_full = smem_u32(&sh->x_full[0]), x_empty = smem_u32(&sh->x_empty[0]);
-        const uint32_t y_full = smem_u32(&sh->y_full[0]), y_empty = smem_u32(&sh->y_empty[0]);
         const uint32_t box_bytes = p.box * 128;
-        const bool whole = per == 1 && p.C == 64 * kMaxChunks;
-        int bits = 0, y = 0, xs = 0, ys = 0;  // xs, ys: barriers armed
-        uint32_t yp = 1;
-        // `count` chunks from chunk `ck` on to `dst`, box by box
-        auto copy = [&](uint32_t dst, uint32_t bar, int ck, int count, int rows, int box0) {
-#pragma unroll 1
-            for (int e = 0; e < per; ++e) {
-                const int row = __shfl_sync(~0u, rows, box0 + e);
-                if (lead)
-                    for (int c = 0; c < count; ++c)
-                        tma_load_3d(dst + e * box_bytes + c * kSlotBytes, &tm_c, bar, (ck + c) * 64, 0, row);
-            }
-        };
+        const bool whole = p.box >= 32 && p.C == 64 * kMaxChunks && p.dv_half == 256;
+        auto at_even = [&](uint64_t* bar) { return map_shared_rank(smem_u32(bar), 0); };
+        int bits = 0, pieces = 0, ks = 0, vs = 0;  // Q, K and V places filled
         while (ok && walk.next(p, &x)) {
             const int n = x.n, key0 = x.key0, end = x.end;
             const int32_t* row_table = p.table + static_cast<int64_t>(x.page_row) * p.max_pages;
+            if (lead) {  // Q, once the scores of the piece before are made
+                if (pieces) ok = wait(&sh->q_free, pieces - 1);
+                if (ok) {
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh->q_full), 2 * chunks * kQBytes);
+                    for (int k = 0; k < chunks; ++k)
+                        tma_load_3d_pair(sm_q + k * kQBytes, &tm_q, at_even(&sh->q_full), k * 64, 0, x.row0 + rank * 64);
+                    ++pieces;
+                }
+            }
+            ok = __all_sync(~0u, ok);
             // first row of box `lane` of the batch that starts at step j; a row outside the cache reads as zeros
             auto look_up = [&](int j) {
                 const int key = key0 + (j * per + lane) * p.box;
@@ -704,66 +653,81 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int rows = look_up(0), ahead = batch < n ? look_up(batch) : p.num_rows;
             const bool far = !x.prefix && lane / per < batch;
-            if (far && lane / per < kFetch && (lane / per & (p.halves - 1)) == half) fetch(rows);
+            if (far && lane / per < kFetch && (lane / per & 1) == rank) fetch(rows);
+            // K of step j, then V of step j - 2, as they are used: so K never waits behind a V whose place is not free.
+            int row[kKeys / 16], row1[kKeys / 16], row2[kKeys / 16];  // the boxes of steps j, j - 1, j - 2
+#pragma unroll
+            for (int e = 0; e < kKeys / 16; ++e) row[e] = row1[e] = row2[e] = p.num_rows;
 #pragma unroll 1
-            for (int j0 = 0; j0 < n && ok; j0 += batch) {
-                if (j0) {
+            for (int j = 0; j < n + 2 && ok; ++j) {
+                const int i = j & (batch - 1);
+                if (i == 0 && j > 0 && j < n) {
                     rows = ahead;
-                    ahead = j0 + batch < n ? look_up(j0 + batch) : p.num_rows;
+                    ahead = j + batch < n ? look_up(j + batch) : p.num_rows;
                 }
-                const int steps = min(batch, n - j0);
-#pragma unroll 1
-                for (int j = 0; j < steps && ok; ++j, ++step) {
-                    const int st = step & 1;
-                    const int row0 = __shfl_sync(~0u, rows, j * per);
-                    // step j + kFetch of the run, alternately by the two CTAs
-                    if (far && lane / per == (j + kFetch) % batch && (j & (p.halves - 1)) == half)
-                        fetch(j + kFetch < batch ? rows : ahead);
-                    if (nx) {
-                        const uint32_t bar = x_full + 8 * st, dst = sm_x + st * kOthers * kSlotBytes;
-                        if (lead) {
-                            ok = mbar_wait_lean(x_empty + 8 * st, ((step >> 1) & 1) ^ 1, kTimeoutNs, abort_flag);
-                            if (ok) {
-                                mbar_arrive_expect_tx(bar, nx * kSlotBytes);
-                                ++xs;
-                                if (whole) {
-                                    tma_load_3d(dst, &tm_4, bar, 0, row0, v0 ^ kGroup);
-                                    tma_load_3d(dst + kGroup * kSlotBytes, &tm_c, bar, 2 * kGroup * 64, 0, row0);
-                                }
+#pragma unroll
+                for (int e = 0; e < kKeys / 16; ++e) {
+                    row2[e] = row1[e];
+                    row1[e] = row[e];
+                    row[e] = __shfl_sync(~0u, rows, min(i * per + e, 31));
+                }
+                // step j + kFetch of the run, alternately by the two CTAs
+                if (far && j < n && lane / per == ((i + kFetch) & (batch - 1)) && (j & 1) == rank)
+                    fetch(i + kFetch < batch ? rows : ahead);
+                if (lead && j < n) {
+                    const int st = (step + j) & 1;
+                    ok = wait(&sh->k_free[st], ((step + j) >> 1) ^ 1);
+                    if (ok) {
+                        ++ks;
+                        const uint32_t bar = at_even(&sh->k_full[st]), dst = sm_k + st * kMaxChunks * kKBytes;
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh->k_full[st]), 2 * chunks * kKBytes);
+                        // this CTA's 32 keys: half of a box of 64 (or outside, like it), a box of 32, two of 16
+                        const int k0 = per == 1 ? (rank && row[0] < p.num_rows ? row[0] + 32 : row[0])
+                                                : rank == 0 ? row[0] : per == 2 ? row[1] : row[2];
+                        if (whole) {
+                            tma_load_3d_pair(dst, &tm_k4, bar, 0, k0, 0);
+                            tma_load_3d_pair(dst + 4 * kKBytes, &tm_k4, bar, 0, k0, 4);
+                            tma_load_3d_pair(dst + 8 * kKBytes, &tm_c, bar, 8 * 64, 0, k0);
+                        } else {
+                            for (int k = 0; k < chunks; ++k) {
+                                tma_load_3d_pair(dst + k * kKBytes, &tm_c, bar, k * 64, 0, k0);
+                                if (per == 4)
+                                    tma_load_3d_pair(dst + k * kKBytes + box_bytes, &tm_c, bar, k * 64, 0, rank ? row[3] : row[1]);
                             }
                         }
-                        ok = __all_sync(~0u, ok);
-                        if (!ok) break;
-                        if (!whole) {
-                            copy(dst, bar, other(0), min(nx, v0 ? v0 : nx), rows, j * per);
-                            if (v0 && nx > v0) copy(dst + v0 * kSlotBytes, bar, other(v0), nx - v0, rows, j * per);
-                        }
-                    }
-#pragma unroll 1
-                    for (int e = 0; e < pairs; ++e) {
-                        const uint32_t bar = y_full + 8 * y, dst = sm_y + y * 2 * kSlotBytes;
-                        const int count = min(2, nvc - 2 * e);
-                        if (lead) {
-                            ok = mbar_wait_lean(y_empty + 8 * y, yp, kTimeoutNs, abort_flag);
-                            if (ok) {
-                                mbar_arrive_expect_tx(bar, count * kSlotBytes);
-                                ++ys;
-                                if (whole) tma_load_3d(dst, &tm_2, bar, 0, row0, v0 + 2 * e);
-                            }
-                        }
-                        ok = __all_sync(~0u, ok);
-                        if (!ok) break;
-                        if (!whole) copy(dst, bar, v0 + 2 * e, count, rows, j * per);
-                        if (++y == kPairs) y = 0, yp ^= 1u;
                     }
                 }
+                if (lead && j > 1 && ok) {
+                    const int st = (step + j) & 1;
+                    ok = wait(&sh->v_free[st], ((step + j - 2) >> 1) ^ 1);
+                    if (ok) {
+                        ++vs;
+                        const uint32_t bar = at_even(&sh->v_full[st]), dst = sm_v + st * kMaxValues * kVBytes;
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh->v_full[st]), 2 * nvc * kVBytes);
+                        if (whole && per == 1) {
+                            tma_load_3d_pair(dst, &tm_v4, bar, 0, row2[0], rank * 4);
+                        } else {
+                            const int boxes = per == 1 ? 2 : per;  // a box of 64 in two of 32
+                            const uint32_t bytes = per == 1 ? 32 * 128 : box_bytes;
+#pragma unroll
+                            for (int e = 0; e < kKeys / 16; ++e) {
+                                if (e >= boxes) break;
+                                const int vr = per == 1 ? (e && row2[0] < p.num_rows ? row2[0] + 32 : row2[0]) : row2[e];
+                                for (int k = 0; k < nvc; ++k)
+                                    tma_load_3d_pair(dst + k * kVBytes + e * bytes, &tm_c, bar, v0 + k * 64, 0, vr);
+                            }
+                        }
+                    }
+                }
+                ok = __all_sync(~0u, ok);
             }
+            step += n;
         }
-        // no copy may still be landing when the CTA leaves
-        if (lead) {
-            for (int u = max(xs - 2, 0); u < xs; ++u) mbar_wait(x_full + 8 * (u & 1), (u >> 1) & 1, kTimeoutNs, nullptr);
-            for (int u = max(ys - kPairs, 0); u < ys; ++u)
-                mbar_wait(y_full + 8 * (u % kPairs), (u / kPairs) & 1, kTimeoutNs, nullptr);
+        // no copy of either CTA may still be landing when they leave
+        if (lead && rank == 0) {
+            if (pieces) mbar_wait(smem_u32(&sh->q_full), (pieces - 1) & 1, kTimeoutNs, nullptr);
+            for (int u = max(ks - 2, 0); u < ks; ++u) mbar_wait(smem_u32(&sh->k_full[u & 1]), (u >> 1) & 1, kTimeoutNs, nullptr);
+            for (int u = max(vs - 2, 0); u < vs; ++u) mbar_wait(smem_u32(&sh->v_full[u & 1]), (u >> 1) & 1, kTimeoutNs, nullptr);
         }
         if (bits) raise_status(p.status, bits);
     }
@@ -774,9 +738,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    cluster_sync_all();  // neither CTA leaves or frees TMEM while the other's copies and products may touch it
     if (warp == kMmaWarp) {
         tc_fence_after();
-        tmem_dealloc(tmem, 512);
+        tmem_dealloc_pair(tmem, 512);
     }
 }
 
@@ -859,7 +824,7 @@ int check_cache_dims(const mla_prolog_cache_dims& d) {
 
 // Workspace: the cut, the costs before each sequence, the partial results.
 struct Layout {
-    int row_tiles, head_tiles, halves, units;
+    int row_tiles, head_tiles, units;
     size_t bases, part_lse, part_o, bytes;
 };
 
@@ -868,8 +833,7 @@ Layout layout(const mla_prolog_cache_dims& d, int sms) {
     const int64_t rows = static_cast<int64_t>(d.batch) * d.num_heads;
     y.row_tiles = static_cast<int>((rows + kRows - 1) / kRows);
     y.head_tiles = (d.num_heads + kRows - 1) / kRows;
-    y.halves = d.kv_lora_rank > kHalf ? 2 : 1;
-    y.units = sms / y.halves > 0 ? sms / y.halves : 1;
+    y.units = sms / 2 > 0 ? sms / 2 : 1;
     auto round = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t parts = static_cast<size_t>(y.row_tiles) * kRows + rows + static_cast<size_t>(y.units) * kRows;
     y.bases = round(sizeof(Cut));
@@ -917,16 +881,18 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     if (workspace_bytes < y.bytes) return MLA_ERR_INVALID_ARG;
     const int C = d->kv_lora_rank + d->rope_dim, box = gcd(d->page_size, kKeys);
     const int64_t rows = d->num_pages * d->page_size;
-    CUtensorMap tm, tm4, tm2;
+    const int dv_half = (d->kv_lora_rank / 2 + 15) / 16 * 16;
+    CUtensorMap tq, tc, tk4, tv4;
     // an empty cache has no valid page: every read is outside the map, which then only needs a valid address
     const void* base = rows ? kv_cache : q;
-    bool good = encode_bf16_3d(&tm, base, C, 1, rows ? rows : 1, 1, box);
-    // the same rows by whole chunks, [chunk][row][64], four or two of them in one copy
-    const bool widest = C == 64 * kMaxChunks;
-    tm4 = tm2 = tm;
-    if (widest)
-        good = good && encode_bf16_chunks(&tm4, base, C, rows ? rows : 1, box, 4) &&
-               encode_bf16_chunks(&tm2, base, C, rows ? rows : 1, box, 2);
+    const uint64_t map_rows = rows ? rows : 1;
+    bool good = encode_bf16_3d(&tq, q, C, 1, static_cast<uint64_t>(d->batch) * d->num_heads, 1, 64) &&
+                encode_bf16_3d(&tc, base, C, 1, map_rows, 1, box < 32 ? box : 32);
+    // the same rows by whole chunks, [chunk][row][64], four in one copy: 32 keys for the scores, 64 for the values
+    tk4 = tv4 = tc;
+    if (C == 64 * kMaxChunks)
+        good = good && encode_bf16_chunks(&tk4, base, C, map_rows, 32, 4) &&
+               encode_bf16_chunks(&tv4, base, C, map_rows, kKeys, 4);
     if (!good) return report_cuda(cudaErrorInvalidValue, "tensor maps of attend_cache");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     CacheParams p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(kv_cache), page_table, seq_lens, seqs, shared_len, static_cast<uint16_t*>(out),
@@ -934,23 +900,30 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
                   reinterpret_cast<float*>(ws + y.part_o), reinterpret_cast<float*>(ws + y.part_lse), d->batch,
                   d->num_heads, d->kv_lora_rank, C, d->page_size, d->table_rows, d->max_pages,
                   static_cast<int>(rows ? rows : 1), static_cast<int>(d->num_pages), box, y.row_tiles, y.head_tiles,
-                  y.halves, y.units, d->scale};
+                  y.units, dv_half, d->scale};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = allow_smem(&mla_attend_cache_kernel, kSmem, &ready);
     if (e != cudaSuccess) return report_cuda(e, "mla_attend_cache_kernel attributes");
-    mla_attend_cache_kernel<<<y.units * y.halves, kThreads, kSmem, st>>>(tm, tm4, tm2, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
-    const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
     cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(y.units * 2);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmem;
+    cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    e = cudaLaunchKernelEx(&cfg, mla_attend_cache_kernel, tq, tc, tk4, tv4, p);
+    if (e != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
+    const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(128);
+    cfg.dynamicSmemBytes = 0;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     e = cudaLaunchKernelEx(&cfg, mla_attend_join_kernel, p);
     return e == cudaSuccess ? MLA_OK : report_cuda(e, "launch mla_attend_join_kernel");
 }
