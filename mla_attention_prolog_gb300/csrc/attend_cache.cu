@@ -18,7 +18,7 @@
 // columns.
 //
 // The work is cut into as many equal runs of key steps as there are CTA pairs
-// (a tile costs its steps plus kOverhead for its start and end); a run takes
+// (a tile costs its steps and some more for its start and end); a run takes
 // whole or partial tiles.  Partial results go to the workspace in FP32, and a
 // second kernel joins them.
 #include <cmath>
@@ -53,9 +53,9 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.f;             // log2 of the largest P
 // Own pages are asked of L2 this many steps before their copies: the ring holds two steps, which cover the
 // latency of L2 but not that of HBM.
-constexpr int kFetch = 2;
-constexpr int kOverhead = 7;              // a tile's start and end, in key steps
-constexpr int kMinRun = 8;                // shortest run worth a CTA pair, in key steps
+constexpr int kFetch = 1;
+constexpr int kOverhead = 4, kRowsPerStep = 16;  // a tile's start and end, in key steps: so many, and one per so many rows
+constexpr int kMinRun = 4;                // shortest run worth a CTA pair, in key steps after its tile's start
 
 // What the join kernel needs to know of the cut (start of the workspace).
 struct Cut {
@@ -81,7 +81,8 @@ struct CacheParams {
     float* part_lse;    //   and their log2-sum-exp [part rows]
     int B, H, Lkv, C, page_size, table_rows, max_pages, num_rows, num_pages, box;
     int row_tiles, head_tiles, units;
-    int dv_half;  // value columns of a CTA
+    int dv_half;   // value columns of a CTA
+    int overhead;  // cost of a tile beside its steps
     float scale;
 };
 
@@ -105,13 +106,14 @@ __device__ __forceinline__ int own_steps(int len, int shared) {
     return (len - own_start(len, shared) + kKeys - 1) / kKeys;
 }
 __device__ __forceinline__ int64_t seq_cost(const CacheParams& p, int steps) {
-    return steps ? static_cast<int64_t>(p.head_tiles) * (steps + kOverhead) : 0;
+    return steps ? static_cast<int64_t>(p.head_tiles) * (steps + p.overhead) : 0;
 }
 
 // The steps [*j0, *j1) of a tile of `steps` at cost `base` that the costs
 // [from, to) cover.
-__device__ __forceinline__ void covered(int64_t base, int steps, int64_t from, int64_t to, int* j0, int* j1) {
-    const int64_t a = from - base - kOverhead, e = to - base - kOverhead;
+__device__ __forceinline__ void covered(const CacheParams& p, int64_t base, int steps, int64_t from, int64_t to, int* j0,
+                                        int* j1) {
+    const int64_t a = from - base - p.overhead, e = to - base - p.overhead;
     *j0 = a < 0 ? 0 : a > steps ? steps : static_cast<int>(a);
     *j1 = e < 0 ? 0 : e > steps ? steps : static_cast<int>(e);
 }
@@ -148,8 +150,8 @@ struct Walk {
             int steps;
             if (at < prefix_cost) {
                 steps = shared / kKeys;
-                const int t = static_cast<int>(at / (steps + kOverhead));
-                tile_base = static_cast<int64_t>(t) * (steps + kOverhead);
+                const int t = static_cast<int>(at / (steps + p.overhead));
+                tile_base = static_cast<int64_t>(t) * (steps + p.overhead);
                 x->row0 = t * kRows;
                 x->rows = min(kRows, p.B * p.H - x->row0);
                 tile_row = x->row0;
@@ -166,8 +168,8 @@ struct Walk {
                     steps = own_steps(len, shared);
                 }
                 if (b >= p.B) return false;
-                const int ht = static_cast<int>((at - base) / (steps + kOverhead));
-                tile_base = base + static_cast<int64_t>(ht) * (steps + kOverhead);
+                const int ht = static_cast<int>((at - base) / (steps + p.overhead));
+                tile_base = base + static_cast<int64_t>(ht) * (steps + p.overhead);
                 x->row0 = b * p.H + ht * kRows;
                 x->rows = min(kRows, p.H - ht * kRows);
                 tile_row = static_cast<int64_t>(p.row_tiles) * kRows + x->row0;
@@ -177,8 +179,8 @@ struct Walk {
                 x->prefix = false;
             }
             int j0, j1;
-            covered(tile_base, steps, at, end, &j0, &j1);
-            const int64_t tile_end = tile_base + steps + kOverhead;
+            covered(p, tile_base, steps, at, end, &j0, &j1);
+            const int64_t tile_end = tile_base + steps + p.overhead;
             at = tile_end < end ? tile_end : end;
             if (j1 <= j0) continue;
             x->part = part_row(p, tile_row, unit);
@@ -256,7 +258,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
         if (sh->sharers < 2) shared = 0;
     }
     const int source = sh->source;
-    const int64_t prefix = shared ? static_cast<int64_t>(p.row_tiles) * (shared / kKeys + kOverhead) : 0;
+    const int64_t prefix = shared ? static_cast<int64_t>(p.row_tiles) * (shared / kKeys + p.overhead) : 0;
     int64_t total = prefix, sum;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
@@ -267,7 +269,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
         total += sum;
     }
     int64_t run = (total + p.units - 1) / p.units;
-    if (run < kMinRun) run = kMinRun;
+    if (run < kMinRun + p.overhead) run = kMinRun + p.overhead;
     if (writer) {
         if (threadIdx.x == 0) *p.cut = Cut{prefix, run, shared, source};
         raise_status(p.status, bits);
@@ -763,43 +765,59 @@ __global__ void __launch_bounds__(128) mla_attend_join_kernel(const CacheParams 
     for (int k = 0; k < 2; ++k) {
         if (k == 0) {
             steps[0] = len >= cut.shared ? cut.shared / kKeys : 0;
-            base[0] = row / kRows * (cut.shared / kKeys + kOverhead);
+            base[0] = row / kRows * (cut.shared / kKeys + p.overhead);
             part[0] = row;
         } else {
             steps[1] = own_steps(len, cut.shared);
-            base[1] = p.bases[b] + static_cast<int64_t>(h / kRows) * (steps[1] + kOverhead);
+            base[1] = p.bases[b] + static_cast<int64_t>(h / kRows) * (steps[1] + p.overhead);
             part[1] = static_cast<int64_t>(p.row_tiles) * kRows + row;
         }
-        u0[k] = static_cast<int>((base[k] + kOverhead) / cut.run);
-        u1[k] = steps[k] ? static_cast<int>((base[k] + kOverhead + steps[k] - 1) / cut.run) : u0[k] - 1;
+        u0[k] = static_cast<int>((base[k] + p.overhead) / cut.run);
+        u1[k] = steps[k] ? static_cast<int>((base[k] + p.overhead + steps[k] - 1) / cut.run) : u0[k] - 1;
         count += u1[k] - u0[k] + 1;
     }
     if (count == 1) return;
-    float top = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        for (int u = u0[k]; u <= u1[k]; ++u) {
-            const float v = p.part_lse[part_row(p, part[k], u)];
-            top = v != v ? v : fmaxf(top, v);
-        }
-    const float ref = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
+    // Two pieces are on their way at once; the running maximum, sum and row go on from one two to the next.
+    constexpr int kAtOnce = 2;
+    float ref = 0.f, sum = 0.f, top = -INFINITY;
     float4 acc[4] = {};
+    const int count0 = u1[0] - u0[0] + 1;
+    for (int first = 0; first < count; first += kAtOnce) {
+        float lse[kAtOnce];
+        float4 o[kAtOnce][4];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-        for (int u = u0[k]; u <= u1[k]; ++u) {
-            const int64_t at = part_row(p, part[k], u);
-            const float w = exp2f(p.part_lse[at] - ref);
+        for (int k = 0; k < kAtOnce; ++k) {
+            const int i = first + k;
+            const bool own = i >= count0;
+            const int64_t at = i < count ? part_row(p, own ? part[1] : part[0], own ? u0[1] + i - count0 : u0[0] + i) : 0;
+            lse[k] = i < count ? p.part_lse[at] : -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (i < count && (c * 32 + lane) * 4 < p.Lkv)
+                    o[k][c] = reinterpret_cast<const float4*>(p.part_o + at * p.Lkv)[c * 32 + lane];
+        }
+        float next = top;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) next = fmaxf(next, lse[k]);
+        const float keep = top == -INFINITY ? 0.f : exp2f(top - next);
+        top = next;
+        ref = top == -INFINITY ? 0.f : top;
+        sum *= keep;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c].x *= keep, acc[c].y *= keep, acc[c].z *= keep, acc[c].w *= keep;
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+            if (first + k >= count) break;
+            const float w = exp2f(lse[k] - ref);
             sum += w;
-            const float4* o = reinterpret_cast<const float4*>(p.part_o + at * p.Lkv);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if ((i * 32 + lane) * 4 < p.Lkv) {
-                    const float4 v = o[i * 32 + lane];
-                    acc[i].x = fmaf(w, v.x, acc[i].x), acc[i].y = fmaf(w, v.y, acc[i].y);
-                    acc[i].z = fmaf(w, v.z, acc[i].z), acc[i].w = fmaf(w, v.w, acc[i].w);
+            for (int c = 0; c < 4; ++c)
+                if ((c * 32 + lane) * 4 < p.Lkv) {
+                    acc[c].x = fmaf(w, o[k][c].x, acc[c].x), acc[c].y = fmaf(w, o[k][c].y, acc[c].y);
+                    acc[c].z = fmaf(w, o[k][c].z, acc[c].z), acc[c].w = fmaf(w, o[k][c].w, acc[c].w);
                 }
         }
+    }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -900,7 +918,7 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
                   reinterpret_cast<float*>(ws + y.part_o), reinterpret_cast<float*>(ws + y.part_lse), d->batch,
                   d->num_heads, d->kv_lora_rank, C, d->page_size, d->table_rows, d->max_pages,
                   static_cast<int>(rows ? rows : 1), static_cast<int>(d->num_pages), box, y.row_tiles, y.head_tiles,
-                  y.units, dv_half, d->scale};
+                  y.units, dv_half, kOverhead + (d->num_heads < kRows ? d->num_heads : kRows) / kRowsPerStep, d->scale};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = allow_smem(&mla_attend_cache_kernel, kSmem, &ready);
