@@ -558,9 +558,9 @@ int mla_prolog_lpt(const int64_t* cost, int32_t n, int32_t groups, int32_t* tabl
  * the output sums are FP32; the probabilities are rounded to BF16 for the
  * product with v, and out once at the end.
  *
- * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): Tq, Tk, sequences >= 0;
+ * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): 0 <= Tq, Tk <= 2^30, sequences >= 0;
  * kv_heads >= 1 divides num_heads; qk_dim and v_dim positive multiples of 16,
- * qk_dim <= 256, v_dim <= 128; num_heads <= 65535; scale finite and > 0.
+ * qk_dim <= 256, v_dim <= 128; num_heads <= 65535; 0 < scale <= 1e30.
  */
 #define MLA_PROMPT_CAUSAL           0x1u /* the causal rule above; without it every key of
                                             the sequence is allowed                         */
@@ -628,7 +628,7 @@ int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* dims, const void* q, 
  * batch * num_heads <= 2^24; Lkv a positive multiple of 16 up to 512, R a
  * multiple of 16 (0 .. 128) with Lkv + R <= 576; page_size a positive
  * multiple of 16; num_pages * page_size <= 2^31 - 1; max_pages >= 1 and
- * max_pages * page_size <= 2^30; table_rows >= 0; scale finite and > 0.
+ * max_pages * page_size <= 2^30; table_rows >= 0; 0 < scale <= 1e30.
  */
 typedef struct mla_prolog_cache_dims {
     int32_t batch;         /* rows of q                                             */
@@ -685,8 +685,8 @@ int mla_prolog_attend_cache_workspace(const mla_prolog_cache_dims* dims, size_t*
  * numbers only; mla_prolog_copy_pages() moves the cache's contents.
  * Calls on one pool must be ordered (one stream).
  * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): sequences, num_pages >= 0;
- * page_size, max_pages >= 1; num_pages * page_size and max_pages * page_size
- * <= 2^31 - 1; lists of 0 .. 1024 entries.
+ * page_size, max_pages >= 1; num_pages * page_size <= 2^31 - 1 and max_pages *
+ * page_size <= 2^30; lists of 0 .. 1024 entries; total <= 2^30.
  * Errors of all: INVALID_ARG, UNSUPPORTED_DIMS, CUDA.
  */
 typedef struct mla_prolog_pool {
@@ -759,7 +759,7 @@ int mla_prolog_pages_compact(const mla_prolog_pool* pool, int32_t* moved_to, int
  * be NULL).  No dst may be listed twice or be another entry's src (the order
  * of the copies is not specified).  page_bytes a positive multiple of 16;
  * cache and layer_stride (>= num_pages * page_bytes for two layers or more)
- * 16-byte aligned; 0 <= layers <= 65535.
+ * 16-byte aligned; 0 <= layers <= 65535; n <= 2^30.
  */
 int mla_prolog_copy_pages(void* cache, int32_t layers, int64_t layer_stride, int64_t num_pages, int64_t page_bytes,
                           const int32_t* src, const int32_t* dst, int32_t n, int32_t* status, void* stream);

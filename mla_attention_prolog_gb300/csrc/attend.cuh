@@ -16,6 +16,9 @@ namespace mlap {
 int report_cuda(cudaError_t e, const char* where);
 void* tensor_map_encoder();
 
+// A softmax scale whose product with log2 e and a score keeps its meaning in FP32.
+inline bool scale_ok(float scale) { return scale > 0.f && scale <= 1e30f; }
+
 inline bool ptr_ok(const void* p, uintptr_t align) {
     return p && reinterpret_cast<uintptr_t>(p) % align == 0;
 }

@@ -21,7 +21,6 @@
 // (a tile costs its steps and some more for its start and end); a run takes
 // whole or partial tiles.  Partial results go to the workspace in FP32, and a
 // second kernel joins them.
-#include <cmath>
 #include <cstdint>
 
 #include "attend.cuh"
@@ -731,6 +730,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int u = max(ks - 2, 0); u < ks; ++u) mbar_wait(smem_u32(&sh->k_full[u & 1]), (u >> 1) & 1, kTimeoutNs, nullptr);
             for (int u = max(vs - 2, 0); u < vs; ++u) mbar_wait(smem_u32(&sh->v_full[u & 1]), (u >> 1) & 1, kTimeoutNs, nullptr);
         }
+        // and what the tensor core frees has arrived (a piece's last products have ended before its results go out)
+        if (lead) {
+            if (pieces) ok = ok && wait(&sh->q_free, pieces - 1);
+            for (int u = max(ks - 2, 0); u < ks; ++u) ok = ok && wait(&sh->k_free[u & 1], u >> 1);
+            for (int u = max(vs - 2, 0); u < vs; ++u) ok = ok && wait(&sh->v_free[u & 1], u >> 1);
+        }
         if (bits) raise_status(p.status, bits);
     }
     if (!ok) {
@@ -835,7 +840,7 @@ int check_cache_dims(const mla_prolog_cache_dims& d) {
         return MLA_ERR_UNSUPPORTED_DIMS;
     if (d.page_size < 16 || d.page_size % 16 || d.table_rows < 0 || d.max_pages < 1 || d.num_pages < 0 ||
         d.num_pages > most / d.page_size || static_cast<int64_t>(d.max_pages) * d.page_size > (1 << 30) ||
-        !(d.scale > 0.f) || !std::isfinite(d.scale))
+        !scale_ok(d.scale))
         return MLA_ERR_UNSUPPORTED_DIMS;
     return MLA_OK;
 }

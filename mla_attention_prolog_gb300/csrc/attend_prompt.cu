@@ -18,7 +18,6 @@
 // The maximum that P is scaled by moves only when a row's maximum has grown
 // by more than 2^8: until then P <= 2^8, which neither BF16 nor the FP32 sums
 // mind, and O need not be rescaled.
-#include <cmath>
 #include <cstdint>
 
 #include "attend.cuh"
@@ -584,6 +583,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                       kTimeoutNs, nullptr);
         for (int t = 0; t < 2; ++t)
             if (q_loaded >> t & 1) mbar_wait(smem_u32(&sh->q_full[t]), 0, kTimeoutNs, nullptr);
+        // and what the tensor core frees has arrived (it ends before the epilogue does)
+        for (int u = max(sent - 2 * kAhead, 0); u < sent; ++u)
+            ok = ok && mbar_wait(smem_u32(u & 1 ? &sh->v_free[(u >> 1) % kAhead] : &sh->k_free[(u >> 1) % kAhead]),
+                                 phase_of(u >> 1), kTimeoutNs, abort_flag);
     }
     if (!ok) {
         sh->abort_flag = 1;
@@ -612,7 +615,7 @@ extern "C" int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* d, const v
     if ((d->flags & ~known) || (per_head && !int8)) return MLA_ERR_INVALID_ARG;
     if (d->Tq < 0 || d->Tk < 0 || d->sequences < 0 || d->kv_heads < 1 || d->num_heads < 1 ||
         d->num_heads % d->kv_heads || d->num_heads > 65535 || d->qk_dim < 16 || d->qk_dim > 256 || d->qk_dim % 16 ||
-        d->v_dim < 16 || d->v_dim > 128 || d->v_dim % 16 || !(d->scale > 0.f) || !std::isfinite(d->scale))
+        d->v_dim < 16 || d->v_dim > 128 || d->v_dim % 16 || d->Tq > (1 << 30) || d->Tk > (1 << 30) || !scale_ok(d->scale))
         return MLA_ERR_UNSUPPORTED_DIMS;
     if (int8 ? !ptr_ok(q_scale, 4) : q_scale != nullptr) return MLA_ERR_INVALID_ARG;
     if (d->Tq == 0 || d->sequences == 0) return MLA_OK;

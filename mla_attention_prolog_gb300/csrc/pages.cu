@@ -17,6 +17,7 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxList = 1024;
 constexpr int kPer = kMaxList / kThreads;  // list entries per thread
+constexpr int kMost = 1 << 30;             // tokens of a sequence, slots or copies of a call: 32-bit sums hold twice that
 
 struct Pool {
     int32_t sequences, max_pages, page_size, num_pages;
@@ -69,7 +70,7 @@ struct Span {
     int64_t pages;
 };
 __device__ __forceinline__ Span span_of(const Pool& p) {
-    const int w = ceil_div(p.num_pages, kThreads);
+    const int w = (p.num_pages - 1) / kThreads + 1;
     const int words = w < 1 ? 1 : w > 32 ? 32 : w;
     return Span{words, static_cast<int64_t>(words) * kThreads};
 }
@@ -157,8 +158,6 @@ __device__ __forceinline__ void deal_pages(const Pool& p, const int64_t* first, 
         if (base != at) {
             mask = free_mask(p, sp, base);
             at = base;
-            rank = block_scan(__popc(mask), &sum);
-        } else if (base) {
             rank = block_scan(__popc(mask), &sum);
         }
         for_pages(p, sp, base, mask, before + rank, [&](int32_t page, bool set, int64_t r) {
@@ -480,9 +479,8 @@ __global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(uint8_t* _
 int check_pool(const mla_prolog_pool* h, Pool* p) {
     if (!h) return MLA_ERR_INVALID_ARG;
     if (h->sequences < 0 || h->num_pages < 0 || h->max_pages < 1 || h->page_size < 1) return MLA_ERR_UNSUPPORTED_DIMS;
-    const int64_t most = INT32_MAX;
-    if (static_cast<int64_t>(h->max_pages) * h->page_size > most ||
-        static_cast<int64_t>(h->num_pages) * h->page_size > most)
+    if (static_cast<int64_t>(h->max_pages) * h->page_size > kMost ||
+        static_cast<int64_t>(h->num_pages) * h->page_size > INT32_MAX)
         return MLA_ERR_UNSUPPORTED_DIMS;
     if (h->sequences && (!ptr_ok(h->page_table, 4) || !ptr_ok(h->seq_lens, 4))) return MLA_ERR_INVALID_ARG;
     if (h->num_pages && !ptr_ok(h->refs, 4)) return MLA_ERR_INVALID_ARG;
@@ -515,6 +513,7 @@ int mla_prolog_pages_extend(const mla_prolog_pool* pool, const int32_t* seqs, co
     int rc = check_pool(pool, &p);
     if (rc == MLA_OK) rc = check_list(n, seqs, counts);
     if (rc != MLA_OK) return rc;
+    if (total > kMost) return MLA_ERR_UNSUPPORTED_DIMS;
     if (total < 0 || (slot_mapping && !ptr_ok(slot_mapping, 4)) || (positions && !ptr_ok(positions, 4)))
         return MLA_ERR_INVALID_ARG;
     if (n == 0 && total == 0) return MLA_OK;
@@ -571,6 +570,7 @@ int mla_prolog_copy_pages(void* cache, int32_t layers, int64_t layer_stride, int
                           const int32_t* src, const int32_t* dst, int32_t n, int32_t* status, void* stream) {
     if (layers < 0 || num_pages < 0 || n < 0 || page_bytes <= 0 || page_bytes % 16 || layers > 65535)
         return MLA_ERR_INVALID_ARG;
+    if (n > kMost) return MLA_ERR_UNSUPPORTED_DIMS;
     if (num_pages > INT64_MAX / page_bytes) return MLA_ERR_INVALID_ARG;
     if (layers > 1 && (layer_stride % 16 || layer_stride < num_pages * page_bytes)) return MLA_ERR_INVALID_ARG;
     if (status && !ptr_ok(status, 4)) return MLA_ERR_INVALID_ARG;

@@ -46,6 +46,11 @@ def test_prompt_pointers(L, kw):
     assert prompt(L, prompt_dims(), **kw) == INVALID
 
 
+@pytest.mark.parametrize("kw", [dict(Tq=(1 << 30) + 1), dict(Tk=(1 << 30) + 1), dict(scale=2e30), dict(scale=1e-50)])
+def test_prompt_dims_behind_32_bits(L, kw):
+    assert prompt(L, prompt_dims(**kw)) == DIMS
+
+
 def test_prompt_nothing_to_do(L):
     assert prompt(L, None) == INVALID
     assert prompt(L, prompt_dims(Tq=0), q=None, out=None) == 0
@@ -83,6 +88,10 @@ def test_cache_dims(L, kw, code):
                                 dict(status=ctypes.c_void_p(2))])
 def test_cache_pointers(L, kw):
     assert cache(L, cache_dims(), **kw) == INVALID
+
+
+def test_cache_scale_behind_fp32(L):
+    assert cache(L, cache_dims(scale=2e30)) == DIMS
 
 
 def test_cache_nothing_to_do(L):
@@ -128,6 +137,16 @@ def test_pool_lists(L):
     assert L.mla_prolog_pages_fork(p, None, None, 0, None, None, None) == 0
     assert L.mla_prolog_pages_release(p, None, 0, None) == 0
     assert L.mla_prolog_pages_release(None, P4, 1, None) == INVALID
+
+
+def test_pool_sizes_whose_sums_pass_32_bits(L):
+    p = ctypes.byref(pool(max_pages=1 << 27))   # 2^31 tokens in a sequence
+    assert L.mla_prolog_pages_release(p, P4, 1, None) == DIMS
+    p = ctypes.byref(pool(max_pages=(1 << 26) + 1))
+    assert L.mla_prolog_pages_release(p, P4, 1, None) == DIMS
+    p = ctypes.byref(pool())
+    assert L.mla_prolog_pages_extend(p, P4, P4, 1, P4, P4, (1 << 30) + 1, None) == DIMS
+    assert L.mla_prolog_copy_pages(P16, 1, 0, 10, 32, P4, P4, (1 << 30) + 1, None, None) == DIMS
 
 
 @pytest.mark.parametrize("kw", [dict(layers=-1), dict(layers=70000), dict(page_bytes=0), dict(page_bytes=24),

@@ -215,6 +215,68 @@ def test_prompt_on_a_stream_and_in_a_graph():
         lse.index_fill(0, torch.arange(321, 324, device=DEV), 123.0))
 
 
+def test_prompt_many_short_sequences():
+    """More sequences than one look of a warp covers, many of them empty; the
+    first ones' rows lie behind rows of no sequence."""
+    lens = [i * 7 % 5 - 1 if i % 5 else 0 for i in range(700)]
+    lens = [max(n, 0) for n in lens] + [150]
+    c = prompt_case(20, lens, lens, 2, 1, 64, 64)
+    out, lse, status = run_prompt(c)
+    assert status == 0
+    check_prompt(c, out, lse)
+    head = 4   # the same rows, but the first sequences left out: rows before cu_q[0] stay as they were
+    first = int(c["cu_q"][head].item())
+    sub = {**c, "cu_q": c["cu_q"][head:].contiguous(), "cu_k": c["cu_k"][head:].contiguous()}
+    part, plse, status = run_prompt(sub)
+    assert status == 0 and first > 0
+    assert (part[:first].view(torch.int16) == POISON).all() and (plse[:first] == 123.0).all()
+    assert torch.equal(part[first:].view(torch.int16), out[first:].view(torch.int16)) and torch.equal(plse[first:], lse[first:])
+
+
+def test_prompt_int8_lowest_code_and_negative_scales():
+    c = prompt_case(21, [140, 3], [140, 3], 2, 2, 192, 128, q="int8")
+    c["q"][:, :, ::5] = -128
+    c["q_scale"][::3] *= -1.0
+    c["qd"] = c["q"].double() * c["q_scale"].double().reshape(-1, 1, 1)
+    out, lse, status = run_prompt(c)
+    assert status == 0
+    check_prompt(c, out, lse)
+
+
+def test_prompt_one_query_on_many_keys():
+    c = prompt_case(22, [1, 2], [20011, 5000], 4, 2, 192, 128)
+    out, lse, status = run_prompt(c)
+    assert status == 0
+    check_prompt(c, out, lse)
+
+
+def test_prompt_and_cache_calls_at_once():
+    """Prompts and decoding steps on three streams at the same time."""
+    ps = [prompt_case(23, [700, 90], [700, 90], 4, 4, 192, 128), prompt_case(24, [33, 300], [133, 300], 4, 4, 192, 128)]
+    cc = cache_case(25, [900, 10, 2000, 64], 128, 512, 64, 64)
+    B, H, L = 4, 128, 512
+    pouts = [[torch.zeros((*c["q"].shape[:2], 128), dtype=torch.bfloat16, device=DEV), torch.zeros(c["q"].shape[:2], device=DEV)]
+             for c in ps]
+    cout = [torch.zeros((B, H, L), dtype=torch.bfloat16, device=DEV), torch.zeros((B, H), device=DEV)]
+    ws = torch.empty(binding.attend_cache_workspace_bytes(B, H, L, 64), dtype=torch.uint8, device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, o, s in zip(ps, pouts, streams):
+            binding.attend_prompt(c["q"], c["k"], c["v"], c["cu_q"], c["cu_k"], *o, scale=c["scale"], status=status, stream=s)
+        binding.attend_cache(cc["q"], cc["cache"], cc["table"], cc["lens"], *cout, ws, scale=cc["scale"], status=status,
+                             stream=streams[2])
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    for c, (o, z) in zip(ps, pouts):
+        n = sum(c["new"])
+        o.view(torch.int16)[n:] = POISON
+        z[n:] = 123.0
+        check_prompt(c, o, z)
+    check_cache(cc, *cout)
+
+
 # ------------------------------------------------------------------ the cache
 
 def cache_case(seed, lens, H, Lkv, R, page, shared=0, spare=3):
