@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int unit = blockIdx.x / 2, rank = blockIdx.x % 2;
     const int v0 = rank * p.dv_half, nvc = (p.dv_half + 63) / 64;  // value columns that this CTA brings
 
+    pdl_wait();  // what the kernel before in the stream wrote
     Walk walk;
     if (!make_cut(p, unit, sh, &walk)) return;
     if (warp == kLoadWarp && lane == 0) {
@@ -757,8 +758,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 __global__ void __launch_bounds__(128) mla_attend_join_kernel(const CacheParams p) {
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (row >= static_cast<int64_t>(p.B) * p.H) return;
+    pdl_launch_dependents();
     pdl_wait();
+    if (row >= static_cast<int64_t>(p.B) * p.H) return;
     const Cut cut = *p.cut;
     const int b = static_cast<int>(row / p.H), h = static_cast<int>(row % p.H);
     int trow, bits = 0;
@@ -929,25 +931,22 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     cudaError_t e = allow_smem(&mla_attend_cache_kernel, kSmem, &ready);
     if (e != cudaSuccess) return report_cuda(e, "mla_attend_cache_kernel attributes");
     cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3(y.units * 2);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = kSmem;
     cfg.stream = st;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.numAttrs = 2;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     e = cudaLaunchKernelEx(&cfg, mla_attend_cache_kernel, tq, tc, tk4, tv4, p);
     if (e != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
     const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-    cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    e = cudaLaunchKernelEx(&cfg, mla_attend_join_kernel, p);
+    e = launch_kernel(mla_attend_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, st, true, p);
     return e == cudaSuccess ? MLA_OK : report_cuda(e, "launch mla_attend_join_kernel");
 }
 

@@ -191,7 +191,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int width = min(p.head_group, p.H - g * p.head_group);
     const int tile = in_group / width, h = g * p.head_group + in_group % width;
     const int hk = h / (p.H / p.Hk);
-    if (warp == 0) find_job(p, tile, blockIdx.x == 0, sh);
+    if (warp == 0) {
+        pdl_wait();
+        find_job(p, tile, blockIdx.x == 0, sh);
+    }
     if (warp == kLoadWarp && lane == 0) {
         for (int t = 0; t < 2; ++t) {
             mbar_init(smem_u32(&sh->q_full[t]), p.q8 ? kTile : 1);
@@ -216,9 +219,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(smem_u32(&sh->tmem), 512);
         tmem_relinquish();
     }
+    pdl_wait();  // what the kernel before in the stream wrote
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    // The next kernel of the stream may be brought to the SMs, now that this CTA has its TMEM: one that took
+    // TMEM first and then waited for this grid would never get to run.
+    pdl_launch_dependents();
     const uint32_t tmem = sh->tmem;
     const Job jb{sh->job[0], sh->job[1], sh->job[2], sh->job[3], sh->job[4]};
     if (jb.nq == 0) {
@@ -658,8 +665,7 @@ extern "C" int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* d, const v
     static std::atomic<uint64_t> ready{0};
     cudaError_t e = allow_smem(&mla_attend_prompt_kernel, kSmemMax, &ready);
     if (e != cudaSuccess) return report_cuda(e, "mla_attend_prompt_kernel attributes");
-    mla_attend_prompt_kernel<<<static_cast<unsigned>(tiles * d->num_heads), kThreads, smem,
-                               static_cast<cudaStream_t>(stream)>>>(tq, tk, tv, p);
-    e = cudaGetLastError();
+    e = launch_kernel(mla_attend_prompt_kernel, dim3(static_cast<unsigned>(tiles * d->num_heads)), dim3(kThreads), smem,
+                      static_cast<cudaStream_t>(stream), true, tq, tk, tv, p);
     return e == cudaSuccess ? MLA_OK : report_cuda(e, "launch mla_attend_prompt_kernel");
 }

@@ -9,6 +9,7 @@
 #include <cstdint>
 
 #include "attend.cuh"
+#include "ptx.cuh"
 
 namespace mlap {
 namespace {
@@ -26,6 +27,13 @@ struct Pool {
     int32_t* refs;
     int32_t* status;
 };
+
+// First thing in every kernel here: the next one of the stream may be brought
+// to the SMs meanwhile, and what the one before wrote is awaited.
+__device__ __forceinline__ void pdl_begin() {
+    pdl_launch_dependents();
+    pdl_wait();
+}
 
 __device__ __forceinline__ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
@@ -176,6 +184,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_extend_kernel(Pool p, cons
     __shared__ int32_t seq[kMaxList], need[kMaxList], old[kMaxList];
     __shared__ int64_t first[kMaxList], tok[kMaxList];
     __shared__ uint8_t ok[kMaxList], again[kMaxList];
+    pdl_begin();
     const int t = threadIdx.x;
     const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
     for (int i = t; i < n; i += kThreads) seq[i] = seqs[i];
@@ -269,6 +278,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_fork_kernel(Pool p, const 
     __shared__ int32_t par[kMaxList], child[kMaxList], need[kMaxList], len[kMaxList];
     __shared__ int64_t first[kMaxList];
     __shared__ uint8_t ok[kMaxList], again[kMaxList];
+    pdl_begin();
     const int t = threadIdx.x;
     for (int i = t; i < n; i += kThreads) par[i] = parents[i], child[i] = children[i];
     __syncthreads();
@@ -334,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_fork_kernel(Pool p, const 
 
 __global__ void __launch_bounds__(kThreads) mla_pages_release_kernel(Pool p, const int32_t* __restrict__ seqs, int n) {
     __shared__ int32_t seq[kMaxList];
+    pdl_begin();
     const int t = threadIdx.x;
     for (int i = t; i < n; i += kThreads) seq[i] = seqs[i];
     __syncthreads();
@@ -369,6 +380,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_release_kernel(Pool p, con
 // places below L are written last.
 __global__ void __launch_bounds__(kThreads) mla_pages_compact_kernel(Pool p, int32_t* __restrict__ moved_to,
                                                                      int32_t* __restrict__ live_out) {
+    pdl_begin();
     const int t = threadIdx.x;
     const Span sp = span_of(p);
     int64_t live = 0, sum, at = -1;
@@ -420,6 +432,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_compact_kernel(Pool p, int
 }
 
 __global__ void __launch_bounds__(256) mla_pages_retable_kernel(Pool p, const int32_t* __restrict__ moved_to) {
+    pdl_begin();
     const int64_t n = static_cast<int64_t>(p.sequences) * p.max_pages;
     int bits = 0;
     for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
@@ -444,6 +457,7 @@ __global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(uint8_t* _
                                                                      const int32_t* __restrict__ src,
                                                                      const int32_t* __restrict__ dst, int n, int per,
                                                                      int pieces, int32_t* status) {
+    pdl_begin();
     uint8_t* layer = cache + blockIdx.y * layer_stride;
     const int64_t words = page_bytes / 16;
     const int64_t piece = (words + pieces - 1) / pieces, from_word = blockIdx.z * piece;
@@ -495,8 +509,9 @@ int check_list(int32_t n, const void* a, const void* b) {
     return n == 0 || (ptr_ok(a, 4) && ptr_ok(b, 4)) ? MLA_OK : MLA_ERR_INVALID_ARG;
 }
 
-int launched(const char* what) {
-    const cudaError_t e = cudaGetLastError();
+template <class... KArgs, class... Args>
+int start(const char* what, void (*kernel)(KArgs...), dim3 grid, int threads, void* stream, Args... args) {
+    const cudaError_t e = launch_kernel(kernel, grid, dim3(threads), 0, static_cast<cudaStream_t>(stream), true, args...);
     return e == cudaSuccess ? MLA_OK : report_cuda(e, what);
 }
 
@@ -519,9 +534,8 @@ int mla_prolog_pages_extend(const mla_prolog_pool* pool, const int32_t* seqs, co
     if (n == 0 && total == 0) return MLA_OK;
     int sms;
     if ((rc = current_sm103(&sms)) != MLA_OK) return rc;
-    mla_pages_extend_kernel<<<1, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, seqs, counts, n, slot_mapping,
-                                                                                  positions, total);
-    return launched("launch mla_pages_extend_kernel");
+    return start("launch mla_pages_extend_kernel", mla_pages_extend_kernel, 1, kThreads, stream, p, seqs, counts, n,
+                 slot_mapping, positions, total);
 }
 
 int mla_prolog_pages_fork(const mla_prolog_pool* pool, const int32_t* parents, const int32_t* children, int32_t n,
@@ -533,9 +547,8 @@ int mla_prolog_pages_fork(const mla_prolog_pool* pool, const int32_t* parents, c
     if (rc != MLA_OK || n == 0) return rc;
     int sms;
     if ((rc = current_sm103(&sms)) != MLA_OK) return rc;
-    mla_pages_fork_kernel<<<1, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, parents, children, n, copy_src,
-                                                                                copy_dst);
-    return launched("launch mla_pages_fork_kernel");
+    return start("launch mla_pages_fork_kernel", mla_pages_fork_kernel, 1, kThreads, stream, p, parents, children, n,
+                 copy_src, copy_dst);
 }
 
 int mla_prolog_pages_release(const mla_prolog_pool* pool, const int32_t* seqs, int32_t n, void* stream) {
@@ -545,8 +558,7 @@ int mla_prolog_pages_release(const mla_prolog_pool* pool, const int32_t* seqs, i
     if (rc != MLA_OK || n == 0) return rc;
     int sms;
     if ((rc = current_sm103(&sms)) != MLA_OK) return rc;
-    mla_pages_release_kernel<<<1, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p, seqs, n);
-    return launched("launch mla_pages_release_kernel");
+    return start("launch mla_pages_release_kernel", mla_pages_release_kernel, 1, kThreads, stream, p, seqs, n);
 }
 
 int mla_prolog_pages_compact(const mla_prolog_pool* pool, int32_t* moved_to, int32_t* live, void* stream) {
@@ -556,14 +568,12 @@ int mla_prolog_pages_compact(const mla_prolog_pool* pool, int32_t* moved_to, int
     if ((p.num_pages && !ptr_ok(moved_to, 4)) || (live && !ptr_ok(live, 4))) return MLA_ERR_INVALID_ARG;
     int sms;
     if ((rc = current_sm103(&sms)) != MLA_OK) return rc;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    mla_pages_compact_kernel<<<1, kThreads, 0, st>>>(p, moved_to, live);
-    if ((rc = launched("launch mla_pages_compact_kernel")) != MLA_OK) return rc;
+    rc = start("launch mla_pages_compact_kernel", mla_pages_compact_kernel, 1, kThreads, stream, p, moved_to, live);
     const int64_t entries = static_cast<int64_t>(p.sequences) * p.max_pages;
-    if (entries == 0) return MLA_OK;
+    if (rc != MLA_OK || entries == 0) return rc;
     const int64_t blocks = (entries + 255) / 256;
-    mla_pages_retable_kernel<<<static_cast<int>(blocks < 8 * sms ? blocks : 8 * sms), 256, 0, st>>>(p, moved_to);
-    return launched("launch mla_pages_retable_kernel");
+    return start("launch mla_pages_retable_kernel", mla_pages_retable_kernel,
+                 static_cast<unsigned>(blocks < 8 * sms ? blocks : 8 * sms), 256, stream, p, moved_to);
 }
 
 int mla_prolog_copy_pages(void* cache, int32_t layers, int64_t layer_stride, int64_t num_pages, int64_t page_bytes,
@@ -585,10 +595,8 @@ int mla_prolog_copy_pages(void* cache, int32_t layers, int64_t layer_stride, int
     const int per = many ? 8 : 1;
     const int64_t step_bytes = kCopyStep * 16;
     const int pieces = many ? 1 : static_cast<int>(std::min<int64_t>((page_bytes + step_bytes - 1) / step_bytes, 16));
-    mla_copy_pages_kernel<<<dim3((n + per - 1) / per, layers, pieces), kCopyThreads, 0,
-                            static_cast<cudaStream_t>(stream)>>>(static_cast<uint8_t*>(cache), layer_stride, num_pages,
-                                                                 page_bytes, src, dst, n, per, pieces, status);
-    return launched("launch mla_copy_pages_kernel");
+    return start("launch mla_copy_pages_kernel", mla_copy_pages_kernel, dim3((n + per - 1) / per, layers, pieces), kCopyThreads,
+                 stream, static_cast<uint8_t*>(cache), layer_stride, num_pages, page_bytes, src, dst, n, per, pieces, status);
 }
 
 }  // extern "C"
