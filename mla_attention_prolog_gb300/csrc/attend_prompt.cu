@@ -15,6 +15,10 @@
 // tiles fill the 512 columns of TMEM exactly (v_dim <= 128).  Warp roles: 0-3
 // and 4-7 softmax of tile 0 and 1, 8 issues the MMAs, 9 the TMA loads.
 //
+// With few tile pairs a cluster of 2, 4 or 8 CTAs takes each: every CTA the
+// key tiles of its rank, with its own maximum and sum, and the rows are joined
+// through the cluster's shared memory.
+//
 // The maximum that P is scaled by moves only when a row's maximum has grown
 // by more than 2^8: until then P <= 2^8, which neither BF16 nor the FP32 sums
 // mind, and O need not be rescaled.
@@ -31,6 +35,8 @@ constexpr int kSlotBytes = kTile * 128;    // 128 rows x 64 BF16 columns: one TM
 constexpr int kMaxSlots = 8;
 constexpr int kAhead = 4;                  // K (V) tiles whose barriers are in use at once
 constexpr int kThreads = 320;
+constexpr int kMaxShift = 3;               // at most 8 CTAs share a tile pair's keys,
+constexpr int kSplitTiles = 6;             //   of sequences of this many key tiles on average
 constexpr int kMmaWarp = 8, kLoadWarp = 9;
 constexpr int kMiscBytes = 512;
 constexpr int kSmemMax = 232448;           // 227 KB
@@ -52,6 +58,7 @@ struct PromptParams {
     float scale;
     int causal, q_per_head;
     int slots;        // ring slots
+    int shift;        // log2 of the CTAs that share a tile pair's keys
     int tile_bound;   // >= 256-row tiles of all sequences
     int head_group;   // query heads whose K and V stay in L2 together
 };
@@ -174,6 +181,76 @@ __device__ __forceinline__ void clean_v(uint32_t smem, int chunks, int row, bool
     }
 }
 
+// Joins what the S CTAs of a cluster made of a tile pair's rows, each from its
+// share of the keys: O (not divided by the row sum) and, behind it, (ms, sum) of
+// every row lie in each one's shared memory at `sm`, with rows of `pitch`
+// bytes whose 16-byte pieces are turned by the row.  Each CTA takes 256 / S of
+// the rows, a warp 32 / S, eight loads of O in flight.
+template <int S, class RowsOf, class Limit>
+__device__ __forceinline__ void join_rows(const PromptParams& p, const Job& jb, int h, int hk, uint32_t sm, int pitch,
+                                          uint32_t bad, int first_masked, int rank, RowsOf rows_of, Limit limit) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t sm_of[S], words = 0;  // lane w: word w of the keys whose v holds a NaN or an infinity, of any CTA
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+        sm_of[k] = map_shared_rank(sm, k);
+        if (lane < 12) words |= ld_cluster_u32(map_shared_rank(bad, k) + lane * 4);
+    }
+    const uint32_t any_bad = __ballot_sync(~0u, words != 0);
+    const bool in = lane * 4 < p.Dv;
+    constexpr int kAtOnce = 8 / S;
+#pragma unroll 1
+    for (int k0 = 0; k0 < 32 / S; k0 += kAtOnce) {
+        const int row0 = rank * (2 * kTile / S) + warp * (32 / S) + k0;
+        float4 o[kAtOnce][S];
+        float2 st[kAtOnce][S];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+                const int r = row0 + i;
+                st[i][k] = ld_cluster_f2(sm_of[k] + 2 * kTile * pitch + r * 8);
+                o[i][k] = in ? ld_cluster_f4(sm_of[k] + r * pitch + ((lane ^ (r & 7)) << 4)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            const int t = (row0 + i) / kTile, r = (row0 + i) % kTile;
+            if (r >= rows_of(t)) continue;
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < S; ++k)
+                if (st[i][k].y != 0.f) top = fmaxf(top, st[i][k].x);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < S; ++k) {
+                if (st[i][k].y == 0.f) continue;  // no key of this share: its O was not written
+                const float w = ex2(st[i][k].x - top);
+                sum = fmaf(w, st[i][k].y, sum);
+                acc.x = fmaf(w, o[i][k].x, acc.x), acc.y = fmaf(w, o[i][k].y, acc.y);
+                acc.z = fmaf(w, o[i][k].z, acc.z), acc.w = fmaf(w, o[i][k].w, acc.w);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            float v[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+            const int row = jb.r0 + t * kTile + r, lim = limit(row);
+            if (any_bad)
+                for (int w = 0; w < 12; ++w)
+                    for (uint32_t bits = __shfl_sync(~0u, words, w); bits; bits &= bits - 1) {
+                        const int key = (first_masked + w / 4) * kTile + (w & 3) * 32 + __ffs(bits) - 1;
+                        if (key >= lim || !in) continue;
+                        const uint16_t* x = p.v + ((static_cast<int64_t>(jb.k0) + key) * p.Hk + hk) * p.Dv + lane * 4;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if ((x[e] & 0x7F80) == 0x7F80) v[e] += __uint_as_float(static_cast<uint32_t>(x[e]) << 16);
+                    }
+            const int64_t at = (static_cast<int64_t>(jb.q0) + row) * p.H + h;
+            if (in)
+                *reinterpret_cast<uint2*>(p.out + at * p.Dv + lane * 4) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+            if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : top * kLn2 + logf(sum);
+        }
+    }
+}
+
+template <bool kSplit>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_attend_prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                              const __grid_constant__ CUtensorMap tm_v, const PromptParams p) {
@@ -185,9 +262,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     Shared* sh = reinterpret_cast<Shared*>(raw + pad + (2 * nqk + p.slots) * kSlotBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    // blockIdx -> (group of heads, tile pair, head of the group)
+    // blockIdx -> (group of heads, tile pair, head of the group, share of the keys)
+    const int shift = kSplit ? p.shift : 0, split = 1 << shift, rank = blockIdx.x & (split - 1);
     const int per_group = p.head_group * p.tile_bound;
-    const int g = blockIdx.x / per_group, in_group = blockIdx.x % per_group;
+    const int g = (blockIdx.x >> shift) / per_group, in_group = (blockIdx.x >> shift) % per_group;
     const int width = min(p.head_group, p.H - g * p.head_group);
     const int tile = in_group / width, h = g * p.head_group + in_group % width;
     const int hk = h / (p.H / p.Hk);
@@ -241,10 +319,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int rows = rows_of(t);
         return rows ? (limit(jb.r0 + t * kTile + rows - 1) + kTile - 1) / kTile : 0;
     };
-    const int n0 = tiles_of(0), n1 = tiles_of(1), nmax = max(n0, n1);
+    // this CTA's key tiles: the rank-th of every `split` (the tiles at a causal row's end hold less work)
+    auto share = [&](int n) { return (max(n - rank, 0) + split - 1) >> shift; };
+    const int n0 = share(tiles_of(0)), n1 = share(tiles_of(1)), nmax = max(n0, n1);
     const int first_masked = limit(jb.r0) / kTile;
     const int span = nqk + nv;  // ring slots per key tile: K's, then V's
     auto phase_of = [&](int j) { return static_cast<uint32_t>(j / kAhead) & 1u; };  // of key tile j's barriers
+    const int pitch = (p.Dv + 31) / 32 * 128;  // bytes of a row of O in shared memory
     const volatile int* abort_flag = &sh->abort_flag;
     bool ok = true;
 
@@ -308,6 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lim0 = limit(jb.r0 + t * kTile);  // of the tile's first row, which sees the fewest
         float m = -INFINITY, ms = 0.f, l = 0.f;     // row maximum of S, ms = m c, row sum of P
         for (int j = 0; j < n; ++j) {
+            const int key0 = ((j << shift) + rank) * kTile;
             ok = mbar_wait(smem_u32(&sh->s_full[t]), j & 1, kTimeoutNs, abort_flag);
             if (!__all_sync(~0u, ok)) {
                 ok = false;
@@ -316,9 +398,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             uint32_t s[kTile];
             float mt = tmem_ld128_max(ts, s);  // of the row
-            const bool masked = (j + 1) * kTile > lim0;
+            const bool masked = key0 + kTile > lim0;
             if (masked) {
-                const int left = lim - j * kTile;
+                const int left = lim - key0;
 #pragma unroll
                 for (int i = 0; i < kTile; ++i)
                     if (i >= left) s[i] = 0xFF800000u;
@@ -383,72 +465,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 for (int cidx = 0; cidx < nv; ++cidx)
-                    clean_v(sm_ring + (use + cidx) % p.slots * kSlotBytes, 1, r, j * kTile + r < jb.nk,
-                            sh->bad + (j - first_masked) * 4);
+                    clean_v(sm_ring + (use + cidx) % p.slots * kSlotBytes, 1, r, key0 + r < jb.nk,
+                            sh->bad + (key0 / kTile - first_masked) * 4);
                 fence_proxy_async_shared();
             }
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(smem_u32(&sh->p_full[t]));
         }
-        if (ok && rows) {
-            if (n) {
-                ok = mbar_wait(smem_u32(&sh->o_done[t]), (n - 1) & 1, kTimeoutNs, abort_flag);
-                ok = __all_sync(~0u, ok);
-                tc_fence_after();
-            }
-            if (ok) {
-                uint32_t any_bad = 0;
-#pragma unroll
-                for (int i = 0; i < 12; ++i) any_bad |= *const_cast<volatile uint32_t*>(sh->bad + i);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                // A warp's rows pass through its part of the tile's Q (no score is left to make), 64 columns at a
-                // time, so that it stores four rows' whole lines at once.
-                const uint32_t stage = sm_q + t * nqk * kSlotBytes + (warp & 3) * 32 * 128;
-                const int64_t row_bytes = static_cast<int64_t>(p.H) * p.Dv * 2;
-                uint8_t* rows_out = reinterpret_cast<uint8_t*>(p.out + (at - static_cast<int64_t>(lane) * p.H) * p.Dv);
-                const int wrows = clampi(rows - (warp & 3) * 32, 0, 32);
+        if (ok && n) {
+            ok = mbar_wait(smem_u32(&sh->o_done[t]), (n - 1) & 1, kTimeoutNs, abort_flag);
+            ok = __all_sync(~0u, ok);
+            tc_fence_after();
+        }
+        if (kSplit) {
+            // The tiles have been read when both warpgroups' products are made: O and the sums take their place.
+            const bool all = named_bar_and(1, 2 * kTile, ok);
+            if (all) {
+                const uint32_t sm_o = sm_q + (t * kTile + r) * pitch;
+                if (n)
 #pragma unroll 1
-                for (int d = 0; d < p.Dv; d += 64) {
-                    float o[64];  // (what lies behind v_dim is not stored)
-                    if (n) {
-                        uint32_t raw_o[64];
-                        tmem_ld64_raw(to + d, raw_o);
+                    for (int d = 0; d < p.Dv; d += 32) {  // (what lies behind v_dim is not read)
+                        float o[32];
+                        tmem_ld32(to + d, o);
 #pragma unroll
-                        for (int i = 0; i < 64; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(raw_o[i]) * inv;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) o[i] = 0.f;
+                        for (int i = 0; i < 8; ++i)
+                            st_shared_v4(sm_o + (((d / 4 + i) ^ (r & 7)) << 4), __float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]),
+                                         __float_as_uint(o[4 * i + 2]), __float_as_uint(o[4 * i + 3]));
                     }
-                    if (any_bad) {
-                        for (int w = 0; w < 12; ++w)
-                            for (uint32_t bits = *const_cast<volatile uint32_t*>(sh->bad + w); bits; bits &= bits - 1) {
-                                const int key = (first_masked + w / 4) * kTile + (w & 3) * 32 + __ffs(bits) - 1;
-                                if (key >= lim) continue;
-                                const uint16_t* v = p.v + ((static_cast<int64_t>(jb.k0) + key) * p.Hk + hk) * p.Dv + d;
-#pragma unroll
-                                for (int i = 0; i < 64; ++i)
-                                    if (d + i < p.Dv && (v[i] & 0x7F80) == 0x7F80)
-                                        o[i] += __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
-                            }
-                    }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        st_shared_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), pack_bf16x2(o[8 * i], o[8 * i + 1]),
-                                     pack_bf16x2(o[8 * i + 2], o[8 * i + 3]), pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
-                                     pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
-                    __syncwarp();
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int row2 = i * 4 + (lane >> 3), col = d + (lane & 7) * 8;
-                        uint4 v;
-                        ld_shared_v4(stage + row2 * 128 + (((lane & 7) ^ (row2 & 7)) << 4), v.x, v.y, v.z, v.w);
-                        if (row2 < wrows && col < p.Dv) *reinterpret_cast<uint4*>(rows_out + row2 * row_bytes + col * 2) = v;
-                    }
-                    __syncwarp();
-                }
-                if (mine && p.lse) p.lse[at] = l == 0.f ? -INFINITY : ms * kLn2 + logf(l);
+                st_shared_v2(sm_q + 2 * kTile * pitch + (t * kTile + r) * 8, __float_as_uint(ms), __float_as_uint(l));
             }
+        } else if (ok && rows) {
+            uint32_t any_bad = 0;
+#pragma unroll
+            for (int i = 0; i < 12; ++i) any_bad |= *const_cast<volatile uint32_t*>(sh->bad + i);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            // A warp's rows pass through its part of the tile's Q (no score is left to make), 64 columns at a
+            // time, so that it stores four rows' whole lines at once.
+            const uint32_t stage = sm_q + t * nqk * kSlotBytes + (warp & 3) * 32 * 128;
+            const int64_t row_bytes = static_cast<int64_t>(p.H) * p.Dv * 2;
+            uint8_t* rows_out = reinterpret_cast<uint8_t*>(p.out + (at - static_cast<int64_t>(lane) * p.H) * p.Dv);
+            const int wrows = clampi(rows - (warp & 3) * 32, 0, 32);
+#pragma unroll 1
+            for (int d = 0; d < p.Dv; d += 64) {
+                float o[64];  // (what lies behind v_dim is not stored)
+                if (n) {
+                    uint32_t raw_o[64];
+                    tmem_ld64_raw(to + d, raw_o);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) o[i] = l == 0.f ? 0.f : __uint_as_float(raw_o[i]) * inv;
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i) o[i] = 0.f;
+                }
+                if (any_bad) {
+                    for (int w = 0; w < 12; ++w)
+                        for (uint32_t bits = *const_cast<volatile uint32_t*>(sh->bad + w); bits; bits &= bits - 1) {
+                            const int key = (first_masked + w / 4) * kTile + (w & 3) * 32 + __ffs(bits) - 1;
+                            if (key >= lim) continue;
+                            const uint16_t* v = p.v + ((static_cast<int64_t>(jb.k0) + key) * p.Hk + hk) * p.Dv + d;
+#pragma unroll
+                            for (int i = 0; i < 64; ++i)
+                                if (d + i < p.Dv && (v[i] & 0x7F80) == 0x7F80)
+                                    o[i] += __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    st_shared_v4(stage + lane * 128 + ((i ^ (lane & 7)) << 4), pack_bf16x2(o[8 * i], o[8 * i + 1]),
+                                 pack_bf16x2(o[8 * i + 2], o[8 * i + 3]), pack_bf16x2(o[8 * i + 4], o[8 * i + 5]),
+                                 pack_bf16x2(o[8 * i + 6], o[8 * i + 7]));
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int row2 = i * 4 + (lane >> 3), col = d + (lane & 7) * 8;
+                    uint4 v;
+                    ld_shared_v4(stage + row2 * 128 + (((lane & 7) ^ (row2 & 7)) << 4), v.x, v.y, v.z, v.w);
+                    if (row2 < wrows && col < p.Dv) *reinterpret_cast<uint4*>(rows_out + row2 * row_bytes + col * 2) = v;
+                }
+                __syncwarp();
+            }
+            if (mine && p.lse) p.lse[at] = l == 0.f ? -INFINITY : ms * kLn2 + logf(l);
         }
     } else if (warp == kMmaWarp) {
         // ---------------------------------------------------------------- MMA
@@ -574,7 +671,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++sent;
             mbar_arrive_expect_tx(smem_u32(&full[j % kAhead]), chunks * kSlotBytes);
             for (int c = 0; c < chunks; ++c) {
-                tma_load_3d(sm_ring + slot * kSlotBytes, map, smem_u32(&full[j % kAhead]), c * 64, hk, jb.k0 + j * kTile);
+                tma_load_3d(sm_ring + slot * kSlotBytes, map, smem_u32(&full[j % kAhead]), c * 64, hk,
+                            jb.k0 + ((j << shift) + rank) * kTile);
                 if (++slot == p.slots) slot = 0;
             }
         };
@@ -606,6 +704,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (kSplit) {
+        __syncwarp();
+        cluster_sync_all();
+        if (warp < 8) {
+            auto join = [&](auto s) {
+                join_rows<decltype(s)::value>(p, jb, h, hk, sm_q, pitch, smem_u32(sh->bad), first_masked, rank, rows_of, limit);
+            };
+            if (split == 2) join(Steps<2>());
+            else if (split == 4) join(Steps<4>());
+            else join(Steps<8>());
+        }
+        __syncwarp();
+        cluster_sync_all();  // no CTA leaves while another reads its shared memory
+    }
+}
+
+// Clusters of 1 << shift CTAs of the current device that run at the same time
+// (asked of the driver once per device).
+cudaError_t clusters_at_once(int shift, int* most) {
+    static std::atomic<int> known[64][kMaxShift + 1];  // 0: not asked yet, else the answer + 1
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) {
+        const int k = known[dev][shift].load(std::memory_order_acquire);
+        if (k) return *most = k - 1, cudaSuccess;
+    }
+    static std::atomic<uint64_t> ready{0};
+    e = allow_smem(&mla_attend_prompt_kernel<true>, kSmemMax, &ready);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(1u << shift);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemMax;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << shift;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    e = cudaOccupancyMaxActiveClusters(most, &mla_attend_prompt_kernel<true>, &cfg);
+    if (e == cudaSuccess && dev < 64) known[dev][shift].store(*most + 1, std::memory_order_release);
+    return e;
 }
 
 }  // namespace
@@ -629,10 +770,11 @@ extern "C" int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* d, const v
     if (!ptr_ok(q, 16) || !ptr_ok(out, 16) || !ptr_ok(cu_q, 4) || !ptr_ok(cu_k, 4)) return MLA_ERR_INVALID_ARG;
     if (d->Tk && (!ptr_ok(k, 16) || !ptr_ok(v, 16))) return MLA_ERR_INVALID_ARG;
     if ((lse && !ptr_ok(lse, 4)) || (status && !ptr_ok(status, 4))) return MLA_ERR_INVALID_ARG;
-    // 256-row tiles: at most one ragged tile per sequence that holds a row
+    // 256-row tiles of sequences that hold a row: each wastes 255 rows at most
     const int64_t ragged = d->sequences < d->Tq ? d->sequences : d->Tq;
-    const int64_t tiles = d->Tq / (2 * kTile) + ragged;
-    if (tiles * d->num_heads > INT32_MAX) return MLA_ERR_UNSUPPORTED_DIMS;
+    const int64_t tiles = (d->Tq + (2 * kTile - 1) * ragged) / (2 * kTile);
+    const int64_t jobs = tiles * d->num_heads;
+    if (jobs > INT32_MAX) return MLA_ERR_UNSUPPORTED_DIMS;
     int sms;
     const int rc = current_sm103(&sms);
     if (rc != MLA_OK) return rc;
@@ -658,14 +800,41 @@ extern "C" int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* d, const v
     const int per_kv = d->num_heads / d->kv_heads;
     int64_t group = kv_bytes > 0 ? (int64_t(48) << 20) / kv_bytes : d->kv_heads;
     group = (group < 1 ? 1 : group > d->kv_heads ? d->kv_heads : group) * per_kv;
+    // Few tile pairs with many keys: a cluster shares a tile pair's keys, as large a one as leaves room for all of
+    // them at once.  In us, on 1 / 2 / 4 / 8 CTAs, D 192: 4 pairs of 156 key tiles 218 / 115 / 63 / 37; 16 pairs
+    // 220 / 116 / 65 / 78 (their clusters of 8 do not fit at once); 32 pairs of 64 tiles 125 / 72 / 44 / 77; 64 pairs
+    // of 8 tiles 21.8 / 19.8 / 30 / 67; 128 pairs of 32 tiles 60 / 77.  Short ones have nothing to share: 16 pairs of
+    // 2 tiles 12.1 / 14.2 / 13.9 / 26.
+    int shift = 0;
+    if (d->Tk >= kSplitTiles * kTile * static_cast<int64_t>(d->sequences)) {
+        for (shift = kMaxShift; shift > 0; --shift) {
+            int most = 0;
+            const cudaError_t e = clusters_at_once(shift, &most);
+            if (e != cudaSuccess) return report_cuda(e, "clusters of mla_attend_prompt_kernel");
+            if (jobs <= most) break;
+        }
+    }
     PromptParams p{int8 ? static_cast<const int8_t*>(q) : nullptr, q_scale, static_cast<const uint16_t*>(v), cu_q, cu_k,
                    static_cast<uint16_t*>(out), lse, status, d->Tq, d->Tk, d->sequences, d->num_heads, d->kv_heads,
-                   d->qk_dim, d->v_dim, d->scale, (d->flags & MLA_PROMPT_CAUSAL) != 0, per_head, slots,
+                   d->qk_dim, d->v_dim, d->scale, (d->flags & MLA_PROMPT_CAUSAL) != 0, per_head, slots, shift,
                    static_cast<int>(tiles), static_cast<int>(group)};
-    static std::atomic<uint64_t> ready{0};
-    cudaError_t e = allow_smem(&mla_attend_prompt_kernel, kSmemMax, &ready);
+    static std::atomic<uint64_t> ready[2];
+    auto kernel = shift ? &mla_attend_prompt_kernel<true> : &mla_attend_prompt_kernel<false>;
+    cudaError_t e = allow_smem(kernel, kSmemMax, &ready[shift ? 1 : 0]);
     if (e != cudaSuccess) return report_cuda(e, "mla_attend_prompt_kernel attributes");
-    e = launch_kernel(mla_attend_prompt_kernel, dim3(static_cast<unsigned>(tiles * d->num_heads)), dim3(kThreads), smem,
-                      static_cast<cudaStream_t>(stream), true, tq, tk, tv, p);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3(static_cast<unsigned>(jobs << shift));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = shift ? 2 : 1;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1u << shift;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    e = cudaLaunchKernelEx(&cfg, kernel, tq, tk, tv, p);
     return e == cudaSuccess ? MLA_OK : report_cuda(e, "launch mla_attend_prompt_kernel");
 }

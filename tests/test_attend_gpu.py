@@ -250,6 +250,47 @@ def test_prompt_one_query_on_many_keys():
     check_prompt(c, out, lse)
 
 
+@pytest.mark.parametrize("H", [2, 20, 60])   # clusters of 8, 4 and 2 CTAs on a tile pair's keys
+@pytest.mark.parametrize("dims,q", [((192, 128), "bf16"), ((192, 128), "int8"), ((80, 48), "bf16"), ((256, 112), "bf16"),
+                                    ((16, 16), "int8_per_head")])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prompt_keys_shared_by_a_cluster(H, dims, q, causal):
+    for new, total in (([130], [1531]), ([256], [769]), ([1], [1000])):
+        c = prompt_case(26, new, total, H, H // 2, *dims, q=q)
+        out, lse, status = run_prompt(c, causal)
+        assert status == 0
+        check_prompt(c, out, lse, causal)
+    again, lse2, _ = run_prompt(c, causal)
+    assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)
+
+
+def test_prompt_clusters_with_uneven_sequences():
+    """Clusters whose CTAs have a key tile, or none, and rows that see no key."""
+    for H in (1, 10, 30):
+        c = prompt_case(27, [5, 260], [2400, 131], H, 1, 192, 128)
+        out, lse, status = run_prompt(c)
+        assert status == 0
+        check_prompt(c, out, lse)
+
+
+@pytest.mark.parametrize("H", [2, 20, 60])
+def test_prompt_clusters_and_hidden_keys(H):
+    c = prompt_case(28, [300], [1000], H, 2, 192, 128)
+    c["v"][900, 0, 5] = math.inf    # seen by the queries from 200 on
+    c["v"][910, 1, 7] = NAN
+    c["k"][950, 0] = NAN
+    out, lse, _ = run_prompt(c)
+    clean = {**c, "k": c["k"].clone(), "v": c["v"].clone()}
+    clean["k"][900:], clean["v"][900:] = 1.0, 1.0
+    want, want_lse, _ = run_prompt(clean)
+    h = H // 2   # heads of key head 0
+    assert torch.equal(out[:200].view(torch.int16), want[:200].view(torch.int16)) and torch.equal(lse[:200], want_lse[:200])
+    assert (out[200:250, :h, 5] == math.inf).all() and torch.isfinite(out[:250, :h, :5]).all()
+    assert torch.isnan(out[210:300, h:, 7]).all() and torch.isfinite(out[:210, h:, 7]).all()
+    assert torch.isfinite(out[:300, h:, 8:]).all() and torch.isfinite(lse[:250, :h]).all()
+    assert torch.isnan(out[250:300, :h]).all() and torch.isnan(lse[250:300, :h]).all()
+
+
 def test_prompt_and_cache_calls_at_once():
     """Prompts and decoding steps on three streams at the same time."""
     ps = [prompt_case(23, [700, 90], [700, 90], 4, 4, 192, 128), prompt_case(24, [33, 300], [133, 300], 4, 4, 192, 128)]
