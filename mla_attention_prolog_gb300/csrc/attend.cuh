@@ -11,6 +11,10 @@
 
 namespace mlap {
 
+constexpr int kStatusSeqRange = MLA_STATUS_SEQ_RANGE;
+constexpr int kStatusPageRange = MLA_STATUS_PAGE_RANGE;
+constexpr int kStatusPoolFull = MLA_STATUS_POOL_FULL;
+
 // api.cu: the error text of mla_prolog_last_cuda_error(), and the driver's
 // cuTensorMapEncodeTiled (null where the driver has none).
 int report_cuda(cudaError_t e, const char* where);

@@ -24,7 +24,7 @@
 #include <cstdint>
 
 #include "attend.cuh"
-#include "ptx.cuh"
+#include "attend_ptx.cuh"
 
 namespace mlap {
 namespace {
@@ -41,7 +41,7 @@ constexpr int kStageBytes = 4 * 32 * 128;  // where results pass through on thei
 static_assert(2 * kPBytes <= kStageBytes, "");
 constexpr int kThreads = 192;
 constexpr int kMmaWarp = 4, kLoadWarp = 5;
-constexpr int kMiscBytes = 1536;
+constexpr int kMiscBytes = 2048;
 constexpr int kSmemQ = kMaxChunks * kQBytes, kSmemK = 2 * kMaxChunks * kKBytes, kSmemV = 2 * kMaxValues * kVBytes;
 constexpr int kSmem = 1024 + kMiscBytes + kSmemQ + kSmemK + kSmemV + kStageBytes;
 static_assert(kSmem <= 232448, "227 KB");
@@ -108,6 +108,11 @@ __device__ __forceinline__ int64_t seq_cost(const CacheParams& p, int steps) {
     return steps ? static_cast<int64_t>(p.head_tiles) * (steps + p.overhead) : 0;
 }
 
+// Most quotients here fit 32 bits, whose division takes a third of the time.
+__device__ __forceinline__ int quotient(int64_t a, int b) {
+    return static_cast<int>(a <= INT32_MAX ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b);
+}
+
 // The steps [*j0, *j1) of a tile of `steps` at cost `base` that the costs
 // [from, to) cover.
 __device__ __forceinline__ void covered(const CacheParams& p, int64_t base, int steps, int64_t from, int64_t to, int* j0,
@@ -132,7 +137,9 @@ struct Piece {
     bool prefix, whole;  // whole: covers the tile's keys
 };
 
-// A unit's walk over its pieces; every role walks on its own.
+// A unit's walk over its pieces; every warp walks on its own, one lane of it,
+// with its state in shared memory (on the stack it fell out of what L1 the
+// tiles leave: 1.2 to 3 us a piece against 0.4).
 struct Walk {
     int64_t at, end, prefix_cost, base;  // base: cost before batch row b
     int shared, source_row, b, len, row, unit;
@@ -149,7 +156,7 @@ struct Walk {
             int steps;
             if (at < prefix_cost) {
                 steps = shared / kKeys;
-                const int t = static_cast<int>(at / (steps + p.overhead));
+                const int t = quotient(at, steps + p.overhead);
                 tile_base = static_cast<int64_t>(t) * (steps + p.overhead);
                 x->row0 = t * kRows;
                 x->rows = min(kRows, p.B * p.H - x->row0);
@@ -167,7 +174,7 @@ struct Walk {
                     steps = own_steps(len, shared);
                 }
                 if (b >= p.B) return false;
-                const int ht = static_cast<int>((at - base) / (steps + p.overhead));
+                const int ht = p.head_tiles == 1 ? 0 : quotient(at - base, steps + p.overhead);
                 tile_base = base + static_cast<int64_t>(ht) * (steps + p.overhead);
                 x->row0 = b * p.H + ht * kRows;
                 x->rows = min(kRows, p.H - ht * kRows);
@@ -202,6 +209,8 @@ struct Shared {
     int64_t scan[kThreads / 32];
     int64_t total, first_base;
     int first_b, sharers, source, shared;
+    Walk walk[kThreads / 32];
+    Piece piece[kThreads / 32];  // the next one of each
 };
 static_assert(sizeof(Shared) <= kMiscBytes, "");
 
@@ -258,13 +267,14 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
     }
     const int source = sh->source;
     const int64_t prefix = shared ? static_cast<int64_t>(p.row_tiles) * (shared / kKeys + p.overhead) : 0;
-    int64_t total = prefix, sum;
+    int64_t total = prefix, sum, first_base = 0, first_cost = 0;
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         const int len = len_of(b);
         const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
         const int64_t before = total + block_scan(mine, sh->scan, &sum);
         if (writer && b < p.B) p.bases[b] = before;
+        if (b0 == 0) first_base = before, first_cost = mine;
         total += sum;
     }
     int64_t run = (total + p.units - 1) / p.units;
@@ -286,11 +296,8 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
     if (shared) batch_len(p, source, &w->source_row, &bits);
     if (w->at >= prefix) {  // the batch row that holds `at`
         if (p.B <= kThreads) {
-            const int b = threadIdx.x;
-            const int len = len_of(b);
-            const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
-            const int64_t before = prefix + block_scan(mine, sh->scan, &sum);
-            if (mine && w->at >= before && w->at < before + mine) sh->first_b = b, sh->first_base = before;
+            if (first_cost && w->at >= first_base && w->at < first_base + first_cost)
+                sh->first_b = threadIdx.x, sh->first_base = first_base;
         } else {
             int64_t base = prefix;
             for (int b0 = 0; b0 < p.B; b0 += kThreads) {
@@ -313,8 +320,8 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
 
 __global__ void __launch_bounds__(kThreads, 1)
     mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
-                            const __grid_constant__ CUtensorMap tm_k4, const __grid_constant__ CUtensorMap tm_v4,
-                            const CacheParams p) {
+                            const __grid_constant__ CUtensorMap tm_q4, const __grid_constant__ CUtensorMap tm_k4,
+                            const __grid_constant__ CUtensorMap tm_v4, const __grid_constant__ CacheParams p) {
     extern __shared__ uint8_t raw[];
     const uint32_t raw_at = smem_u32(raw);
     const uint32_t pad = (1024u - (raw_at & 1023u)) & 1023u;  // the same in both CTAs of a pair
@@ -325,9 +332,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int unit = blockIdx.x / 2, rank = blockIdx.x % 2;
     const int v0 = rank * p.dv_half, nvc = (p.dv_half + 63) / 64;  // value columns that this CTA brings
 
-    pdl_wait();  // what the kernel before in the stream wrote
-    Walk walk;
-    if (!make_cut(p, unit, sh, &walk)) return;
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh->k_full[i]), 1);
@@ -347,18 +351,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh->drain), 1);
         sh->abort_flag = 0;
         fence_barrier_init();
-        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_q4);
         prefetch_tensormap(&tm_c);
+        prefetch_tensormap(&tm_k4);
+        prefetch_tensormap(&tm_v4);
     }
     if (warp == kMmaWarp) {
         tmem_alloc_pair(smem_u32(&sh->tmem), 512);
         tmem_relinquish_pair();
     }
     tc_fence_before();
+    pdl_wait();  // what the kernel before in the stream wrote
+    __syncwarp();
+    cluster_arrive();  // the peer's barriers are ready once both have come here; the cut is made meanwhile
+    Walk start;
+    const bool any = make_cut(p, unit, sh, &start);
+    if (lane == 0) sh->walk[warp] = start;
+    cluster_wait();
     __syncthreads();
-    cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem = sh->tmem;
+    if (!any) {  // (the same in both CTAs)
+        if (warp == kMmaWarp) tmem_dealloc_pair(tmem, 512);
+        return;
+    }
     const volatile int* abort_flag = &sh->abort_flag;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
         return mbar_wait_lean(smem_u32(bar), parity & 1u, kTimeoutNs, abort_flag);
@@ -366,6 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int step = 0;  // key steps so far, over all pieces: the phase of every barrier
     Piece x;
+    Walk& walk = sh->walk[warp];
+    Piece& next = sh->piece[warp];
+    // The warp's next piece, which one lane has found (`got`) or finds now.
+    auto take = [&](bool got) {
+        __syncwarp();
+        x = next;
+        return __shfl_sync(~0u, static_cast<int>(got), 0) != 0;
+    };
 
     if (warp < 4) {
         // ------------------------------------------------------------ softmax
@@ -381,7 +405,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float c = p.scale * kLog2e;
         int tails = 0;  // steps so far that ended inside
         const int dv0 = side * p.dv_half, dv = min(p.dv_half, p.Lkv - dv0);  // value columns of this thread
-        while (ok && walk.next(p, &x)) {
+        bool got = lane == 0 && walk.next(p, &next);
+        while (ok && take(got)) {
             const bool mine = tile_row < x.rows;
             const int n = x.n, keys = x.end - x.key0;
             float m = -INFINITY, ms = 0.f, l = 0.f;  // row maximum of S, ms = m c, sum of this thread's half of P
@@ -470,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_before();
                 arrive(p_full + 8 * (step & 1));
             }
+            got = lane == 0 && walk.next(p, &next);  // while the last products run
             sh->row_sum[threadIdx.x] = l;
             ok = __all_sync(~0u, ok && wait(&sh->pv_done[(step - 1) & 1], (step - 1) >> 1));
             if (named_bar_or(1, 128, !ok)) {
@@ -481,10 +507,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // A row whose keys this piece covers alone is finished; the others leave a partial result.
             bool direct = x.whole;
             const int b = (x.row0 + tile_row) / p.H;
-            if (walk.shared && direct && mine) {
+            if (start.shared && direct && mine) {
                 int trow, bits = 0;
                 const int len = batch_len(p, b, &trow, &bits);
-                direct = x.prefix ? len == walk.shared : len < walk.shared;
+                direct = x.prefix ? len == start.shared : len < start.shared;
             }
             // A warp's rows pass through shared memory, 128 bytes of each at a time, so that it stores four rows'
             // whole lines at once: 64 columns of finished rows, 32 of partial ones.
@@ -564,7 +590,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 return ok;
             };
             auto commit = [&](uint64_t* bar) { mma_commit_pair(smem_u32(bar), 0x3); };
-            for (int piece = 0; walk.next(p, &x); ++piece) {
+            bool got = walk.next(p, &next);
+            for (int piece = 0; got; ++piece) {
+                x = next;
                 const int n = x.n;
                 if (!look(&sh->q_full, piece)) break;
                 // Per round: the scores of step t, then P V of step t - 2, whose softmax ran meanwhile.
@@ -589,7 +617,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         commit(&sh->s_full[f4]);
                         commit(&sh->k_free[e]);
-                        if (t + 1 == n) commit(&sh->q_free);
+                        if (t + 1 == n) {
+                            commit(&sh->q_free);
+                            got = walk.next(p, &next);
+                        }
                     }
                     if (t > 1) {
                         const int pv = st - 2, f = pv & 1;
@@ -627,35 +658,51 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool whole = p.box >= 32 && p.C == 64 * kMaxChunks && p.dv_half == 256;
         auto at_even = [&](uint64_t* bar) { return map_shared_rank(smem_u32(bar), 0); };
         int bits = 0, pieces = 0, ks = 0, vs = 0;  // Q, K and V places filled
-        while (ok && walk.next(p, &x)) {
-            const int n = x.n, key0 = x.key0, end = x.end;
-            const int32_t* row_table = p.table + static_cast<int64_t>(x.page_row) * p.max_pages;
+        // first row of box `lane` of the batch that starts at a piece's step j; a row outside the cache reads as zeros
+        auto look_up = [&](const Piece& y, int j) {
+            const int key = y.key0 + (j * per + lane) * p.box;
+            if (j * per + lane >= y.n * per || key >= y.end) return p.num_rows;
+            const int page = p.table[static_cast<int64_t>(y.page_row) * p.max_pages + key / p.page_size];
+            if (page >= 0 && page < p.num_pages) return page * p.page_size + key % p.page_size;
+            bits |= kStatusPageRange;
+            return p.num_rows;
+        };
+        // Asks L2 for this lane's box of cache rows, which lie in one piece of memory.
+        auto fetch = [&](int row) {
+            if (row < p.num_rows) bulk_prefetch_l2(p.cache + static_cast<int64_t>(row) * p.C, p.box * p.C * 2);
+        };
+        // The first steps of a piece, which is found and asked of L2 while the one before still runs.
+        auto begin = [&](const Piece& y) {
+            const int rows = look_up(y, 0);
+            if (!y.prefix && lane / per < batch && lane / per < kFetch && (lane / per & 1) == rank) fetch(rows);
+            const int mine = min(64, y.rows - rank * 64);  // this CTA's rows of Q
+            if (lane == 31 && mine > 0)
+                bulk_prefetch_l2(p.q + (static_cast<int64_t>(y.row0) + rank * 64) * p.C, mine * p.C * 2);
+            return rows;
+        };
+        bool have = take(lane == 0 && walk.next(p, &next));
+        int rows = have ? begin(x) : 0, rows_next = 0;
+        while (ok && have) {
+            const int n = x.n;
             if (lead) {  // Q, once the scores of the piece before are made
                 if (pieces) ok = wait(&sh->q_free, pieces - 1);
                 if (ok) {
                     if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh->q_full), 2 * chunks * kQBytes);
-                    for (int k = 0; k < chunks; ++k)
-                        tma_load_3d_pair(sm_q + k * kQBytes, &tm_q, at_even(&sh->q_full), k * 64, 0, x.row0 + rank * 64);
+                    const int row = x.row0 + rank * 64;
+                    if (p.C == 64 * kMaxChunks) {
+                        tma_load_3d_pair(sm_q, &tm_q4, at_even(&sh->q_full), 0, row, 0);
+                        tma_load_3d_pair(sm_q + 4 * kQBytes, &tm_q4, at_even(&sh->q_full), 0, row, 4);
+                        tma_load_3d_pair(sm_q + 8 * kQBytes, &tm_q, at_even(&sh->q_full), 8 * 64, 0, row);
+                    } else {
+                        for (int k = 0; k < chunks; ++k)
+                            tma_load_3d_pair(sm_q + k * kQBytes, &tm_q, at_even(&sh->q_full), k * 64, 0, row);
+                    }
                     ++pieces;
                 }
             }
             ok = __all_sync(~0u, ok);
-            // first row of box `lane` of the batch that starts at step j; a row outside the cache reads as zeros
-            auto look_up = [&](int j) {
-                const int key = key0 + (j * per + lane) * p.box;
-                if (j * per + lane >= n * per || key >= end) return p.num_rows;
-                const int page = row_table[key / p.page_size];
-                if (page >= 0 && page < p.num_pages) return page * p.page_size + key % p.page_size;
-                bits |= kStatusPageRange;
-                return p.num_rows;
-            };
-            // Asks L2 for this lane's box of cache rows, which lie in one piece of memory.
-            auto fetch = [&](int row) {
-                if (row < p.num_rows) bulk_prefetch_l2(p.cache + static_cast<int64_t>(row) * p.C, p.box * p.C * 2);
-            };
-            int rows = look_up(0), ahead = batch < n ? look_up(batch) : p.num_rows;
+            int ahead = batch < n ? look_up(x, batch) : p.num_rows;
             const bool far = !x.prefix && lane / per < batch;
-            if (far && lane / per < kFetch && (lane / per & 1) == rank) fetch(rows);
             // K of step j, then V of step j - 2, as they are used: so K never waits behind a V whose place is not free.
             int row[kKeys / 16], row1[kKeys / 16], row2[kKeys / 16];  // the boxes of steps j, j - 1, j - 2
 #pragma unroll
@@ -665,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int i = j & (batch - 1);
                 if (i == 0 && j > 0 && j < n) {
                     rows = ahead;
-                    ahead = j + batch < n ? look_up(j + batch) : p.num_rows;
+                    ahead = j + batch < n ? look_up(x, j + batch) : p.num_rows;
                 }
 #pragma unroll
                 for (int e = 0; e < kKeys / 16; ++e) {
@@ -721,9 +768,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                     }
                 }
+                if (j == n - 1) {
+                    __syncwarp();
+                    have = __shfl_sync(~0u, static_cast<int>(lane == 0 && walk.next(p, &next)), 0);
+                    __syncwarp();
+                    if (have) rows_next = begin(next);
+                }
                 ok = __all_sync(~0u, ok);
             }
             step += n;
+            x = next;
+            rows = rows_next;
         }
         // no copy of either CTA may still be landing when they leave
         if (lead && rank == 0) {
@@ -755,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial results of each row, in the order of the cut; a row with
 // one piece was finished by that piece.  One warp per row.
-__global__ void __launch_bounds__(128) mla_attend_join_kernel(const CacheParams p) {
+__global__ void __launch_bounds__(128) mla_attend_join_kernel(const __grid_constant__ CacheParams p) {
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     pdl_launch_dependents();
@@ -907,16 +962,17 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     const int C = d->kv_lora_rank + d->rope_dim, box = gcd(d->page_size, kKeys);
     const int64_t rows = d->num_pages * d->page_size;
     const int dv_half = (d->kv_lora_rank / 2 + 15) / 16 * 16;
-    CUtensorMap tq, tc, tk4, tv4;
+    CUtensorMap tq, tc, tq4, tk4, tv4;
     // an empty cache has no valid page: every read is outside the map, which then only needs a valid address
     const void* base = rows ? kv_cache : q;
     const uint64_t map_rows = rows ? rows : 1;
     bool good = encode_bf16_3d(&tq, q, C, 1, static_cast<uint64_t>(d->batch) * d->num_heads, 1, 64) &&
                 encode_bf16_3d(&tc, base, C, 1, map_rows, 1, box < 32 ? box : 32);
-    // the same rows by whole chunks, [chunk][row][64], four in one copy: 32 keys for the scores, 64 for the values
-    tk4 = tv4 = tc;
+    // the same rows by whole chunks, [chunk][row][64], four in one copy: Q, 32 keys for the scores, 64 for the values
+    tq4 = tk4 = tv4 = tc;
     if (C == 64 * kMaxChunks)
-        good = good && encode_bf16_chunks(&tk4, base, C, map_rows, 32, 4) &&
+        good = good && encode_bf16_chunks(&tq4, q, C, static_cast<uint64_t>(d->batch) * d->num_heads, 64, 4) &&
+               encode_bf16_chunks(&tk4, base, C, map_rows, 32, 4) &&
                encode_bf16_chunks(&tv4, base, C, map_rows, kKeys, 4);
     if (!good) return report_cuda(cudaErrorInvalidValue, "tensor maps of attend_cache");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -943,7 +999,7 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    e = cudaLaunchKernelEx(&cfg, mla_attend_cache_kernel, tq, tc, tk4, tv4, p);
+    e = cudaLaunchKernelEx(&cfg, mla_attend_cache_kernel, tq, tc, tq4, tk4, tv4, p);
     if (e != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
     const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
     e = launch_kernel(mla_attend_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, st, true, p);

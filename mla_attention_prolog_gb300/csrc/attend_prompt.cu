@@ -25,7 +25,7 @@
 #include <cstdint>
 
 #include "attend.cuh"
-#include "ptx.cuh"
+#include "attend_ptx.cuh"
 
 namespace mlap {
 namespace {

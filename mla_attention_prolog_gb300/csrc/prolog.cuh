@@ -15,9 +15,6 @@ namespace mlap {
 constexpr int kStatusPositionRange = 0x1;
 constexpr int kStatusWaitTimeout = 0x2;
 constexpr int kStatusSlotRange = 0x4;
-constexpr int kStatusSeqRange = 0x8;
-constexpr int kStatusPageRange = 0x10;
-constexpr int kStatusPoolFull = 0x20;
 
 constexpr int kBM = 128;  // MMA M: token rows per tile (one TMEM lane per row)
 constexpr int kBK = 64;   // K per pipeline stage: one 128-byte swizzle atom of BF16
