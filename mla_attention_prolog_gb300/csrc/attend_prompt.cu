@@ -196,6 +196,20 @@ __device__ __forceinline__ uint32_t codes_bf16x2(uint32_t four, uint32_t selecto
     return r;
 }
 
+// True if the 64 values of a v row's chunk are finite: x * 0 added up stays 0
+// unless an x is infinite or NaN.
+__device__ __forceinline__ bool finite_row(uint32_t smem, int row) {
+    const int lane = threadIdx.x & 31;
+    uint32_t w[8][4], acc[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ld_shared_v4(smem + row * 128 + (((i + lane) & 7) << 4), w[i][0], w[i][1], w[i][2], w[i][3]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(acc[k]) : "r"(w[i][k]), "r"(0));
+    return ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7FFF7FFFu) == 0;
+}
+
 // Zeroes what no row may multiply: v rows behind the sequence's end, and NaN
 // or infinite elements of v (in tiles where the mask hides keys from some
 // rows); their keys are noted, and the rows that do see them add them in the
@@ -204,7 +218,8 @@ __device__ __forceinline__ void clean_v(uint32_t smem, int chunks, int row, bool
     const int lane = threadIdx.x & 31;
     bool hit = false;
     for (int c = 0; c < chunks; ++c) {
-#pragma unroll
+        if (inside && finite_row(smem + c * kSlotBytes, row)) continue;
+#pragma unroll 1
         for (int i = 0; i < 8; ++i) {
             const uint32_t at = smem + c * kSlotBytes + row * 128 + (((i + lane) & 7) << 4);
             uint32_t w[4];
