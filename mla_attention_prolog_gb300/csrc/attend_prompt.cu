@@ -210,42 +210,29 @@ __device__ __forceinline__ bool finite_row(uint32_t smem, int row) {
     return ((acc[0] | acc[1] | acc[2] | acc[3]) & 0x7FFF7FFFu) == 0;
 }
 
-// Zeroes what no row may multiply: v rows behind the sequence's end, and NaN
-// or infinite elements of v (in tiles where the mask hides keys from some
-// rows); their keys are noted, and the rows that do see them add them in the
-// epilogue.  One key row per thread of the warpgroup.
-__device__ __forceinline__ void clean_v(uint32_t smem, int chunks, int row, bool inside, uint32_t* bad) {
+// Zeroes what no row may multiply, in one slot of v: rows behind the sequence's
+// end, and NaN or infinite elements (in tiles where the mask hides keys from
+// some rows); their keys are noted, and the rows that do see them add them in
+// the epilogue.  One key row per thread of the warpgroup.
+__device__ __forceinline__ void clean_v(uint32_t smem, int row, bool inside, uint32_t* bad) {
     const int lane = threadIdx.x & 31;
-    bool hit = false;
-    for (int c = 0; c < chunks; ++c) {
-        if (inside && finite_row(smem + c * kSlotBytes, row)) continue;
+    if (!inside) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) st_shared_v4(smem + row * 128 + (((i + lane) & 7) << 4), 0, 0, 0, 0);
+    } else if (!finite_row(smem, row)) {
+        atomicOr(bad + (row >> 5), 1u << (row & 31));  // noted before it is gone
+        __threadfence_block();
 #pragma unroll 1
         for (int i = 0; i < 8; ++i) {
-            const uint32_t at = smem + c * kSlotBytes + row * 128 + (((i + lane) & 7) << 4);
+            const uint32_t at = smem + row * 128 + (((i + lane) & 7) << 4);
             uint32_t w[4];
-            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(at)
-                         : "memory");
-            bool change = false;
+            ld_shared_v4(at, w[0], w[1], w[2], w[3]);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                uint32_t m = 0;
-                if (!inside || (w[k] & 0x7F80u) == 0x7F80u) m |= 0xFFFFu;
-                if (!inside || (w[k] & 0x7F800000u) == 0x7F800000u) m |= 0xFFFF0000u;
-                if (m) {
-                    w[k] &= ~m;
-                    change = true;
-                }
+                if ((w[k] & 0x7F80u) == 0x7F80u) w[k] &= 0xFFFF0000u;
+                if ((w[k] & 0x7F800000u) == 0x7F800000u) w[k] &= 0xFFFFu;
             }
-            if (change) {
-                if (inside && !hit) {  // noted before it is gone
-                    hit = true;
-                    atomicOr(bad + (row >> 5), 1u << (row & 31));
-                    __threadfence_block();
-                }
-                st_shared_v4(at, w[0], w[1], w[2], w[3]);
-            }
+            st_shared_v4(at, w[0], w[1], w[2], w[3]);
         }
     }
 }
@@ -534,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 for (int cidx = 0; cidx < nv; ++cidx)
-                    clean_v(sm_ring + (use + cidx) % p.slots * kSlotBytes, 1, r, key0 + r < jb.nk,
+                    clean_v(sm_ring + (use + cidx) % p.slots * kSlotBytes, r, key0 + r < jb.nk,
                             sh->bad + (key0 / kTile - first_masked) * 4);
                 fence_proxy_async_shared();
             }
