@@ -9,6 +9,7 @@ an sm_103 GPU, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -380,24 +381,46 @@ def _on(t: torch.Tensor, name: str, dims: int) -> torch.device:
     raise ValueError(f"{name} must have {dims} dimensions, got shape {tuple(t.shape)}")
 
 
-def _stream_on(device, stream: Optional[torch.cuda.Stream]) -> Optional[int]:
+def _at(t, name: str, dtype, shape, index: int) -> Optional[int]:
+    """``_ptr`` on device ``index``, the usual case first: a call of a small
+    operator takes a few microseconds in all."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    return _ptr(t, name, dtype, shape, torch.device("cuda", index))
+
+
+def _run(f, name: str, index: int, stream: Optional[torch.cuda.Stream], *args) -> None:
+    """Calls an entry point with device ``index`` as the current one, on
+    ``stream`` or the device's current stream."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(device.index) or None
-    if stream.device != device:
-        raise ValueError(f"the stream is on {stream.device}, the tensors on {device}")
-    return stream.cuda_stream or None
-
-
-def _run(name: str, device, *args) -> None:
-    """Calls an entry point with `device` as the current one."""
-    f = getattr(_lib or lib(), name)
-    if torch._C._cuda_getDevice() == device.index:
-        rc = f(*args)
+        s = torch._C._cuda_getCurrentRawStream(index)
+    elif stream.device.index != index:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on cuda:{index}")
     else:
-        with torch.cuda.device(device):
-            rc = f(*args)
+        s = stream.cuda_stream
+    if torch._C._cuda_getDevice() == index:
+        rc = f(*args, s)
+    else:
+        with torch.cuda.device(index):
+            rc = f(*args, s)
     if rc != MLA_OK:
         raise MlaPrologError(rc, name)
+
+
+@functools.lru_cache(maxsize=256)
+def _prompt_dims(*sizes):
+    return ctypes.byref(MlaPrologPromptDims(*sizes))
+
+
+@functools.lru_cache(maxsize=256)
+def _cache_dims(*sizes):
+    return ctypes.byref(MlaPrologCacheDims(*sizes))
+
+
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
 
 
 def attend_prompt(q, k, v, cu_q, cu_k, out, lse=None, *, scale: float, causal: bool = True, q_scale=None,
@@ -406,26 +429,31 @@ def attend_prompt(q, k, v, cu_q, cu_k, out, lse=None, *, scale: float, causal: b
     (``mla_prolog_attend_prompt``): q BF16 [Tq, H, Dqk], or int8 codes with
     ``q_scale`` [Tq] or [Tq, H]; k [Tk, Hk, Dqk], v [Tk, Hk, Dv]; cu_q, cu_k
     int32 [sequences + 1]; out BF16 [Tq, H, Dv], lse FP32 [Tq, H]."""
-    dev = _on(q, "q", 3)
-    _on(k, "k", 3), _on(v, "v", 3)
-    (Tq, H, Dqk), (Tk, Hk, _), Dv, n = q.shape, k.shape, v.shape[2], cu_q.numel() - 1
-    if n < 0:
+    try:
+        (Tq, H, Dqk), (Tk, Hk, _), (_, _, Dv), (n,) = q.shape, k.shape, v.shape, cu_q.shape
+        index = q.get_device()
+    except (AttributeError, ValueError):
+        index = -1
+    if index < 0:
+        for t, name, dims in ((q, "q", 3), (k, "k", 3), (v, "v", 3), (cu_q, "cu_q", 1)):
+            _on(t, name, dims)
+    if n < 1:
         raise ValueError("cu_q must have at least one entry")
-    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     flags = MLA_PROMPT_CAUSAL if causal else 0
-    scale_shape = (Tq,)
+    q_type = _BF16
     if q_scale is not None:
         flags |= MLA_PROMPT_Q_INT8
+        q_type, scale_shape = torch.int8, (Tq,)
         if q_scale.dim() == 2:
             flags |= MLA_PROMPT_Q_SCALE_PER_HEAD
             scale_shape = (Tq, H)
-    d = MlaPrologPromptDims(Tq, Tk, n, H, Hk, Dqk, Dv, scale, flags)
-    args = [_ptr(q, "q", torch.int8 if q_scale is not None else bf, (Tq, H, Dqk), dev),
-            _ptr(q_scale, "q_scale", f32, scale_shape, dev), _ptr(k, "k", bf, (Tk, Hk, Dqk), dev),
-            _ptr(v, "v", bf, (Tk, Hk, Dv), dev), _ptr(cu_q, "cu_q", i32, (n + 1,), dev),
-            _ptr(cu_k, "cu_k", i32, (n + 1,), dev), _ptr(out, "out", bf, (Tq, H, Dv), dev),
-            _ptr(lse, "lse", f32, (Tq, H), dev), _ptr(status, "status", i32, (1,), dev)]
-    _run("mla_prolog_attend_prompt", dev, ctypes.byref(d), *args, _stream_on(dev, stream))
+        q_scale = _at(q_scale, "q_scale", _F32, scale_shape, index)
+    _run((_lib or lib()).mla_prolog_attend_prompt, "mla_prolog_attend_prompt", index, stream,
+         _prompt_dims(Tq, Tk, n - 1, H, Hk, Dqk, Dv, scale, flags), _at(q, "q", q_type, (Tq, H, Dqk), index), q_scale,
+         _at(k, "k", _BF16, (Tk, Hk, Dqk), index), _at(v, "v", _BF16, (Tk, Hk, Dv), index),
+         _at(cu_q, "cu_q", _I32, (n,), index), _at(cu_k, "cu_k", _I32, (n,), index),
+         _at(out, "out", _BF16, (Tq, H, Dv), index), None if lse is None else _at(lse, "lse", _F32, (Tq, H), index),
+         None if status is None else _at(status, "status", _I32, (1,), index))
 
 
 def attend_cache_workspace_bytes(batch: int, num_heads: int, kv_lora_rank: int, rope_dim: int) -> int:
@@ -444,18 +472,25 @@ def attend_cache(q, kv_cache, page_table, seq_lens, out, lse, workspace, *, scal
     int32 [S]; seqs int32 [B] (None: row b is sequence b); shared_len int32 [1];
     out BF16 [B, H, Lkv]; lse FP32 [B, H] or None; workspace uint8 of at least
     ``attend_cache_workspace_bytes``."""
-    dev = _on(q, "q", 3)
-    _on(kv_cache, "kv_cache", 3), _on(page_table, "page_table", 2), _on(out, "out", 3), _on(workspace, "workspace", 1)
-    (B, H, C), (pages, page_size, _), Lkv, (S, width) = q.shape, kv_cache.shape, out.shape[2], page_table.shape
-    bf, i32 = torch.bfloat16, torch.int32
-    d = MlaPrologCacheDims(B, H, Lkv, C - Lkv, page_size, S, width, scale, pages)
-    args = [_ptr(q, "q", bf, (B, H, C), dev), _ptr(kv_cache, "kv_cache", bf, (pages, page_size, C), dev),
-            _ptr(page_table, "page_table", i32, (S, width), dev), _ptr(seq_lens, "seq_lens", i32, (S,), dev),
-            _ptr(seqs, "seqs", i32, (B,), dev), _ptr(shared_len, "shared_len", i32, (1,), dev),
-            _ptr(out, "out", bf, (B, H, Lkv), dev), _ptr(lse, "lse", torch.float32, (B, H), dev),
-            _ptr(workspace, "workspace", torch.uint8, tuple(workspace.shape), dev), workspace.numel(),
-            _ptr(status, "status", i32, (1,), dev)]
-    _run("mla_prolog_attend_cache", dev, ctypes.byref(d), *args, _stream_on(dev, stream))
+    try:
+        (B, H, C), (pages, page_size, _), (_, _, Lkv), (S, width), (room,) = \
+            q.shape, kv_cache.shape, out.shape, page_table.shape, workspace.shape
+        index = q.get_device()
+    except (AttributeError, ValueError):
+        index = -1
+    if index < 0:
+        for t, name, dims in ((q, "q", 3), (kv_cache, "kv_cache", 3), (page_table, "page_table", 2), (out, "out", 3),
+                              (workspace, "workspace", 1)):
+            _on(t, name, dims)
+    _run((_lib or lib()).mla_prolog_attend_cache, "mla_prolog_attend_cache", index, stream,
+         _cache_dims(B, H, Lkv, C - Lkv, page_size, S, width, scale, pages), _at(q, "q", _BF16, (B, H, C), index),
+         _at(kv_cache, "kv_cache", _BF16, (pages, page_size, C), index),
+         _at(page_table, "page_table", _I32, (S, width), index), _at(seq_lens, "seq_lens", _I32, (S,), index),
+         None if seqs is None else _at(seqs, "seqs", _I32, (B,), index),
+         None if shared_len is None else _at(shared_len, "shared_len", _I32, (1,), index),
+         _at(out, "out", _BF16, (B, H, Lkv), index), None if lse is None else _at(lse, "lse", _F32, (B, H), index),
+         _at(workspace, "workspace", torch.uint8, (room,), index), room,
+         None if status is None else _at(status, "status", _I32, (1,), index))
 
 
 class PagePool:
@@ -472,14 +507,13 @@ class PagePool:
                                    _ptr(seq_lens, "seq_lens", i32, (S,), self.device),
                                    _ptr(refs, "refs", i32, (refs.numel(),), self.device),
                                    _ptr(status, "status", i32, (1,), self.device))
-
-        self._ref = ctypes.byref(self._pool)
+        self._ref, self._index = ctypes.byref(self._pool), self.device.index
 
     def _list(self, t, name, n):
-        return _ptr(t, name, torch.int32, (n,), self.device)
+        return None if t is None else _at(t, name, _I32, (n,), self._index)
 
     def _call(self, name, *args, stream):
-        _run(name, self.device, self._ref, *args, _stream_on(self.device, stream))
+        _run(getattr(_lib or lib(), name), name, self._index, stream, self._ref, *args)
 
     def extend(self, seqs, counts, slot_mapping=None, positions=None, stream=None) -> None:
         """Grows sequence seqs[i] by counts[i] tokens; slot_mapping and
@@ -519,7 +553,7 @@ def copy_pages(cache, src, dst, status=None, stream=None) -> None:
     shape = (1, *cache.shape) if one else cache.shape
     page_bytes = shape[2] * shape[3] * 2
     n = dst.numel()
-    args = [_ptr(cache, "cache", torch.bfloat16, cache.shape, dev), shape[0], shape[1] * page_bytes, shape[1],
-            page_bytes, _ptr(src, "src", torch.int32, (n,), dev), _ptr(dst, "dst", torch.int32, (n,), dev), n,
-            _ptr(status, "status", torch.int32, (1,), dev)]
-    _run("mla_prolog_copy_pages", dev, *args, _stream_on(dev, stream))
+    i = dev.index
+    _run((_lib or lib()).mla_prolog_copy_pages, "mla_prolog_copy_pages", i, stream, _at(cache, "cache", _BF16, cache.shape, i),
+         shape[0], shape[1] * page_bytes, shape[1], page_bytes, None if src is None else _at(src, "src", _I32, (n,), i),
+         _at(dst, "dst", _I32, (n,), i), n, None if status is None else _at(status, "status", _I32, (1,), i))

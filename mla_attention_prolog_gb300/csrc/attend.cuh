@@ -27,16 +27,20 @@ inline bool ptr_ok(const void* p, uintptr_t align) {
     return p && reinterpret_cast<uintptr_t>(p) % align == 0;
 }
 
-// The current device and its SM count; MLA_ERR_DEVICE unless it is sm_103.
-// Two attribute queries (no cudaGetDeviceProperties): cheap on every call.
+// The current device's SM count; MLA_ERR_DEVICE unless it is sm_103.  Asked of
+// the driver once per device.
 inline int current_sm103(int* sms) {
+    static std::atomic<int> known[64];
     int dev = 0, major = 0, minor = 0;
     cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess && dev < 64 && (*sms = known[dev].load(std::memory_order_relaxed)) > 0) return MLA_OK;
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
     if (e != cudaSuccess) return report_cuda(e, "device query");
-    return major == 10 && minor == 3 ? MLA_OK : MLA_ERR_DEVICE;
+    if (major != 10 || minor != 3) return MLA_ERR_DEVICE;
+    if (dev < 64) known[dev].store(*sms, std::memory_order_relaxed);
+    return MLA_OK;
 }
 
 // Lets `kernel` use `bytes` of dynamic shared memory on the current device;

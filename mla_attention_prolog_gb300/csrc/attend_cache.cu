@@ -319,9 +319,8 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_c,
-                            const __grid_constant__ CUtensorMap tm_q4, const __grid_constant__ CUtensorMap tm_k4,
-                            const __grid_constant__ CUtensorMap tm_v4, const __grid_constant__ CacheParams p) {
+    mla_attend_cache_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CacheParams p) {
     extern __shared__ uint8_t raw[];
     const uint32_t raw_at = smem_u32(raw);
     const uint32_t pad = (1024u - (raw_at & 1023u)) & 1023u;  // the same in both CTAs of a pair
@@ -351,10 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(smem_u32(&sh->drain), 1);
         sh->abort_flag = 0;
         fence_barrier_init();
-        prefetch_tensormap(&tm_q4);
-        prefetch_tensormap(&tm_c);
-        prefetch_tensormap(&tm_k4);
-        prefetch_tensormap(&tm_v4);
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
     }
     if (warp == kMmaWarp) {
         tmem_alloc_pair(smem_u32(&sh->tmem), 512);
@@ -690,9 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh->q_full), 2 * chunks * kQBytes);
                     const int row = x.row0 + rank * 64;
                     if (p.C == 64 * kMaxChunks) {
-                        tma_load_3d_pair(sm_q, &tm_q4, at_even(&sh->q_full), 0, row, 0);
-                        tma_load_3d_pair(sm_q + 4 * kQBytes, &tm_q4, at_even(&sh->q_full), 0, row, 4);
-                        tma_load_3d_pair(sm_q + 8 * kQBytes, &tm_q, at_even(&sh->q_full), 8 * 64, 0, row);
+                        for (int k = 0; k < kMaxChunks; k += 3)
+                            tma_load_3d_pair(sm_q + k * kQBytes, &tm_q, at_even(&sh->q_full), 0, row, k);
                     } else {
                         for (int k = 0; k < chunks; ++k)
                             tma_load_3d_pair(sm_q + k * kQBytes, &tm_q, at_even(&sh->q_full), k * 64, 0, row);
@@ -734,14 +731,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int k0 = per == 1 ? (rank && row[0] < p.num_rows ? row[0] + 32 : row[0])
                                                 : rank == 0 ? row[0] : per == 2 ? row[1] : row[2];
                         if (whole) {
-                            tma_load_3d_pair(dst, &tm_k4, bar, 0, k0, 0);
-                            tma_load_3d_pair(dst + 4 * kKBytes, &tm_k4, bar, 0, k0, 4);
-                            tma_load_3d_pair(dst + 8 * kKBytes, &tm_c, bar, 8 * 64, 0, k0);
+#pragma unroll
+                            for (int k = 0; k < kMaxChunks; k += 3)
+                                tma_load_3d_pair(dst + k * kKBytes, &tm_k, bar, 0, k0, k);
                         } else {
                             for (int k = 0; k < chunks; ++k) {
-                                tma_load_3d_pair(dst + k * kKBytes, &tm_c, bar, k * 64, 0, k0);
+                                tma_load_3d_pair(dst + k * kKBytes, &tm_k, bar, k * 64, 0, k0);
                                 if (per == 4)
-                                    tma_load_3d_pair(dst + k * kKBytes + box_bytes, &tm_c, bar, k * 64, 0, rank ? row[3] : row[1]);
+                                    tma_load_3d_pair(dst + k * kKBytes + box_bytes, &tm_k, bar, k * 64, 0, rank ? row[3] : row[1]);
                             }
                         }
                     }
@@ -754,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t bar = at_even(&sh->v_full[st]), dst = sm_v + st * kMaxValues * kVBytes;
                         if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh->v_full[st]), 2 * nvc * kVBytes);
                         if (whole && per == 1) {
-                            tma_load_3d_pair(dst, &tm_v4, bar, 0, row2[0], rank * 4);
+                            tma_load_3d_pair(dst, &tm_v, bar, 0, row2[0], rank * 4);
                         } else {
                             const int boxes = per == 1 ? 2 : per;  // a box of 64 in two of 32
                             const uint32_t bytes = per == 1 ? 32 * 128 : box_bytes;
@@ -763,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if (e >= boxes) break;
                                 const int vr = per == 1 ? (e && row2[0] < p.num_rows ? row2[0] + 32 : row2[0]) : row2[e];
                                 for (int k = 0; k < nvc; ++k)
-                                    tma_load_3d_pair(dst + k * kVBytes + e * bytes, &tm_c, bar, v0 + k * 64, 0, vr);
+                                    tma_load_3d_pair(dst + k * kVBytes + e * bytes, &tm_v, bar, v0 + k * 64, 0, vr);
                             }
                         }
                     }
@@ -962,18 +959,19 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     const int C = d->kv_lora_rank + d->rope_dim, box = gcd(d->page_size, kKeys);
     const int64_t rows = d->num_pages * d->page_size;
     const int dv_half = (d->kv_lora_rank / 2 + 15) / 16 * 16;
-    CUtensorMap tq, tc, tq4, tk4, tv4;
+    CUtensorMap tq, tk, tv;
     // an empty cache has no valid page: every read is outside the map, which then only needs a valid address
     const void* base = rows ? kv_cache : q;
     const uint64_t map_rows = rows ? rows : 1;
-    bool good = encode_bf16_3d(&tq, q, C, 1, static_cast<uint64_t>(d->batch) * d->num_heads, 1, 64) &&
-                encode_bf16_3d(&tc, base, C, 1, map_rows, 1, box < 32 ? box : 32);
-    // the same rows by whole chunks, [chunk][row][64], four in one copy: Q, 32 keys for the scores, 64 for the values
-    tq4 = tk4 = tv4 = tc;
-    if (C == 64 * kMaxChunks)
-        good = good && encode_bf16_chunks(&tq4, q, C, static_cast<uint64_t>(d->batch) * d->num_heads, 64, 4) &&
-               encode_bf16_chunks(&tk4, base, C, map_rows, 32, 4) &&
-               encode_bf16_chunks(&tv4, base, C, map_rows, kKeys, 4);
+    // The widest rows by whole chunks, [chunk][row][64], several in one copy: Q and the 32 keys for the scores by three,
+    // the 64 keys of values by four.  (whole, per: as in the kernel.)
+    const uint64_t q_rows = static_cast<uint64_t>(d->batch) * d->num_heads;
+    const bool wide = C == 64 * kMaxChunks, whole = wide && box >= 32 && dv_half == 256;
+    const uint32_t box_rows = box < 32 ? box : 32;
+    bool good = wide ? encode_bf16_chunks(&tq, q, C, q_rows, 64, 3) : encode_bf16_3d(&tq, q, C, 1, q_rows, 1, 64);
+    good = good && (whole ? encode_bf16_chunks(&tk, base, C, map_rows, 32, 3) : encode_bf16_3d(&tk, base, C, 1, map_rows, 1, box_rows));
+    if (!whole) tv = tk;
+    else good = good && (box == kKeys ? encode_bf16_chunks(&tv, base, C, map_rows, kKeys, 4) : encode_bf16_3d(&tv, base, C, 1, map_rows, 1, box_rows));
     if (!good) return report_cuda(cudaErrorInvalidValue, "tensor maps of attend_cache");
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     CacheParams p{static_cast<const uint16_t*>(q), static_cast<const uint16_t*>(kv_cache), page_table, seq_lens, seqs, shared_len, static_cast<uint16_t*>(out),
@@ -999,7 +997,7 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* d, const void* q, const
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = 2;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    e = cudaLaunchKernelEx(&cfg, mla_attend_cache_kernel, tq, tc, tq4, tk4, tv4, p);
+    e = cudaLaunchKernelEx(&cfg, mla_attend_cache_kernel, tq, tk, tv, p);
     if (e != cudaSuccess) return report_cuda(e, "launch mla_attend_cache_kernel");
     const int64_t blocks = (static_cast<int64_t>(d->batch) * d->num_heads + 3) / 4;
     e = launch_kernel(mla_attend_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, st, true, p);
