@@ -3,9 +3,10 @@
 // cache's contents.
 //
 // The bookkeeping calls run as one CTA of 1024 threads.  They touch a few
-// hundred KB at most and are bound by latency (launch, then two or three
-// dependent passes over refs), so one CTA that needs no grid-wide hand-over
-// beats a spread of the same work over SMs that would have to meet twice.
+// hundred KB at most and are bound by latency (lists, lengths, a pass over
+// refs, the dealing out), so one CTA that needs no grid-wide hand-over beats a
+// spread of the same work over SMs that would have to meet twice.  All calls
+// are dependent launches, which hide each other's launch latency.
 #include <cstdint>
 
 #include "attend.cuh"
@@ -504,7 +505,8 @@ __global__ void __launch_bounds__(256) mla_pages_retable_kernel(Pool p, const in
 }
 
 // A CTA copies `per` entries' pages of one layer, or one of `pieces` pieces of
-// one entry's page; each thread keeps 8 loads of 16 bytes in flight.
+// one entry's page; each thread keeps 8 loads of 16 bytes in flight.  Bound by
+// HBM: 1.09 GB in 174 us, 6.3 TB/s (94 % of the measured copy rate).
 constexpr int kCopyThreads = 256, kCopyLoads = 8, kCopyStep = kCopyThreads * kCopyLoads;
 
 __global__ void __launch_bounds__(kCopyThreads) mla_copy_pages_kernel(uint8_t* __restrict__ cache, int64_t layer_stride,
