@@ -215,9 +215,13 @@ def kernel_work(d: wl.Dims, cache: bool = False, names=()):
 
 
 def csrc_digest() -> str:
+    """Of the sources that the prolog is built from (not the attention and page
+    operators' own)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "mla_attention_prolog_gb300", "csrc")
     for n in sorted(os.listdir(csrc)):
+        if n.startswith(("attend", "pages")):
+            continue
         with open(os.path.join(csrc, n), "rb") as fh:
             h.update(n.encode() + fh.read())
     return h.hexdigest()[:16]

@@ -65,7 +65,9 @@ constexpr float kSlack = 8.f;             // log2 of the largest P
 // Own pages are asked of L2 this many steps before their copies: the ring holds two steps, which cover the
 // latency of L2 but not that of HBM.
 constexpr int kFetch = 1;
-constexpr int kOverhead = 4, kRowsPerStep = 16;  // a tile's start and end, in key steps: so many, and one per so many rows
+// A tile's start and end, in key steps: so many, and one per so many rows.  (V2-Lite 64 sequences, V3 shared prefix: 48
+// and 240 us; 4 alone 49 and 289; 3 and one per 32 rows 51 and 255; 2 or 3 and one per 16 rows 51 and 239.)
+constexpr int kOverhead = 4, kRowsPerStep = 16;
 constexpr int kMinRun = 4;                // shortest run worth a CTA pair, in key steps after its tile's start
 
 // What the join kernel needs to know of the cut (start of the workspace).

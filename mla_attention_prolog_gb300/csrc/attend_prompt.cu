@@ -34,7 +34,7 @@
 // CTA that keeps 64 keys per step, P in halves, exponentials on the last
 // tile's maximum, a persistent CTA or a CTA pair per 256 rows each measured
 // slower.  128 heads x 16384 tokens, INT8 q: 6.88 ms, 1600 TFLOP/s (83 % of the
-// measured cuBLAS rate); four prompts of 700 to 4099: 963 us, 989 TFLOP/s;
+// measured cuBLAS rate); four prompts of 700 to 4099: 931 us, 1023 TFLOP/s;
 // 16 heads x 4096: 70.5 us, 1220; eight ragged prompts: 43.6 us, 644.
 #include <cstdint>
 
@@ -865,11 +865,17 @@ extern "C" int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* d, const v
     // Heads go in groups whose K and V fit L2 together, and within a group the
     // tile pairs with the most keys first: few heads at a time keep K and V on
     // chip when they are large, many spread uneven tiles over the SMs when
-    // they are small.
+    // they are small.  In us, groups of 12 / 24 / 48 / 96 MB / all heads: eight
+    // ragged prompts 63 / 57 / 43 / 43 / 43; four V3 prompts 979 / 949 / 961 / 933
+    // / 1073; V3 16384 6850 / 6877 / 6843 / 7052 / 8085.  Groups are made alike,
+    // so that a small last one does not leave SMs idle (961: 14 of 9 heads and one
+    // of 2; 12 of 10 and one of 8: 931).
     const int64_t kv_bytes = static_cast<int64_t>(d->Tk) * (d->qk_dim + d->v_dim) * 2;
     const int per_kv = d->num_heads / d->kv_heads;
     int64_t group = kv_bytes > 0 ? (int64_t(48) << 20) / kv_bytes : d->kv_heads;
-    group = (group < 1 ? 1 : group > d->kv_heads ? d->kv_heads : group) * per_kv;
+    group = group < 1 ? 1 : group > d->kv_heads ? d->kv_heads : group;
+    const int64_t groups = d->kv_heads / group;
+    group = (d->kv_heads + groups - 1) / groups * per_kv;
     // Few tile pairs with many keys: a cluster shares a tile pair's keys, as large a one as leaves room for all of
     // them at once.  In us, on 1 / 2 / 4 / 8 CTAs, D 192: 4 pairs of 156 key tiles 218 / 115 / 63 / 37; 16 pairs
     // 220 / 116 / 65 / 78 (their clusters of 8 do not fit at once); 32 pairs of 64 tiles 125 / 72 / 44 / 77; 64 pairs

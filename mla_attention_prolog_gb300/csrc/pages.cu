@@ -647,7 +647,8 @@ int mla_prolog_copy_pages(void* cache, int32_t layers, int64_t layer_stride, int
     const int rc = current_sm103(&sms);
     if (rc != MLA_OK) return rc;
     // Most entries of a long list are skipped (a compaction's): eight to a CTA then, so that the empty CTAs do not
-    // take longer than the copies; a short list is cut into pieces, so that few pages still fill the SMs.
+    // take longer than the copies; a short list is cut into pieces, so that few pages still fill the SMs.  (A step of
+    // both, 256 sequences and 8 layers: 221 us; all as short lists 243, all as long ones 235.)
     const bool many = static_cast<int64_t>(n) * layers > 16 * sms;
     const int per = many ? 8 : 1;
     const int64_t step_bytes = kCopyStep * 16;
