@@ -30,8 +30,8 @@
 // pages of few heads run at the rate of memory); a tile's start and end ~3.5
 // us, of which the copies of the next tile overlap all but the last products
 // and the results' way out; a call's start 6 us and its join 4 us.  V2-Lite (16
-// heads), 64 sequences of 1 to 4096: 47.8 us, 3.8 TB/s; V3 (128 heads), 32 of
-// 2000 to 32768: 142 us, 4.8 TB/s and 1140 TFLOP/s; 128 of 1 to 1024 behind a
+// heads), 64 sequences of 1 to 4096: 48 us, 3.8 TB/s; V3 (128 heads), 32 of
+// 2000 to 32768: 147 us, 4.6 TB/s and 1100 TFLOP/s; 128 of 1 to 1024 behind a
 // prefix of 8192: 241 us, 1290 TFLOP/s; one sequence of 100: 12 us.
 #include <cstdint>
 

@@ -551,6 +551,32 @@ def test_cache_two_graphs_with_their_own_workspaces():
             check_cache(c, out, lse)
 
 
+def test_calls_that_feed_one_another():
+    """Launches overlap the end of the ones before them: a chain of calls, each
+    on what the last one wrote, gives the bits of the same chain with a
+    synchronize between any two."""
+    H, E, n = 4, 64, 300
+    c = prompt_case(30, [n, 17], [n, 17], H, H, 64, E, pad=0)
+    cc = cache_case(31, [n, 17], H, E, 0, 16)
+    ws = torch.empty(binding.attend_cache_workspace_bytes(2, H, E, 0), dtype=torch.uint8, device=DEV)
+    ends = []
+    for apart in (False, True):
+        a, b = c["v"].clone(), torch.empty_like(c["v"])
+        q, o = cc["q"].clone(), torch.empty((2, H, E), dtype=torch.bfloat16, device=DEV)
+        torch.cuda.synchronize()
+        for _ in range(40):
+            binding.attend_prompt(c["q"], c["k"], a, c["cu_q"], c["cu_k"], b, scale=c["scale"])
+            if apart:
+                torch.cuda.synchronize()
+            binding.attend_cache(q, cc["cache"], cc["table"], cc["lens"], o, None, ws, scale=cc["scale"])
+            if apart:
+                torch.cuda.synchronize()
+            a, b, q, o = b, a, o, q
+        torch.cuda.synchronize()
+        ends.append((a.view(torch.int16).clone(), q.view(torch.int16).clone()))
+    assert torch.equal(ends[0][0], ends[1][0]) and torch.equal(ends[0][1], ends[1][1])
+
+
 def test_prolog_cache_and_attention_together():
     """A prompt and a decoding step, end to end: the pool hands out slots, the
     prolog writes K, V and the latent cache, the prompt attention reads K and

@@ -335,3 +335,29 @@ def test_a_captured_step():
         assert [(int(src.item()), int(dst.item()))] == pairs and slots.tolist() == want
         assert moved.tolist() == x.m.compact()[0]
         x.same()
+
+
+def test_steps_that_follow_one_another():
+    """Launches overlap the end of the ones before them: steps of all calls in a
+    row leave what they leave with a synchronize between any two."""
+    ends = []
+    for apart in (False, True):
+        S, width, pages, page = 12, 8, 90, 16
+        table = torch.full((S, width), -1, dtype=torch.int32, device=DEV)
+        lens, refs = i32(*[0] * S), i32(*[0] * pages)
+        pool = binding.PagePool(table, lens, refs, page)
+        g = torch.Generator(DEV).manual_seed(5)
+        cache = torch.randint(-2 ** 15, 2 ** 15, (2, pages, page, 8), generator=g, device=DEV).to(torch.int16).view(torch.bfloat16)
+        src, dst, moved, slots, pos = i32(-1, -1), i32(-1, -1), i32(*[0] * pages), i32(*[0] * 40), i32(*[0] * 40)
+        args = [(i32(k % 4, 4 + k % 4), i32(7, 11), i32(k % 4, 4 + k % 4), i32(8 + k % 4, 8 + (k + 1) % 4)) for k in range(30)]
+        torch.cuda.synchronize()
+        for seqs, counts, parents, children in args:
+            for call in (lambda: pool.extend(seqs, counts, slots, pos), lambda: pool.release(children),
+                         lambda: pool.fork(parents, children, src, dst), lambda: binding.copy_pages(cache, src, dst),
+                         lambda: pool.compact(moved), lambda: binding.copy_pages(cache, None, moved)):
+                call()
+                if apart:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        ends.append([t.clone() for t in (table, lens, refs, cache.view(torch.int16), slots, pos, moved, src, dst)])
+    assert all(torch.equal(a, b) for a, b in zip(*ends)) and ends[0][1].sum() > 0
