@@ -214,9 +214,11 @@ struct Walk {
 };
 
 struct Shared {
-    // full and free: K and V of step i at i % 2, Q of a piece; the even CTA's count for both
-    uint64_t k_full[2], k_free[2], v_full[2], v_free[2], q_full, q_free;
-    uint64_t s_full[kAhead], s_read[kAhead], p_full[2], pv_done[2], v_seen, drain;
+    // full: K and V of step i at i % 2, Q of a piece; the even CTA's count for both.  s_full and pv_done also tell the
+    // loaders that K and V have been read, and p_full (of the step before last) that an S has: the thread that issues the
+    // products waits and commits as rarely as it can.
+    uint64_t k_full[2], v_full[2], q_full;
+    uint64_t s_full[kAhead], p_full[2], pv_done[2], v_seen, drain;
     uint32_t tmem;
     int abort_flag;
     float row_max[kRows], row_sum[kRows];  // what the two threads of a row tell each other
@@ -348,18 +350,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kLoadWarp && lane == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_u32(&sh->k_full[i]), 1);
-            mbar_init(smem_u32(&sh->k_free[i]), 1);
             mbar_init(smem_u32(&sh->v_full[i]), 1);
-            mbar_init(smem_u32(&sh->v_free[i]), 1);
             mbar_init(smem_u32(&sh->p_full[i]), 8);  // the softmax warps of both CTAs
             mbar_init(smem_u32(&sh->pv_done[i]), 1);
         }
-        for (int i = 0; i < kAhead; ++i) {
-            mbar_init(smem_u32(&sh->s_full[i]), 1);
-            mbar_init(smem_u32(&sh->s_read[i]), 8);
-        }
+        for (int i = 0; i < kAhead; ++i) mbar_init(smem_u32(&sh->s_full[i]), 1);
         mbar_init(smem_u32(&sh->q_full), 1);
-        mbar_init(smem_u32(&sh->q_free), 1);
         mbar_init(smem_u32(&sh->v_seen), 1);
         mbar_init(smem_u32(&sh->drain), 1);
         sh->abort_flag = 0;
@@ -409,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int tile_row = rank * 64 + r;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
         const uint32_t to = tmem + lanes + kColO, ts = tmem + lanes + kColS;
-        const uint32_t s_read = map_shared_rank(smem_u32(&sh->s_read[0]), 0), p_full = map_shared_rank(smem_u32(&sh->p_full[0]), 0);
+        const uint32_t p_full = map_shared_rank(smem_u32(&sh->p_full[0]), 0);
         auto arrive = [&](uint32_t bar) {  // one arrival per warp, at the even CTA
             __syncwarp();
             if (lane == 0) mbar_arrive_peer(bar);
@@ -428,8 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t s[32];
                 tc_fence_after();
                 float mt = tmem_ld32_max(ts + step % kAhead * 32, s);
-                tc_fence_before();
-                arrive(s_read + 8 * (step % kAhead));
                 const int left = keys - j * kKeys - side * 32;
                 if (left < 32) {
                     mt = -INFINITY;
@@ -612,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int t = 0; t < n + 2 && ok; ++t) {
                     const int st = step + t, e = st & 1, f4 = st % kAhead;
                     if (t < n) {
-                        if (st >= kAhead && !look(&sh->s_read[f4], st / kAhead - 1)) break;
+                        // (S of step t - 4 has been read: P of step t - 3 was waited for in the round before)
                         if (!look(&sh->k_full[e], st >> 1)) break;
                         const uint32_t d = tmem + kColS + f4 * 32;
                         const uint64_t b = dk + e * (kMaxChunks * kKBytes >> 4);
@@ -628,11 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                               b + (k >> 2) * (kKBytes >> 4) + 2 * (k & 3), idesc_s, k > 0);
                         }
                         commit(&sh->s_full[f4]);
-                        commit(&sh->k_free[e]);
-                        if (t + 1 == n) {
-                            commit(&sh->q_free);
-                            got = walk.next(p, &next);
-                        }
+                        if (t + 1 == n) got = walk.next(p, &next);
                     }
                     if (t > 1) {
                         const int pv = st - 2, f = pv & 1;
@@ -649,7 +639,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if (second) mma_bf16_pair(to + 128, dp + f * (kPBytes >> 4) + 2 * k, b + (2 * kVBytes >> 4) + k * (2048 >> 4), id1, t > 2 || k > 0);
                         }
                         commit(&sh->pv_done[f]);
-                        commit(&sh->v_free[f]);
                     }
                 }
                 if (!ok) break;
@@ -668,6 +657,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool lead = elect_one();
         const uint32_t box_bytes = p.box * 128;
         const bool whole = p.box >= 32 && p.C == 64 * kMaxChunks && p.dv_half == 256;
+        auto s_made = [&](int u) { return wait(&sh->s_full[u % kAhead], u / kAhead); };  // the scores of step u,
+        auto pv_made = [&](int u) { return wait(&sh->pv_done[u & 1], u >> 1); };           // its P V
         auto at_even = [&](uint64_t* bar) { return map_shared_rank(smem_u32(bar), 0); };
         int bits = 0, pieces = 0, ks = 0, vs = 0;  // Q, K and V places filled
         // first row of box `lane` of the batch that starts at a piece's step j; a row outside the cache reads as zeros
@@ -697,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (ok && have) {
             const int n = x.n;
             if (lead) {  // Q, once the scores of the piece before are made
-                if (pieces) ok = wait(&sh->q_free, pieces - 1);
+                if (step) ok = s_made(step - 1);
                 if (ok) {
                     if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh->q_full), 2 * chunks * kQBytes);
                     const int row = x.row0 + rank * 64;
@@ -736,7 +727,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     fetch(i + kFetch < batch ? rows : ahead);
                 if (lead && j < n) {
                     const int st = (step + j) & 1;
-                    ok = wait(&sh->k_free[st], ((step + j) >> 1) ^ 1);
+                    ok = step + j < 2 || s_made(step + j - 2);
                     if (ok) {
                         ++ks;
                         const uint32_t bar = at_even(&sh->k_full[st]), dst = sm_k + st * kMaxChunks * kKBytes;
@@ -759,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (lead && j > 1 && ok) {
                     const int st = (step + j) & 1;
-                    ok = wait(&sh->v_free[st], ((step + j - 2) >> 1) ^ 1);
+                    ok = step + j < 4 || pv_made(step + j - 4);
                     if (ok) {
                         ++vs;
                         const uint32_t bar = at_even(&sh->v_full[st]), dst = sm_v + st * kMaxValues * kVBytes;
@@ -799,9 +790,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // and what the tensor core frees has arrived (a piece's last products have ended before its results go out)
         if (lead) {
-            if (pieces) ok = ok && wait(&sh->q_free, pieces - 1);
-            for (int u = max(ks - 2, 0); u < ks; ++u) ok = ok && wait(&sh->k_free[u & 1], u >> 1);
-            for (int u = max(vs - 2, 0); u < vs; ++u) ok = ok && wait(&sh->v_free[u & 1], u >> 1);
+            for (int u = max(ks - kAhead, 0); u < ks; ++u) ok = ok && s_made(u);
+            for (int u = max(vs - 2, 0); u < vs; ++u) ok = ok && pv_made(u);
         }
         if (bits) raise_status(p.status, bits);
     }
