@@ -75,6 +75,7 @@ struct Cut {
     int64_t prefix_cost;  // cost of the prefix tiles
     int64_t run;          // cost per unit
     int32_t shared;       // keys of the shared prefix (a multiple of kKeys; 0: none)
+    int32_t least;        // sequences of at least so many tokens share it
     int32_t source;       // batch row whose pages hold it
 };
 
@@ -113,10 +114,10 @@ __device__ __forceinline__ int batch_len(const CacheParams& p, int b, int* row, 
     return n < 0 ? 0 : n > cap ? cap : n;
 }
 
-// Keys of batch row b before its own ones, and steps over its own.
-__device__ __forceinline__ int own_start(int len, int shared) { return len >= shared ? shared : 0; }
-__device__ __forceinline__ int own_steps(int len, int shared) {
-    return (len - own_start(len, shared) + kKeys - 1) / kKeys;
+// Keys of a sequence before its own ones, and steps over its own.
+__device__ __forceinline__ int own_start(int len, int shared, int least) { return len >= least ? shared : 0; }
+__device__ __forceinline__ int own_steps(int len, int shared, int least) {
+    return (len - own_start(len, shared, least) + kKeys - 1) / kKeys;
 }
 __device__ __forceinline__ int64_t seq_cost(const CacheParams& p, int steps) {
     return steps ? static_cast<int64_t>(p.head_tiles) * (steps + p.overhead) : 0;
@@ -156,7 +157,7 @@ struct Piece {
 // tiles leave: 1.2 to 3 us a piece against 0.4).
 struct Walk {
     int64_t at, end, prefix_cost, base;  // base: cost before batch row b
-    int shared, source_row, b, len, row, unit;
+    int shared, least, source_row, b, len, row, unit;
 
     __device__ __forceinline__ void enter(const CacheParams& p) {
         int bits = 0;
@@ -180,12 +181,12 @@ struct Walk {
                 x->end = shared;
                 x->prefix = true;
             } else {
-                steps = own_steps(len, shared);
+                steps = own_steps(len, shared, least);
                 while (b < p.B && at >= base + seq_cost(p, steps)) {
                     base += seq_cost(p, steps);
                     ++b;
                     enter(p);
-                    steps = own_steps(len, shared);
+                    steps = own_steps(len, shared, least);
                 }
                 if (b >= p.B) return false;
                 const int ht = p.head_tiles == 1 ? 0 : quotient(at - base, steps + p.overhead);
@@ -194,7 +195,7 @@ struct Walk {
                 x->rows = min(kRows, p.H - ht * kRows);
                 tile_row = static_cast<int64_t>(p.row_tiles) * kRows + x->row0;
                 x->page_row = row;
-                x->key0 = own_start(len, shared);
+                x->key0 = own_start(len, shared, least);
                 x->end = len;
                 x->prefix = false;
             }
@@ -265,15 +266,16 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
         return b < p.B ? batch_len(p, b, &row, &bits) : 0;
     };
     // who shares the prefix
-    int shared = p.shared_len ? *p.shared_len : 0;
-    const int cap = p.max_pages * p.page_size;
+    // (the callers' word holds for sequences of `least` tokens or more; the prefix is handled in whole steps)
+    const int least = p.shared_len ? *p.shared_len : 0, cap = p.max_pages * p.page_size;
+    int shared = least;
     shared = shared < 0 ? 0 : (shared > cap ? cap : shared) / kKeys * kKeys;
     if (threadIdx.x == 0) sh->sharers = 0, sh->source = p.B;
     __syncthreads();
     if (shared > 0) {
         int count = 0, first = p.B;
         for (int b = threadIdx.x; b < p.B; b += kThreads)
-            if (len_of(b) >= shared) ++count, first = min(first, b);
+            if (len_of(b) >= least) ++count, first = min(first, b);
         if (count) {
             atomicAdd(&sh->sharers, count);
             atomicMin(&sh->source, first);
@@ -287,7 +289,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
     for (int b0 = 0; b0 < p.B; b0 += kThreads) {
         const int b = b0 + threadIdx.x;
         const int len = len_of(b);
-        const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
+        const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared, least)) : 0;
         const int64_t before = total + block_scan(mine, sh->scan, &sum);
         if (writer && b < p.B) p.bases[b] = before;
         if (b0 == 0) first_base = before, first_cost = mine;
@@ -296,7 +298,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
     int64_t run = (total + p.units - 1) / p.units;
     if (run < kMinRun + p.overhead) run = kMinRun + p.overhead;
     if (writer) {
-        if (threadIdx.x == 0) *p.cut = Cut{prefix, run, shared, source};
+        if (threadIdx.x == 0) *p.cut = Cut{prefix, run, shared, least, source};
         raise_status(p.status, bits);
     }
     w->unit = unit;
@@ -304,6 +306,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
     w->end = w->at + run < total ? w->at + run : total;
     w->prefix_cost = prefix;
     w->shared = shared;
+    w->least = least;
     w->b = 0;
     w->base = prefix;
     w->len = w->row = 0;
@@ -319,7 +322,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
             for (int b0 = 0; b0 < p.B; b0 += kThreads) {
                 const int b = b0 + threadIdx.x;
                 const int len = len_of(b);
-                const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared)) : 0;
+                const int64_t mine = b < p.B ? seq_cost(p, own_steps(len, shared, least)) : 0;
                 const int64_t before = base + block_scan(mine, sh->scan, &sum);
                 if (mine && w->at >= before && w->at < before + mine) sh->first_b = b, sh->first_base = before;
                 base += sum;
@@ -516,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (start.shared && direct && mine) {
                 int trow, bits = 0;
                 const int len = batch_len(p, b, &trow, &bits);
-                direct = x.prefix ? len == start.shared : len < start.shared;
+                direct = x.prefix ? len >= start.least && len == start.shared : len < start.least;
             }
             // A warp's rows pass through shared memory, 128 bytes of each at a time, so that it stores four rows'
             // whole lines at once: 64 columns of finished rows, 32 of partial ones.
@@ -828,11 +831,11 @@ __global__ void __launch_bounds__(128) mla_attend_join_kernel(const __grid_const
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         if (k == 0) {
-            steps[0] = len >= cut.shared ? cut.shared / kKeys : 0;
+            steps[0] = len >= cut.least ? cut.shared / kKeys : 0;
             base[0] = row / kRows * (cut.shared / kKeys + p.overhead);
             part[0] = row;
         } else {
-            steps[1] = own_steps(len, cut.shared);
+            steps[1] = own_steps(len, cut.shared, cut.least);
             base[1] = p.bases[b] + static_cast<int64_t>(h / kRows) * (steps[1] + p.overhead);
             part[1] = static_cast<int64_t>(p.row_tiles) * kRows + row;
         }

@@ -396,6 +396,16 @@ def test_cache_shared_length_inside_a_page_and_beyond():
         check_cache(c, out, lse)
 
 
+def test_cache_sequences_a_little_shorter_than_the_shared_prefix():
+    """Pages are shared from shared_len tokens on; a shorter sequence has its
+    own, however near its length is."""
+    for shared, lens in ((208, [258, 200, 207, 400, 208, 193, 130]), (144, [144, 130, 143, 500, 128, 64]), (80, [80, 64, 79, 81, 200])):
+        c = cache_case(32, lens, 16, 512, 64, 16, shared)
+        out, lse, status = run_cache(c)
+        assert status == 0
+        check_cache(c, out, lse)
+
+
 def test_cache_one_long_sequence_among_short_ones():
     c = cache_case(4, [9000, 3, 0, 17], 16, 512, 64, 64)
     out, lse, status = run_cache(c)
