@@ -545,32 +545,35 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* out = reinterpret_cast<uint8_t*>(p.out + (x.row0 + row32) * p.Lkv + dv0);
             uint8_t* part = reinterpret_cast<uint8_t*>(p.part_o + (x.part + row32) * p.Lkv + dv0);
 #pragma unroll 1
-            for (int d = 0; d < dv; d += 64) {
-                uint32_t o[64];  // (what lies behind dv is not stored)
-                tmem_ld64_raw(to + d, o);
+            for (int d0 = 0; d0 < dv; d0 += 128) {
+                uint32_t o[128];  // (what lies behind dv is not stored)
+                tmem_ld128_max(to + d0, o);
 #pragma unroll
-                for (int i = 0; i < 64; ++i) o[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
-                const int left = dv - d;
+                for (int i = 0; i < 128; ++i) o[i] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
                 if (part_rows) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        if (k * 32 >= left) break;
+                    for (int k = 0; k < 4; ++k) {
+                        if (d0 + k * 32 >= dv) break;
 #pragma unroll
                         for (int i = 0; i < 8; ++i)
                             put(i, o[k * 32 + 4 * i], o[k * 32 + 4 * i + 1], o[k * 32 + 4 * i + 2], o[k * 32 + 4 * i + 3]);
-                        flush(part + (d + k * 32) * 4, p.Lkv * 4, part_rows, (left - k * 32) * 4);
+                        flush(part + (d0 + k * 32) * 4, p.Lkv * 4, part_rows, (dv - d0 - k * 32) * 4);
                     }
                 }
                 if (direct_rows) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        uint32_t w[4];
+                    for (int k = 0; k < 2; ++k) {
+                        if (d0 + k * 64 >= dv) break;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            w[e] = pack_bf16x2(__uint_as_float(o[8 * i + 2 * e]), __uint_as_float(o[8 * i + 2 * e + 1]));
-                        put(i, w[0], w[1], w[2], w[3]);
+                        for (int i = 0; i < 8; ++i) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                w[e] = pack_bf16x2(__uint_as_float(o[k * 64 + 8 * i + 2 * e]), __uint_as_float(o[k * 64 + 8 * i + 2 * e + 1]));
+                            put(i, w[0], w[1], w[2], w[3]);
+                        }
+                        flush(out + (d0 + k * 64) * 2, p.Lkv * 2, direct_rows, (dv - d0 - k * 64) * 2);
                     }
-                    flush(out + d * 2, p.Lkv * 2, direct_rows, left * 2);
                 }
             }
             if (mine && side == 0) {
