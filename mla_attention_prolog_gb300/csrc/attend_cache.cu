@@ -422,8 +422,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int n = x.n, keys = x.end - x.key0;
             float m = -INFINITY, ms = 0.f, l = 0.f;  // row maximum of S, ms = m c, sum of this thread's half of P
             for (int j = 0; j < n; ++j, ++step) {
-                ok = __all_sync(~0u, wait(&sh->s_full[step % kAhead], step / kAhead));
-                // (a barrier of the whole group follows in every step: it leaves together)
+                // A failed wait stays failed, and the step makes and hands over nothing after it; a barrier of the
+                // whole group follows in every step, where all four warps learn of it and leave together.
+                ok = __all_sync(~0u, ok && wait(&sh->s_full[step % kAhead], step / kAhead));
                 uint32_t s[32];
                 tc_fence_after();
                 float mt = tmem_ld32_max(ts + step % kAhead * 32, s);
@@ -476,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (step > 1) ok = __all_sync(~0u, ok && wait(&sh->pv_done[step & 1], (step >> 1) - 1));
                 if (j > 0 && __any_sync(~0u, alpha != 1.f)) {
                     ok = __all_sync(~0u, ok && wait(&sh->pv_done[(step - 1) & 1], (step - 1) >> 1));
+                    if (!ok) continue;
                     tc_fence_after();
 #pragma unroll 1
                     for (int d = 0; d < p.dv_half; d += 16) {
@@ -486,6 +488,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_st16(to + d, o);
                     }
                 }
+                if (!ok) continue;
                 const uint32_t dst = sm_p + (step & 1) * kPBytes + r * 128;
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -494,6 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (rest < kKeys) {
                     // rows behind the end may hold anything: as values they have to be zero
                     ok = __all_sync(~0u, ok && wait(&sh->v_seen, tails));
+                    if (!ok) continue;
                     ++tails;
                     for (int k = threadIdx.x; k < (kKeys - rest) * nvc * 8; k += 128) {
                         const int row = rest + k / (nvc * 8), in = k % (nvc * 8);
