@@ -410,6 +410,8 @@ def _run(f, name: str, index: int, stream: Optional[torch.cuda.Stream], *args) -
         raise MlaPrologError(rc, name)
 
 
+# Keyed by numbers alone (a scale that is a tensor is read at each call: its
+# key would be the object, whatever it holds by then).
 @functools.lru_cache(maxsize=256)
 def _prompt_dims(*sizes):
     return ctypes.byref(MlaPrologPromptDims(*sizes))
@@ -449,7 +451,7 @@ def attend_prompt(q, k, v, cu_q, cu_k, out, lse=None, *, scale: float, causal: b
             scale_shape = (Tq, H)
         q_scale = _at(q_scale, "q_scale", _F32, scale_shape, index)
     _run((_lib or lib()).mla_prolog_attend_prompt, "mla_prolog_attend_prompt", index, stream,
-         _prompt_dims(Tq, Tk, n - 1, H, Hk, Dqk, Dv, scale, flags), _at(q, "q", q_type, (Tq, H, Dqk), index), q_scale,
+         _prompt_dims(Tq, Tk, n - 1, H, Hk, Dqk, Dv, float(scale), flags), _at(q, "q", q_type, (Tq, H, Dqk), index), q_scale,
          _at(k, "k", _BF16, (Tk, Hk, Dqk), index), _at(v, "v", _BF16, (Tk, Hk, Dv), index),
          _at(cu_q, "cu_q", _I32, (n,), index), _at(cu_k, "cu_k", _I32, (n,), index),
          _at(out, "out", _BF16, (Tq, H, Dv), index), None if lse is None else _at(lse, "lse", _F32, (Tq, H), index),
@@ -483,7 +485,7 @@ def attend_cache(q, kv_cache, page_table, seq_lens, out, lse, workspace, *, scal
                               (workspace, "workspace", 1)):
             _on(t, name, dims)
     _run((_lib or lib()).mla_prolog_attend_cache, "mla_prolog_attend_cache", index, stream,
-         _cache_dims(B, H, Lkv, C - Lkv, page_size, S, width, scale, pages), _at(q, "q", _BF16, (B, H, C), index),
+         _cache_dims(B, H, Lkv, C - Lkv, page_size, S, width, float(scale), pages), _at(q, "q", _BF16, (B, H, C), index),
          _at(kv_cache, "kv_cache", _BF16, (pages, page_size, C), index),
          _at(page_table, "page_table", _I32, (S, width), index), _at(seq_lens, "seq_lens", _I32, (S,), index),
          None if seqs is None else _at(seqs, "seqs", _I32, (B,), index),
