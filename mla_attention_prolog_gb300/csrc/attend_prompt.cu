@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = r < rows;
         float c = p.scale * kLog2e;
         if (p.q8 && n) {
-            const float qs = mine ? p.q_scale[p.q_per_head ? at : jb.q0 + row] : 0.f;
+            // (a row without a key takes no scale, which may be anything: its answer is 0)
+            const float qs = mine && limit(row) > 0 ? p.q_scale[p.q_per_head ? at : jb.q0 + row] : 0.f;
             c *= fabsf(qs);  // a negative scale turns the codes' sign, so that c > 0 keeps the order of the scores
             if (c < 1e-30f) c = 1e-30f;  // a zero row: its scores are 0 (hidden ones stay -inf)
             // The warp's 32 rows of codes in pieces of 16, a lane's pieces 32 apart: neighbouring lanes read

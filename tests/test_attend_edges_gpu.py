@@ -1,12 +1,14 @@
 """Attention operators on the GPU: calls at the edges of their contracts.
 Tolerances as derived in test_attend_gpu.py."""
+import math
+
 import pytest
 import torch
 
 pytestmark = pytest.mark.gpu
 
 from mla_attention_prolog_gb300 import binding  # noqa: E402
-from test_attend_gpu import cache_case, prompt_case, run_cache, run_prompt  # noqa: E402
+from test_attend_gpu import cache_case, check_prompt, prompt_case, run_cache, run_prompt  # noqa: E402
 
 
 def same(a, b):
@@ -22,3 +24,21 @@ def test_a_scale_that_is_a_tensor_is_read_at_each_call(device):
         as_float = float(scale)   # the FP32 number that the tensor holds
         for case, run in ((p, run_prompt), (c, run_cache)):
             assert same(run({**case, "scale": scale}), run({**case, "scale": as_float}))
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("q", ["int8", "int8_per_head"])
+def test_rows_without_a_key_whatever_their_scale(q, bad):
+    """Three of five queries come before the first key; their scale is no number."""
+    c = prompt_case(42, [5, 200], [2, 131], 4, 2, 192, 128, q=q)
+    want = run_prompt(c)
+    check_prompt(c, *want[:2])
+    for rows in (slice(0, 3), slice(5, 74)):
+        c["q_scale"][rows] = bad
+    got = run_prompt(c)
+    assert got[2] == 0 and same(got, want)
+    for rows in (slice(0, 3), slice(5, 74)):
+        assert (got[0][rows] == 0).all() and torch.isneginf(got[1][rows]).all()
+    c["q_scale"][3] = bad   # a row that has keys
+    got = run_prompt(c)
+    assert not torch.isfinite(got[0][3].float()).any() and same([x[4:] for x in got[:2]], [x[4:] for x in want[:2]])
