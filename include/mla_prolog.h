@@ -624,7 +624,7 @@ int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* dims, const void* q, 
  * are kept in FP32 and joined in a fixed order, so equal inputs give equal
  * bits.
  *
- * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): batch >= 0, num_heads >= 1,
+ * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): 0 <= batch <= 2^17, num_heads >= 1,
  * batch * num_heads <= 2^24; Lkv a positive multiple of 16 up to 512, R a
  * multiple of 16 (0 .. 128) with Lkv + R <= 576; page_size a positive
  * multiple of 16; num_pages * page_size <= 2^31 - 1; max_pages >= 1 and

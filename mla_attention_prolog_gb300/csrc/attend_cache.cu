@@ -70,6 +70,10 @@ constexpr int kFetch = 1;
 constexpr int kOverhead = 4, kRowsPerStep = 16;
 constexpr int kMinRun = 4;                // shortest run worth a CTA pair, in key steps after its tile's start (1 to 16 measure alike)
 
+// A walk passes over empty sequences one by one, in a role that others wait for: so many take 74 ms (0.56 us each), far
+// below the waits' limit.
+constexpr int kMaxBatch = 1 << 17;
+
 // What the join kernel needs to know of the cut (start of the workspace).
 struct Cut {
     int64_t prefix_cost;  // cost of the prefix tiles
@@ -903,7 +907,7 @@ __global__ void __launch_bounds__(128) mla_attend_join_kernel(const __grid_const
 
 int check_cache_dims(const mla_prolog_cache_dims& d) {
     const int64_t most = INT32_MAX;
-    if (d.batch < 0 || d.num_heads < 1 || static_cast<int64_t>(d.batch) * d.num_heads > (1 << 24) ||
+    if (d.batch < 0 || d.batch > kMaxBatch || d.num_heads < 1 || static_cast<int64_t>(d.batch) * d.num_heads > (1 << 24) ||
         d.kv_lora_rank < 16 || d.kv_lora_rank > 512 || d.kv_lora_rank % 16 || d.rope_dim < 0 || d.rope_dim > 128 ||
         d.rope_dim % 16 || d.kv_lora_rank + d.rope_dim > 576)
         return MLA_ERR_UNSUPPORTED_DIMS;

@@ -8,7 +8,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from mla_attention_prolog_gb300 import binding  # noqa: E402
-from test_attend_gpu import cache_case, check_prompt, prompt_case, run_cache, run_prompt  # noqa: E402
+from test_attend_gpu import DEV, cache_case, check_cache, check_prompt, prompt_case, run_cache, run_prompt  # noqa: E402
 
 
 def same(a, b):
@@ -42,3 +42,25 @@ def test_rows_without_a_key_whatever_their_scale(q, bad):
     c["q_scale"][3] = bad   # a row that has keys
     got = run_prompt(c)
     assert not torch.isfinite(got[0][3].float()).any() and same([x[4:] for x in got[:2]], [x[4:] for x in want[:2]])
+
+
+def test_cache_the_largest_batch_nearly_all_of_it_empty():
+    """One run passes over all the empty sequences between two others."""
+    B = 1 << 17
+    lens = [70] + [0] * (B - 2) + [90]
+    c = cache_case(43, [70, 90], 1, 64, 16, 16)
+    seqs = torch.full((B,), 2, dtype=torch.int32, device=DEV)
+    seqs[0], seqs[-1] = 0, 1
+    table = torch.cat([c["table"], torch.full_like(c["table"][:1], -1)])
+    q = torch.zeros((B, 1, 80), dtype=torch.bfloat16, device=DEV)
+    q[0], q[-1] = c["q"][0], c["q"][1]
+    for order in (seqs, None):
+        d = {**c, "q": q, "table": table, "lens": torch.cat([c["lens"], torch.zeros_like(c["lens"][:1])])}
+        if order is None:
+            d["table"] = table[2:].repeat(B, 1)
+            d["table"][0], d["table"][-1] = table[0], table[1]
+            d["lens"] = torch.tensor(lens, dtype=torch.int32, device=DEV)
+        out, lse, status = run_cache(d, seqs=order)
+        assert status == 0
+        check_cache(c, out[[0, -1]], lse[[0, -1]])
+        assert (out[1:-1] == 0).all() and torch.isneginf(lse[1:-1]).all()
