@@ -611,11 +611,13 @@ int mla_prolog_attend_prompt(const mla_prolog_prompt_dims* dims, const void* q, 
  *   lse = log sum_j exp(s_j),   j = 0 .. seq_lens[b] - 1
  *
  * row_j is the row of slot page_table[b][j / page_size] * page_size +
- * j % page_size of the cache.  The keys of a prefix that the batch shares
- * are read and multiplied once for all rows of the batch: with
+ * j % page_size of the cache.  A prefix may be shared: with
  * *shared_len = n > 0 the caller states that the sequences of at least n
  * tokens have the same pages under their first n tokens (as
- * mla_prolog_pages_fork() leaves them).  Sequences shorter than n (a padded
+ * mla_prolog_pages_fork() leaves them).  Its keys are then read and multiplied
+ * once for 128 rows (sequence, head) of the batch, where that is less work than
+ * once for each sequence that shares them (chosen by sizes and lengths; the
+ * two differ by roundings).  Sequences shorter than n (a padded
  * batch's empty rows among them) are handled on their own.  A sequence of
  * length 0 gets out = 0 and lse = -inf.  Rows past a sequence's end never
  * reach a result, whatever they hold.

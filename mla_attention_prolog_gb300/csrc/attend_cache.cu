@@ -1,10 +1,10 @@
 // One decoding step over the latent KV cache: mla_prolog_attend_cache.
 //
 // A tile is 128 query rows (sequence, head) that see the same keys: the rows
-// of one sequence on its own pages, or 128 rows of any sequences on the
-// shared prefix, whose rows are thus read and multiplied once per 128 rows
-// instead of once per sequence.  Every key is one cache row of Lkv + R
-// columns, of which the first Lkv are the value too.
+// of one sequence on its own pages, or, where that takes fewer steps, 128 rows
+// of any sequences on the shared prefix, whose rows are then read and
+// multiplied once per 128 rows instead of once per sequence.  Every key is one
+// cache row of Lkv + R columns, of which the first Lkv are the value too.
 //
 //   S = Q K^T   128 x 64 keys, 576 deep     O += P V   128 x Lkv, 64 deep
 //
@@ -68,6 +68,9 @@ constexpr int kFetch = 1;
 // A tile's start and end, in key steps: so many, and one per so many rows.  (V2-Lite 64 sequences, V3 shared prefix: 48
 // and 240 us; 4 alone 49 and 289; 3 and one per 32 rows 51 and 255; 2 or 3 and one per 16 rows 51 and 239.)
 constexpr int kOverhead = 4, kRowsPerStep = 16;
+// A shared prefix in tiles of its own makes a partial result of every row and leaves the rows that share it to the join:
+// as many key steps of each CTA pair (see prefix_pays()).
+constexpr int kJoinSteps = 4;
 constexpr int kMinRun = 4;                // shortest run worth a CTA pair, in key steps after its tile's start (1 to 16 measure alike)
 
 // A walk passes over empty sequences one by one, in a role that others wait for: so many take 74 ms (0.56 us each), far
@@ -125,6 +128,18 @@ __device__ __forceinline__ int own_steps(int len, int shared, int least) {
 }
 __device__ __forceinline__ int64_t seq_cost(const CacheParams& p, int steps) {
     return steps ? static_cast<int64_t>(p.head_tiles) * (steps + p.overhead) : 0;
+}
+
+// Whether a prefix that `sharers` sequences share is multiplied in tiles of its own, which hold the rows of the whole
+// batch (of sequences that do not share it, too), rather than by each of them with its own keys: the fewer key steps
+// win.  128 rows of more than one sequence have to share a tile for that, so few of 128 heads or more do, nor do a few
+// sequences of a large batch.  In us, tiles of their own / with the own keys, 128 sequences of 1 to 1024 behind 8192:
+// 128 heads 231 / 220, 96 heads 191 / 215, 64 heads 143 / 213, 16 heads 69 / 206; 128 heads of which 2 share 199 / 38;
+// 64 heads of which 32 / 64 / 80 share 121 / 72, 130 / 119, 134 / 144; 16 heads of which 16 / 20 / 32 share 48 / 46, 50 / 52,
+// 52 / 68.  64 sequences of 16 heads behind 64 / 256 / 1024: 33 / 31, 35 / 35, 36 / 43; 8 behind 128: 25 / 21.
+__device__ __forceinline__ bool prefix_pays(const CacheParams& p, int shared, int sharers) {
+    const int64_t steps = shared / kKeys;
+    return p.row_tiles * (steps + p.overhead) + static_cast<int64_t>(p.units) * kJoinSteps < sharers * steps * p.head_tiles;
 }
 
 // Most quotients here fit 32 bits, whose division takes a third of the time.
@@ -285,7 +300,7 @@ __device__ __forceinline__ bool make_cut(const CacheParams& p, int unit, Shared*
             atomicMin(&sh->source, first);
         }
         __syncthreads();
-        if (sh->sharers < 2) shared = 0;
+        if (!prefix_pays(p, shared, sh->sharers)) shared = 0;
     }
     const int source = sh->source;
     const int64_t prefix = shared ? static_cast<int64_t>(p.row_tiles) * (shared / kKeys + p.overhead) : 0;

@@ -64,3 +64,53 @@ def test_cache_the_largest_batch_nearly_all_of_it_empty():
         assert status == 0
         check_cache(c, out[[0, -1]], lse[[0, -1]])
         assert (out[1:-1] == 0).all() and torch.isneginf(lse[1:-1]).all()
+
+
+def differ_by_roundings(a, b):
+    """Another cut of the same keys: results that are joined from other pieces."""
+    return not same(a, b)
+
+
+@pytest.mark.parametrize("H,lens,shared", [(16, [1024 + 40, 1024] + [0] * 38, 1024), (16, [0, 3] * 20 + [2048 + 1, 2100], 2048),
+                                           (128, [1100, 1024, 1500, 2000], 1024), (64, [300] * 8, 256)])
+def test_cache_a_prefix_that_is_not_worth_tiles_of_its_own(H, lens, shared):
+    """A shared length that saves no work changes nothing, not a bit."""
+    c = cache_case(44, lens, H, 512, 64, 64, shared)
+    prefix = c["rows"][max(range(len(lens)), key=lens.__getitem__)][:shared]
+    if lens[0] < shared:   # cache_case fills the prefix for a first sequence that shares it
+        g = torch.Generator(DEV).manual_seed(1)
+        c["cache"].view(-1, 576)[prefix] = torch.randn((shared, 576), generator=g, device=DEV).to(torch.bfloat16)
+    got = run_cache(c)
+    assert got[2] == 0 and same(got, run_cache(c, shared=False))
+    check_cache(c, *got[:2])
+
+
+@pytest.mark.parametrize("dims,page,shared,n", [((16, 512, 64), 64, 1024, 60), ((16, 512, 64), 16, 1040, 60), ((64, 512, 64), 64, 2048, 48),
+                                                ((130, 512, 64), 64, 2048, 40), ((5, 256, 32), 48, 672, 64), ((1, 512, 0), 16, 720, 150)])
+def test_cache_a_prefix_in_tiles_of_its_own(dims, page, shared, n):
+    """Many sequences that end at the prefix, a little behind it or far, among
+    empty and shorter ones; in the order of seqs, too."""
+    lens = [shared + (0, 1, 63, 64, 200)[i % 5] for i in range(n)] + [0, shared - 1, shared // 2]
+    c = cache_case(45, lens, *dims, page, shared)
+    got = run_cache(c)
+    assert got[2] == 0 and differ_by_roundings(got, run_cache(c, shared=False))
+    check_cache(c, *got[:2])
+    again = run_cache(c)
+    assert same(got, again)
+    order = list(reversed(range(len(lens))))
+    seqs = torch.tensor(order, dtype=torch.int32, device=DEV)
+    got = run_cache(c, seqs=seqs)
+    assert got[2] == 0
+    check_cache(c, *got[:2], order)
+
+
+def test_cache_a_nan_in_the_prefix_reaches_only_those_who_share_it():
+    shared = 1024
+    lens = [shared + i for i in range(60)] + [0, 100, shared - 1, shared - 64]
+    c = cache_case(46, lens, 16, 512, 64, 64, shared)
+    want = run_cache(c)
+    row = int(c["rows"][0][500])
+    c["cache"].view(-1, 576)[row, 3] = math.nan
+    out, lse, status = run_cache(c)
+    assert status == 0 and torch.isnan(out[:60].float()).all() and torch.isnan(lse[:60]).all()
+    assert same((out[60:], lse[60:]), (want[0][60:], want[1][60:]))
