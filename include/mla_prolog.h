@@ -684,7 +684,11 @@ int mla_prolog_attend_cache_workspace(const mla_prolog_cache_dims* dims, size_t*
  * table entries that hold page p; a page with refs 0 is free, and the lowest
  * free pages are taken first, so equal states give equal results.  Table
  * entries behind a sequence's pages are -1.  The calls below move whole
- * numbers only; mla_prolog_copy_pages() moves the cache's contents.
+ * numbers only; mla_prolog_copy_pages() moves the cache's contents.  A length
+ * outside [0, max_pages * page_size] is cut to it and sets
+ * MLA_STATUS_SEQ_RANGE; a page of a listed sequence outside [0, num_pages) is
+ * left as it is, gets no slot, copy or reference, and sets
+ * MLA_STATUS_PAGE_RANGE.
  * Calls on one pool must be ordered (one stream).
  * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): sequences, num_pages >= 0;
  * page_size, max_pages >= 1; num_pages * page_size <= 2^31 - 1 and max_pages *

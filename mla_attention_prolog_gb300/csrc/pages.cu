@@ -43,6 +43,8 @@ __device__ __forceinline__ int cut_len(const Pool& p, int n) {
     const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
     return n < 0 ? 0 : (n > cap ? static_cast<int>(cap) : n);
 }
+__device__ __forceinline__ int len_bits(const Pool& p, int n) { return cut_len(p, n) != n ? kStatusSeqRange : 0; }
+__device__ __forceinline__ bool in_pool(const Pool& p, int32_t page) { return page >= 0 && page < p.num_pages; }
 
 // Exclusive prefix sums over the block, in place; total[k]: the block's sums.
 // All threads call it.
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_extend_kernel(Pool p, cons
             bits |= kStatusSeqRange;
         } else {
             len = cut_len(p, held);
+            bits |= len_bits(p, held);
             if (len + static_cast<int64_t>(c) > cap) {
                 bits |= kStatusPoolFull;
             } else {
@@ -291,7 +294,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_extend_kernel(Pool p, cons
         const int run = total > kThreads ? 4 : 1;
         for (int j0 = t * run; j0 < total; j0 += kThreads * run) {
             int e = j0 < tokens ? find_entry(tok, n, j0) : n, pos = 0, slot = 0, room = 0;
-            bool good = false, fresh = true;
+            bool good = false, fresh = true, paged = false;
             for (int j = j0; j < j0 + run && j < total; ++j) {
                 while (e < n && j >= (e + 1 < n ? tok[e + 1] : tokens)) ++e, fresh = true;
                 if (fresh) {
@@ -302,10 +305,13 @@ __global__ void __launch_bounds__(kThreads) mla_pages_extend_kernel(Pool p, cons
                 }
                 if (good && room == 0) {
                     const int in = pos % p.page_size;
-                    slot = p.table[static_cast<int64_t>(seq[e]) * p.max_pages + pos / p.page_size] * p.page_size + in;
+                    const int32_t page = p.table[static_cast<int64_t>(seq[e]) * p.max_pages + pos / p.page_size];
+                    paged = in_pool(p, page);  // (the page that the sequence ended in need not be)
+                    slot = paged ? page * p.page_size + in : 0;
                     room = p.page_size - in;
+                    if (!paged) bits |= kStatusPageRange;
                 }
-                if (slots) slots[j] = good ? slot : -1;
+                if (slots) slots[j] = good && paged ? slot : -1;
                 if (positions) positions[j] = good ? pos : 0;
                 ++slot, ++pos, --room;
             }
@@ -338,6 +344,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_fork_kernel(Pool p, const 
     if (mine) {
         const bool good = from && to && empty == 0 && scratch.firsts.place[bucket] == t;
         if (!good) bits |= kStatusSeqRange;
+        if (good) bits |= len_bits(p, held);
         par[t] = a;
         child[t] = c;
         len[t] = good ? cut_len(p, held) : 0;
@@ -361,8 +368,9 @@ __global__ void __launch_bounds__(kThreads) mla_pages_fork_kernel(Pool p, const 
             const int full = len[e] / p.page_size;
             p.table[static_cast<int64_t>(child[e]) * p.max_pages + full] = page;
             p.refs[page] = 1;
-            src[e] = p.table[static_cast<int64_t>(par[e]) * p.max_pages + full];
-            dst[e] = page;
+            const int32_t old = p.table[static_cast<int64_t>(par[e]) * p.max_pages + full];
+            if (in_pool(p, old)) src[e] = old, dst[e] = page;
+            else bits |= kStatusPageRange;
         });
     // the shared pages: a warp per child
     for (int e = t >> 5; e < n; e += kWarps) {
@@ -373,7 +381,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_fork_kernel(Pool p, const 
         for (int j = t & 31; j < full; j += 32) {
             const int32_t page = old[j];
             row[j] = page;
-            if (page >= 0 && page < p.num_pages) atomicAdd(p.refs + page, 1);
+            if (in_pool(p, page)) atomicAdd(p.refs + page, 1);
             else bits |= kStatusPageRange;
         }
         if ((t & 31) == 0) p.lens[child[e]] = len[e];
@@ -397,6 +405,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_release_kernel(Pool p, con
     int bits = t < n && !inside ? kStatusSeqRange : 0;
     if (t < n) {
         seq[t] = inside && firsts.place[bucket] == t ? s : -1;  // the first listing ends the sequence
+        if (seq[t] >= 0) bits |= len_bits(p, len);
         held[t] = ceil_div(cut_len(p, len), p.page_size);
     }
     __syncthreads();
@@ -407,7 +416,7 @@ __global__ void __launch_bounds__(kThreads) mla_pages_release_kernel(Pool p, con
             const int32_t page = row[j];
             row[j] = -1;
             if (j >= held[e]) continue;
-            if (page >= 0 && page < p.num_pages) atomicSub(p.refs + page, 1);
+            if (in_pool(p, page)) atomicSub(p.refs + page, 1);
             else bits |= kStatusPageRange;
         }
         if ((t & 31) == 0) p.lens[seq[e]] = 0;
