@@ -8,7 +8,8 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from mla_attention_prolog_gb300 import binding  # noqa: E402
-from test_attend_gpu import DEV, cache_case, check_cache, check_prompt, prompt_case, run_cache, run_prompt  # noqa: E402
+from test_attend_gpu import (DEV, POISON, cache_case, check, check_cache, check_prompt, prompt_case, row_attention,  # noqa: E402
+                             run_cache, run_prompt)
 
 
 def same(a, b):
@@ -114,3 +115,88 @@ def test_cache_a_nan_in_the_prefix_reaches_only_those_who_share_it():
     out, lse, status = run_cache(c)
     assert status == 0 and torch.isnan(out[:60].float()).all() and torch.isnan(lse[:60]).all()
     assert same((out[60:], lse[60:]), (want[0][60:], want[1][60:]))
+
+
+def cut_to(cu, rows):
+    """What the contract makes of offsets: [(first row, rows)] of each sequence."""
+    inside = [min(max(x, 0), rows) for x in cu]
+    return [(a, max(b - a, 0)) for a, b in zip(inside, inside[1:])]
+
+
+OFFSETS = [([0, 40, 1000], [0, 40, 90]), ([-4, 40, 90], [0, 40, 90]), ([0, 60, 40], [0, 60, 90]), ([95, 95, 200], [0, 40, 90]),
+           ([0, 40, 90], [0, 40, 1000]), ([0, 40, 90], [-7, 40, 90]), ([0, 40, 90], [0, 60, 40]), ([0, 40, 90], [91, 300, 1 << 30]),
+           ([0, 1 << 30, -(1 << 31)], [0, 50, 90]), ([-5, -2, 90], [-(1 << 31), 30, (1 << 31) - 1])]
+
+
+@pytest.mark.parametrize("cu_q,cu_k", OFFSETS)
+@pytest.mark.parametrize("extra", [0, 40])   # empty sequences behind: one look of a warp, and more
+@pytest.mark.parametrize("q", ["bf16", "int8"])
+def test_prompt_offsets_outside_the_buffers_are_cut(cu_q, cu_k, extra, q):
+    """Sequences are cut to their rows inside the buffers, by definition, and
+    rows of none stay as they were."""
+    c = prompt_case(47, [40, 50], [40, 50], 4, 2, 64, 64, q=q, pad=0)
+    cu_q, cu_k = cu_q + [cu_q[-1]] * extra, cu_k + [cu_k[-1]] * extra
+    for name, cu in (("cu_q", cu_q), ("cu_k", cu_k)):
+        c[name] = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    out, lse, status = run_prompt(c)
+    assert status == binding.STATUS_SEQ_RANGE
+    own = torch.zeros(90, dtype=torch.bool, device=DEV)
+    for (a, n), (b, t) in zip(cut_to(cu_q, 90), cut_to(cu_k, 90)):
+        own[a:a + n] = True
+        i, j = torch.arange(n, device=DEV)[:, None], torch.arange(t, device=DEV)[None, :]
+        k, v = (c[x][b:b + t].double().permute(1, 0, 2).repeat_interleave(2, 0) for x in "kv")
+        o, z, to, tz = row_attention(c["qd"][a:a + n].permute(1, 0, 2), k, v, c["scale"], j > i + (t - n))
+        check(out[a:a + n].permute(1, 0, 2), o, to, f"out of the rows from {a}")
+        check(lse[a:a + n].t(), z, tz, f"lse of the rows from {a}")
+    assert (out[~own].view(torch.int16) == POISON).all() and (lse[~own] == 123.0).all()
+
+
+@pytest.mark.parametrize("name,T,per_head", [("tiny_q", 150, False), ("tiny_q", 150, True), ("v3_decode", 128, False)])
+def test_prompt_on_the_codes_scales_keys_and_values_of_the_prolog(name, T, per_head):
+    """The prolog's INT8 q and its scales, K and V, as it leaves them, behind it
+    in the stream; then a chain of both, with other inputs each time, against
+    the same chain with a synchronize between any two."""
+    import dataclasses
+    from helpers import alloc_outputs, device_inputs, run_prolog
+    from mla_attention_prolog_gb300 import workloads as wl
+    w = wl.WORKLOADS[name]
+    d = dataclasses.replace(w.dims, T=T, max_pos=max(T, w.dims.max_pos), flags=w.dims.flags | (0x8 if per_head else 0))
+    dev = torch.device(DEV, torch.cuda.current_device())
+    x = device_inputs(wl.make_inputs(w, d), dev)
+    outs = alloc_outputs(d, dev)
+    p = binding.MlaProlog.from_dims(d)
+    H, D, E = d.num_heads, d.nope_dim + d.rope_dim, d.v_dim
+    cu_ = torch.tensor([0, T - 30, T], dtype=torch.int32, device=dev)
+    first, ends = x["x"].clone(), []
+    for apart in (True, False):
+        x["x"].copy_(first)
+        res = []
+        for turn in range(6):
+            run_prolog(p, x, outs)
+            if apart:
+                torch.cuda.synchronize()
+            out, lse = torch.zeros((T, H, E), dtype=torch.bfloat16, device=dev), torch.zeros((T, H), device=dev)
+            if apart:
+                torch.cuda.synchronize()
+            binding.attend_prompt(outs["out_q_int8"].t, outs["out_k"].t, outs["out_v"].t, cu_, cu_, out, lse, scale=D ** -0.5,
+                                  q_scale=outs["out_scale"].t)
+            if apart:
+                torch.cuda.synchronize()
+            res.append((out, lse))
+            if apart and turn == 0:
+                a = 0
+                for n in (T - 30, 30):
+                    f = lambda t: t[a:a + n].double().permute(1, 0, 2)  # noqa: E731
+                    s = outs["out_scale"].t.double().reshape(T, -1, 1)[a:a + n].permute(1, 0, 2)
+                    i, j = torch.arange(n, device=dev)[:, None], torch.arange(n, device=dev)[None, :]
+                    o, z, to, tz = row_attention(f(outs["out_q_int8"].t) * s, f(outs["out_k"].t), f(outs["out_v"].t), D ** -0.5, j > i)
+                    check(f(out), o, to, f"out from row {a}")
+                    check(lse[a:a + n].t(), z, tz, f"lse from row {a}")
+                    a += n
+            x["x"].copy_(x["x"].roll(1, 0))
+        torch.cuda.synchronize()
+        ends.append(res)
+    assert p.device_status() == 0
+    p.close()
+    for apart, together in zip(*ends):
+        assert same(apart, together)
