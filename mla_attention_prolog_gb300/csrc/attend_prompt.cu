@@ -410,8 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool mine = r < rows;
         float c = p.scale * kLog2e;
         if (p.q8 && n) {
-            // (a row without a key takes no scale, which may be anything: its answer is 0)
-            const float qs = mine && limit(row) > 0 ? p.q_scale[p.q_per_head ? at : jb.q0 + row] : 0.f;
+            const float qs = mine ? p.q_scale[p.q_per_head ? at : jb.q0 + row] : 0.f;
             c *= fabsf(qs);  // a negative scale turns the codes' sign, so that c > 0 keeps the order of the scores
             if (c < 1e-30f) c = 1e-30f;  // a zero row: its scores are 0 (hidden ones stay -inf)
             // The warp's 32 rows of codes in pieces of 16, a lane's pieces 32 apart: neighbouring lanes read
@@ -544,6 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_before();
             mbar_arrive(smem_u32(&sh->p_full[t]));
         }
+        if (lim == 0) l = 0.f;  // a row without a key, whatever its scale: NaN would have come through the hidden scores
         if (ok && n) {
             ok = mbar_wait(smem_u32(&sh->o_done[t]), (n - 1) & 1, kTimeoutNs, abort_flag);
             ok = __all_sync(~0u, ok);
