@@ -590,7 +590,8 @@ typedef struct mla_prolog_prompt_dims {
  *   cu_k     int32 [sequences + 1]: the same for k and v (may be cu_q itself)
  *   out      BF16 [Tq, num_heads, v_dim]
  *   lse      FP32 [Tq, num_heads]; may be NULL
- *   status   int32 (device); MLA_STATUS_* bits are ORed in; may be NULL
+ *   status   int32 (device); MLA_STATUS_* bits are ORed in; may be NULL (then a
+ *            wait that gave up is reported nowhere)
  * Rows of out and lse that belong to no sequence are left as they were.  A
  * sequence whose offsets break the rule above is cut to its part inside the
  * buffers (none if they decrease) and sets MLA_STATUS_SEQ_RANGE.  No
@@ -657,7 +658,8 @@ typedef struct mla_prolog_cache_dims {
  *   workspace   16-byte aligned, at least mla_prolog_attend_cache_workspace()
  *               bytes; its contents need not be kept between calls.  Calls that
  *               may overlap (two streams, two captured graphs) need one each.
- *   status      int32; MLA_STATUS_* bits are ORed in; may be NULL
+ *   status      int32; MLA_STATUS_* bits are ORed in; may be NULL (then a wait
+ *               that gave up is reported nowhere)
  * All device pointers; lengths and tables are read on the device, so a
  * captured call follows them.  A seqs entry or length outside its range is
  * cut to it (the entry: an empty sequence) and sets MLA_STATUS_SEQ_RANGE; a
@@ -671,7 +673,7 @@ int mla_prolog_attend_cache(const mla_prolog_cache_dims* dims, const void* q, co
 
 /* Bytes of workspace that mla_prolog_attend_cache() needs for these dims on
  * the current device (only batch, num_heads, kv_lora_rank and rope_dim
- * count).  Errors: INVALID_ARG, UNSUPPORTED_DIMS, CUDA. */
+ * count).  Errors: INVALID_ARG, UNSUPPORTED_DIMS, DEVICE, CUDA. */
 int mla_prolog_attend_cache_workspace(const mla_prolog_cache_dims* dims, size_t* bytes);
 
 /* ---- pages of the latent cache ------------------------------------------ */
@@ -693,7 +695,7 @@ int mla_prolog_attend_cache_workspace(const mla_prolog_cache_dims* dims, size_t*
  * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): sequences, num_pages >= 0;
  * page_size, max_pages >= 1; num_pages * page_size <= 2^31 - 1 and max_pages *
  * page_size <= 2^30; lists of 0 .. 1024 entries; total <= 2^30.
- * Errors of all: INVALID_ARG, UNSUPPORTED_DIMS, CUDA.
+ * Errors of all: INVALID_ARG, UNSUPPORTED_DIMS, DEVICE, CUDA.
  */
 typedef struct mla_prolog_pool {
     int32_t  sequences;   /* rows of page_table                                   */
@@ -765,7 +767,8 @@ int mla_prolog_pages_compact(const mla_prolog_pool* pool, int32_t* moved_to, int
  * be NULL).  No dst may be listed twice or be another entry's src (the order
  * of the copies is not specified).  page_bytes a positive multiple of 16;
  * cache and layer_stride (>= num_pages * page_bytes for two layers or more)
- * 16-byte aligned; 0 <= layers <= 65535; n <= 2^30.
+ * 16-byte aligned; 0 <= layers <= 65535; n <= 2^30.  Errors: INVALID_ARG,
+ * UNSUPPORTED_DIMS, DEVICE, CUDA.
  */
 int mla_prolog_copy_pages(void* cache, int32_t layers, int64_t layer_stride, int64_t num_pages, int64_t page_bytes,
                           const int32_t* src, const int32_t* dst, int32_t n, int32_t* status, void* stream);

@@ -29,10 +29,11 @@
 // 1.6 to 1.7k (0.78 us, in which 76 pairs read 5.6 MB: 7.2 TB/s, so that own
 // pages of few heads run at the rate of memory); a tile's start and end ~3.5
 // us, of which the copies of the next tile overlap all but the last products
-// and the results' way out; a call's start 6 us and its join 4 us.  V2-Lite (16
-// heads), 64 sequences of 1 to 4096: 48 us, 3.8 TB/s; V3 (128 heads), 32 of
-// 2000 to 32768: 147 us, 4.6 TB/s and 1100 TFLOP/s; 128 of 1 to 1024 behind a
-// prefix of 8192: 241 us, 1290 TFLOP/s; one sequence of 100: 12 us.
+// and the results' way out; a call's start 6 us and its join 3 to 13 us (see
+// there).  V2-Lite (16 heads), 64 sequences of 1 to 4096: 48 us, 3.8 TB/s; V3
+// (128 heads), 32 of 2000 to 32768: 147 us, 4.6 TB/s and 1100 TFLOP/s; 128 of 1
+// to 1024 behind a prefix of 8192: 231 us, 1340 TFLOP/s; one sequence of 100:
+// 12 us.
 #include <cstdint>
 
 #include "attend.cuh"
@@ -65,8 +66,9 @@ constexpr float kSlack = 8.f;             // log2 of the largest P
 // Own pages are asked of L2 this many steps before their copies: the ring holds two steps, which cover the
 // latency of L2 but not that of HBM.  (V2-Lite 64 sequences 48.1 us, two steps 48.7, three 51.)
 constexpr int kFetch = 1;
-// A tile's start and end, in key steps: so many, and one per so many rows.  (V2-Lite 64 sequences, V3 shared prefix: 48
-// and 240 us; 4 alone 49 and 289; 3 and one per 32 rows 51 and 255; 2 or 3 and one per 16 rows 51 and 239.)
+// A tile's start and end, in key steps: so many, and one per so many rows.  (One call after a flush of L2, 128 sequences
+// behind a shared 8192 of 64 heads and of 16 heads: 144 and 68 us; 4 alone 171 and 70; 3 and one per 32 rows 167 and 74;
+// 3 and one per 16 rows 151 and 71; 2 and one per 16 rows 155 and 74.  V2-Lite 64 sequences 58 to 61 with any.)
 constexpr int kOverhead = 4, kRowsPerStep = 16;
 // A shared prefix in tiles of its own makes a partial result of every row and leaves the rows that share it to the join:
 // as many key steps of each CTA pair (see prefix_pays()).
@@ -840,7 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial results of each row, in the order of the cut; a row with
 // one piece was finished by that piece.  One warp per row; bound by the latency
-// of its few dependent reads (cut, length, sums, rows): ~3 us.
+// of its few dependent reads (cut, length, sums, rows): 3.3 us where nothing is
+// to join, 5.7 for 64 sequences of 16 heads, 9.2 for 32 and 13 for 128 of 128.
 __global__ void __launch_bounds__(128) mla_attend_join_kernel(const __grid_constant__ CacheParams p) {
     const int lane = threadIdx.x & 31;
     const int64_t row = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);

@@ -50,8 +50,14 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
 
 // mbar_arrive_cluster() without the cluster-wide release, which holds the
 // thread up until its own stores have reached the other SM (~540 cycles against
-// ~215): for hand-overs to the tensor core, whose operands stay in this CTA and
-// are ordered by the proxy and tcgen05 fences before the arrival.
+// ~215; V3 long contexts 225 us instead of 145, 16 heads 79 instead of 59): for
+// hand-overs to the tensor core, whose operands stay in this CTA and are ordered
+// by the proxy and tcgen05 fences before the arrival.  The arrival releases to
+// its own CTA only, so in PTX's memory model it orders nothing between threads
+// of the two CTAs, and neither side reads what the other's threads wrote.  What
+// the kernel relies on beyond the model: the arrival is not seen before the
+// fences in front of it are done, and a copy that an mbarrier has counted lies
+// in shared memory, whichever CTA's barrier counted it.
 __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
