@@ -33,8 +33,8 @@
 // (qk_dim 192, v_dim 128); and 11k to 17k cycles of a CTA's start and end.  A
 // CTA that keeps 64 keys per step, P in halves, exponentials on the last
 // tile's maximum, a persistent CTA or a CTA pair per 256 rows each measured
-// slower.  128 heads x 16384 tokens, INT8 q: 6.83 ms, 1610 TFLOP/s (83 % of the
-// measured cuBLAS rate); four prompts of 700 to 4099: 927 us, 1028 TFLOP/s;
+// slower.  128 heads x 16384 tokens, INT8 q: 6.83 ms, 1610 TFLOP/s (84 % of the
+// measured cuBLAS rate); four prompts of 700 to 4099: 932 us, 1023 TFLOP/s;
 // 16 heads x 4096: 70.5 us, 1220; eight ragged prompts: 43.4 us, 647.
 #include <cstdint>
 
