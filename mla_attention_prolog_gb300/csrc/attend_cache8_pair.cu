@@ -321,6 +321,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // rows behind the end may hold anything: as values they have to be zero
                     ok = __all_sync(~0u, ok && wait(&sh->v_seen, tails));
                     if (!ok) continue;
+                    mbar_acquire_cluster(smem_u32(&sh->v_seen), tails & 1);
                     ++tails;
                     const int rows = (left + 31) / 32 * 32 - left;
                     for (int i = threadIdx.x; i < rows * half * 8; i += kSoft)
@@ -441,9 +442,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto values = [&](int u, bool first, int keys) {
                 const int e = u & 1;
                 if (!look(&sh->v_full[e], u >> 1)) return;
-                if (keys < kKeys) {  // both CTAs clear the rows behind the end first
+                if (keys < kKeys) {
+                    // Both CTAs clear the rows behind the end first: the copies into the odd one, which this one's barrier
+                    // has counted, come before its threads' stores.
+                    mbar_acquire_cluster(smem_u32(&sh->v_full[e]), u >> 1 & 1);
                     mbar_arrive(smem_u32(&sh->v_seen));
-                    mbar_arrive_peer(map_shared_rank(smem_u32(&sh->v_seen), 1));
+                    mbar_arrive_cluster(map_shared_rank(smem_u32(&sh->v_seen), 1));
                 }
                 if (!look(&sh->p_full, u)) return;
                 // (a piece's first values overwrite O, from which the results of the piece before have been read)

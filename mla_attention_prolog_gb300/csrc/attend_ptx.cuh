@@ -62,6 +62,18 @@ __device__ __forceinline__ void mbar_arrive_peer(uint32_t bar_cluster) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
+// Behind a wait for a phase of this CTA's barrier, which acquires at the scope of
+// the CTA: acquires the same phase at that of the cluster.  With it and
+// mbar_arrive_cluster() a copy into one CTA that a barrier of the other has
+// counted is ordered before what the first CTA's threads store over it.
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(parity)
+        : "memory");
+}
+
 // ------------------------------------------------ attention: TMEM and operands
 
 // 64 consecutive columns of this warp's 32 TMEM lanes as raw 32-bit words,
