@@ -18,7 +18,7 @@ def code(name, start=None, end=None):
     return " ".join(re.sub(r"//[^\n]*", "", src).split())
 
 
-@pytest.mark.parametrize("name", ["attend_cache8_pair.cu"])
+@pytest.mark.parametrize("name", ["attend_cache8_pair.cu", "attend_cache.cu"])
 def test_copies_come_before_the_other_ctas_clears(name):
     """Rows behind a sequence's end are cleared by each CTA of a pair over rows that
     a copy brought, which the even CTA's barrier counted: its arrival at the odd one
