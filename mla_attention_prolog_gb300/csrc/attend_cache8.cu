@@ -294,6 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int h = 0; h < kMine; h += 8) {
                         float a[8], b[8];
+                        __syncwarp();  // (tensor memory is read by converged warps)
                         tmem_ld8x2(s_at + h, s_at + kHeads + h, a, b);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
@@ -458,18 +459,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                 for (int d = 0; d < blocks; ++d) {
                     float o[8];
+                    __syncwarp();
                     get_o(d, h, o);
-                    if (d * 128 + tid >= p.Lkv) continue;
+                    const bool column = d * 128 + tid < p.Lkv;
                     if (x.place >= 0) {
                         float* at = to_part + d * 128;
 #pragma unroll
                         for (int i = 0; i < 8; ++i, at += p.Lkv)
-                            if (i < some) *at = o[i] * inv[i];
+                            if (column && i < some) *at = o[i] * inv[i];
                     } else {
                         uint16_t* at = to_out + d * 128;
 #pragma unroll
                         for (int i = 0; i < 8; ++i, at += p.Lkv)
-                            if (i < some) *at = static_cast<uint16_t>(pack_bf16x2(o[i] * inv[i], 0.f));
+                            if (column && i < some) *at = static_cast<uint16_t>(pack_bf16x2(o[i] * inv[i], 0.f));
                     }
                 }
             }

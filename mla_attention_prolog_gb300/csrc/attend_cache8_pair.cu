@@ -366,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int d = 0; d < half * 64; d += 32) {
                 if (col0 + d >= p.Lkv || row32 >= nh) break;
                 float o[32];
+                __syncwarp();  // (tensor memory is read by converged warps)
                 tmem_ld32(to_ + d, o);
                 // 32 columns: 64 bytes of finished rows, twice 64 of partial ones
 #pragma unroll

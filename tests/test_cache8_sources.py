@@ -36,3 +36,50 @@ def test_copies_come_before_the_other_ctas_clears(name):
     for a in waits:
         behind = src[a:]
         assert behind.index("mbar_acquire_cluster(smem_u32(&sh->v_seen), tails & 1)") < behind.index("st_shared_v4(")
+
+
+def statements(src):
+    """(depth of braces, statement) in the order of the source; a block's head is a statement of the depth around it."""
+    out, depth, inner, now = [], 0, 0, ""
+    for c in src:
+        inner += {"(": 1, ")": -1}.get(c, 0)
+        if c in "{}" or (c == ";" and inner == 0):
+            if now.strip():
+                out.append((depth, now.strip()))
+            now = ""
+            depth += {"{": 1, "}": -1}.get(c, 0)
+        else:
+            now += c
+    return out
+
+
+COLLECTIVE = re.compile(r"\b(tmem_ld\w*|tmem_st\w*|get_o)\(")
+CONVERGES = re.compile(r"__syncwarp\(|named_bar_(sync|or)\(|__\w+_sync\(|sum_across\(|arrive_even\(|" + COLLECTIVE.pattern)
+DIVIDES = re.compile(r"\b(if|for) \(.*\b(lane|tid|threadIdx|mine|rows|r|column)\b")
+LOOP = re.compile(r"\b(for|while) ?\(")
+
+
+@pytest.mark.parametrize("name,start,end,least", [
+    ("attend_cache8.cu", "- softmax\n", "- MMA\n", 7), ("attend_cache8_pair.cu", "- softmax\n", " MMA (the even CTA's", 5)])
+def test_warps_are_converged_at_every_access_to_tensor_memory(name, start, end, least):
+    """tcgen05.ld and .st take a whole converged warp: between one of them and what some lanes alone do (in front of it,
+    or at the end of the round of the loop before) lies something that the whole warp has to come to."""
+    code_ = statements(code(name, start, end))
+    found = 0
+    for i, (depth, s) in enumerate(code_):
+        if not COLLECTIVE.search(s) or s.startswith("auto get_o") or "float (&o)[8]) " in s:
+            continue
+        found += 1
+        # the innermost loop around it
+        head, d = i - 1, depth
+        while head >= 0 and not (code_[head][0] < d and LOOP.search(code_[head][1])):
+            d = min(d, code_[head][0])
+            head -= 1
+        last = i
+        while last + 1 < len(code_) and head >= 0 and code_[last + 1][0] > code_[head][0]:
+            last += 1
+        for s2 in [x for _, x in code_[head + 1:i][::-1]] + [x for _, x in code_[i + 1:last + 1][::-1]]:
+            if CONVERGES.search(s2):
+                break
+            assert not DIVIDES.search(s2), f"`{s}` behind `{s2}`"
+    assert found >= least
