@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(~0u, ok && wait(&sh->scale_full[step % kAhead], step / kAhead));
                 const int k = scale_exp(sh->scale[step % kAhead][tid]);
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh->scale_free[step % kAhead]));
+                if (ok && lane == 0) mbar_arrive(smem_u32(&sh->scale_free[step % kAhead]));
                 const uint64_t up = pk2(pow2(k), pow2(k)), kf = pk2(static_cast<float>(k), static_cast<float>(k));
                 const uint64_t back = pk2(pow2(-k), pow2(-k));
                 ok = __all_sync(~0u, ok && wait(&sh->s_full[step & 1], step >> 1));

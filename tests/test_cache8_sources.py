@@ -83,3 +83,28 @@ def test_warps_are_converged_at_every_access_to_tensor_memory(name, start, end, 
                 break
             assert not DIVIDES.search(s2), f"`{s}` behind `{s2}`"
     assert found >= least
+
+
+LEAVES = re.compile(r"^if \(!ok\) (continue|break)|^if \(failed\)|^if \(!?named_bar_or\(1, kSoft, .*!ok\)\)|^if \(ok( &&|\)) |"
+                    r"r < kHeads && ok|\) scratch->failed\[warp\] = !ok")
+EFFECT = re.compile(r"\b(tmem_st\w*|st_shared_v\d|mbar_arrive\w*|arrive_even|sum_across)\(|\bsh->(m|by)\[.*\] [-*]?= |\bscratch->sum\[")
+
+
+@pytest.mark.parametrize("name,start,end,least", [
+    ("attend_cache8.cu", "- softmax\n", "- MMA\n", 6), ("attend_cache8_pair.cu", "- softmax\n", " MMA (the even CTA's", 6)])
+def test_a_failed_wait_of_the_softmax_warps_stays_failed(name, start, end, least):
+    """A wait that gave up is not forgotten when a later one succeeds, and what depends on it (a bound moved, O scaled, P
+    overwritten, rows cleared, arrivals that hand them over) is not done: the warp leaves, or tells the others, before."""
+    code_ = [s for _, s in statements(code(name, start, end))]
+    waits = [i for i, s in enumerate(code_) if re.search(r"\bok = ", s) and "wait(" in s]
+    assert len(waits) >= least
+    for i in waits:
+        assert re.search(r"\bok && wait\(", code_[i]), f"`{code_[i]}` forgets an earlier wait"
+        leaves = next(j for j in range(i + 1, len(code_)) if LEAVES.search(code_[j]))
+        done = [s for s in code_[i + 1:leaves] if EFFECT.search(s)]
+        assert not done, f"after `{code_[i]}`: {done}"
+    # the shared word that tells them is looked at behind a barrier, before what it guards
+    told = next(i for i, s in enumerate(code_) if "scratch->failed[warp] = !ok" in s)
+    known = next(i for i, s in enumerate(code_) if s.startswith("if (failed) break"))
+    assert any("named_bar_sync(1, kSoft)" in s for s in code_[told:known])
+    assert not [s for s in code_[told:known] if re.search(r"\b(tmem_st\w*|mbar_arrive\w*|arrive_even)\(", s)]
