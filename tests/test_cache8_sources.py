@@ -87,7 +87,7 @@ def test_warps_are_converged_at_every_access_to_tensor_memory(name, start, end, 
 
 LEAVES = re.compile(r"^if \(!ok\) (continue|break)|^if \(failed\)|^if \(!?named_bar_or\(1, kSoft, .*!ok\)\)|^if \(ok( &&|\)) |"
                     r"r < kHeads && ok|\) scratch->failed\[warp\] = !ok")
-EFFECT = re.compile(r"\b(tmem_st\w*|st_shared_v\d|mbar_arrive\w*|arrive_even|sum_across)\(|\bsh->(m|by)\[.*\] [-*]?= |\bscratch->sum\[")
+EFFECT = re.compile(r"\b(tmem_st\w*|st_shared_v\d|mbar_arrive\w*|arrive_even)\(|\bsh->(m|by)\[.*\] [-*]?= |\bscratch->sum\[")
 
 
 @pytest.mark.parametrize("name,start,end,least", [
