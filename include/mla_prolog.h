@@ -870,11 +870,14 @@ int mla_prolog_cache8_read(const mla_prolog_cache8* cache, const int32_t* page_t
  * Precision: the codes are multiplied as they are; q enters as the sum of two
  * E4M3 values (exact where an element is at least 2^-10 of its row's largest,
  * else to 2^-18 of that), the weights, each times its token's scale, as the
- * sum of three E5M2 values (up to 32 heads: to 2^-9, or 2^-19 of the largest)
- * or of an E4M3 and an E5M2 value (to 2^-7, or 2^-15 of the largest); sums,
- * softmax statistics and partial results are FP32, and out is rounded once.  A
- * query row with an infinite or NaN element has out = NaN.  Partial results are joined in a
- * fixed order, so equal inputs give equal bits.
+ * sum of three E5M2 values (up to 32 heads: to 2^-9, or 2^-18 of the largest)
+ * or of an E4M3 and an E5M2 value (to 2^-7, or 2^-15 of the largest).  Where the
+ * second bound is the larger, weights are rounded up or down by turns along the
+ * keys, so that thousands that are alike add up to their share within 2^-7,
+ * however far they lie under the largest (down to 2^-18 of it; FP16 ends at
+ * 2^-26).  Sums, softmax statistics and partial results are FP32, and out is
+ * rounded once.  A query row with an infinite or NaN element has out = NaN.
+ * Partial results are joined in a fixed order, so equal inputs give equal bits.
  *
  * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): 0 <= batch <= 2^17, num_heads >= 1,
  * batch * num_heads <= 2^24; Lkv a positive multiple of 16 up to min(512,

@@ -14,10 +14,12 @@
 // in as sums of such values, with FP32 sums.  q: an E4M3 value and what its
 // rounding left in E4M3 (4 + 4 significant bits: exactly; elements below 2^-10 of
 // a row's largest to 2^-18 of that).  P, up to 32 heads: three E5M2 values, to
-// 2^-9 of itself or 2^-19 of the largest weight; of 64 heads an E4M3 and an E5M2
+// 2^-9 of itself or 2^-18 of the largest weight; of 64 heads an E4M3 and an E5M2
 // value, whose smaller steps below 1 keep weights that lie far under the largest
 // (a first token's, say): to 2^-7 of itself, as near on average as a rounding to
-// BF16, or to 2^-15 of the largest (2^-24 where that one stands alone).
+// BF16, or to 2^-15 of the largest (2^-24 where that one stands alone).  Weights
+// so small that the second bound holds are rounded up or down by turns along the
+// keys, so that many of them that are alike keep their sum (attend_cache8.cuh).
 //
 // A tile is kHeads heads of one sequence on 128 keys a step, keys along the
 // lanes, so that one copy of the cache rows in shared memory serves both
@@ -367,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
+                const uint32_t turns = (turn_of(x.key0 + j * kKeys + tid) ^ 0x80u) * 0x00010001u;
                 uint32_t term[kThree ? 3 : 2][kMine / 4];
 #pragma unroll
                 for (int h = 0; h < kMine; h += 4) {
@@ -375,13 +378,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                     l[h / 2 + 1] = fma2(pk2(c, d), back, l[h / 2 + 1]);
                     uint32_t x0, x1, y0, y1, z0, z1;
                     if constexpr (kThree) {
-                        split_weights3(a, b, x0, y0, z0);
-                        split_weights3(c, d, x1, y1, z1);
+                        split_weights3(a, b, turns, x0, y0, z0);
+                        split_weights3(c, d, turns, x1, y1, z1);
                         term[0][h / 4] = __byte_perm(x0, x1, 0x7531);
                         term[2][h / 4] = __byte_perm(z0, z1, 0x7531);
                     } else {
-                        split_weights(a, b, z0, x0, y0);
-                        split_weights(c, d, z1, x1, y1);
+                        split_weights(a, b, turns, z0, x0, y0);
+                        split_weights(c, d, turns, z1, x1, y1);
                         term[0][h / 4] = x0 | x1 << 16;
                     }
                     term[1][h / 4] = __byte_perm(y0, y1, 0x7531);

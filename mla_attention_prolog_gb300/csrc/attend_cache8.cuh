@@ -208,11 +208,26 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
     return r != 0;
 }
 
+// Weights far under the largest are rounded up or down by turns.  Where 8 bits leave a weight only a few steps, weights
+// that are alike would all be rounded the same way: 16384 keys at 2^-18 of one other had 5 to 11% less or more than their
+// share.  So the last term of a small weight is rounded up in as many keys as its remainder asks for: where the byte that
+// is cut off and a key's turn pass 255.  Turns are the leading bits of the keys' numbers times the golden ratio (modulo
+// 1), which lie evenly for any run of keys: the share is within 0.1% then.  The error of one such weight is a step where it
+// was half of one.  (It takes 1 to 2% on CTA pairs, long contexts 128.5 -> 130.7 us, 1% with 64 heads, nothing with fewer.)
+__device__ __forceinline__ uint32_t turn_of(int i) { return static_cast<uint32_t>(i) * 0x9E3779B1u >> 24; }  // 2^32 / 1.618...
+// What is added to FP16 bits (two values, `p` of weights) before their lower bytes are cut off: half a step, or of weights
+// below `small` (FP16, both halves) the turn.  `turn`: in both halves, less half a step (exclusive or 0x80).
+__device__ __forceinline__ uint32_t round_up(uint32_t p, uint32_t small, uint32_t turn) {
+    uint32_t is_small;
+    asm("set.lt.u32.f16x2 %0, %1, %2;" : "=r"(is_small) : "r"(p), "r"(small));
+    return (is_small & turn) ^ 0x00800080u;
+}
+
 // Two weights as the sum of an E4M3 and an E5M2 value each (bytes in the halves' order; `five` in the upper byte of each
 // half), in FP16, of which E5M2 is the upper byte.  From 256 on E5M2 takes the value and E4M3 what is left of it, below
-// the other way round: to 2^-7 of the weight up to 3584 and down to 2^-6, to 2^-13 below that.  NaN goes by E4M3.
+// the other way round: to 2^-7 of the weight up to 3584 and down to 2^-6, to 2^-13 below that, by turns.  NaN goes by E4M3.
 // `p`: the weights in FP16.
-__device__ __forceinline__ void split_weights(float a, float b, uint32_t& p, uint32_t& four, uint32_t& five) {
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t turn, uint32_t& p, uint32_t& four, uint32_t& five) {
     uint32_t is_large, large, rest, again, left;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(b), "f"(a));
     asm("set.ge.u32.f16x2 %0, %1, %2;" : "=r"(is_large) : "r"(p), "r"(0x5c005c00u));
@@ -223,17 +238,19 @@ __device__ __forceinline__ void split_weights(float a, float b, uint32_t& p, uin
     four = c;
     again = f16x2_of_e4m3x2(c);
     asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(left) : "r"(rest), "r"(again));
-    five = large | ((left + 0x00800080u) & 0xff00ff00u & ~is_large);
+    five = large | ((left + round_up(p, 0x24002400u, turn)) & 0xff00ff00u & ~is_large);  // 2^-6
 }
-// The same as the sum of three E5M2 values each, upper bytes of the halves: to 2^-9 of the weight (2^-11 for FP16), 2^-17.
-__device__ __forceinline__ void split_weights3(float a, float b, uint32_t& x, uint32_t& y, uint32_t& z) {
+// The same as the sum of three E5M2 values each, upper bytes of the halves: to 2^-9 of the weight (2^-11 for FP16) down to
+// 2^-8, to 2^-16 below that, by turns.
+__device__ __forceinline__ void split_weights3(float a, float b, uint32_t turn, uint32_t& x, uint32_t& y, uint32_t& z) {
     uint32_t p;
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(p) : "f"(b), "f"(a));
+    const uint32_t up = round_up(p, 0x1c001c00u, turn);  // 2^-8
     x = (p + 0x00800080u) & 0xff00ff00u;
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(p) : "r"(x));
     y = (p + 0x00800080u) & 0xff00ff00u;
     asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(p) : "r"(y));
-    z = p + 0x00800080u;
+    z = p + up;
 }
 
 // Sum of values below 2^45 over the warp.

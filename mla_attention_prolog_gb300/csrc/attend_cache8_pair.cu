@@ -78,6 +78,13 @@ __device__ __forceinline__ void mma_pair8(uint32_t d, uint64_t a, uint64_t b, ui
         : "memory");
 }
 
+// The turns of keys i and i + 1 of 32 that a thread has (attend_cache8.cuh), less half a step, before they are crossed with
+// the 32 keys': their numbers' bits backwards, in the upper five.
+__host__ __device__ constexpr uint32_t turn_at(int i) {
+    return static_cast<uint32_t>((i & 1) << 7 | (i & 2) << 5 | (i & 4) << 3 | (i & 8) << 1 | i >> 1 & 8 | 4) ^ 0x80u;
+}
+__host__ __device__ constexpr uint32_t turns_at(int i) { return turn_at(i) | turn_at(i + 1) << 16; }
+
 __global__ void __launch_bounds__(kThreads, 1)
     mla_attend_cache8_pair_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_rest,
                                   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -210,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 32; ++i) w[i] = key_at + i < left ? w[i] : -INFINITY;
                         }
+                        const uint32_t turns = turn_of((x.key0 + j * kKeys + key_at) >> 5) * 0x00010001u;
                         const uint64_t mm = pk2(-m, -m);
                         uint32_t big = 0;
                         sum = 0;
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const uint64_t e = pk2(ex2(a), ex2(b));
                                 sum = add2(sum, e);
                                 upk2(mul2(e, u[h]), a, b);
-                                split_weights(a, b, pp, c4[h], c5[h]);
+                                split_weights(a, b, turns ^ turns_at(i + 2 * h), pp, c4[h], c5[h]);
                                 asm("max.f16x2 %0, %0, %1;" : "+r"(big) : "r"(pp));
                             }
                             four[i / 4] = c4[0] | c4[1] << 16;

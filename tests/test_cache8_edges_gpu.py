@@ -108,3 +108,70 @@ def test_rising_scores(H):
     cache.exps[table[0].long()[t // 64], t % 64] = (100 + t // 40).to(torch.uint8)
     out, lse = base.run_attend(cache, table, [1500], q, 128, 1.0)
     base.check_attend(cache, table, [1500], q, 128, 1.0, out, lse)
+
+
+# ------------------------------------------------- many small weights, alike
+#
+# n keys of weight P each behind others that outweigh them: what they add up to counts.  With P as the kernel holds it (its
+# largest at 2^2 to 2^11.75), the sum is off by
+#
+#   FP16     2^-11 of itself, or 2^-25 / P where that is more: 2^-9 for P >= 2^-16
+#   terms    where rounded to nearest: E4M3 to 2^-4 and the rest by E5M2 to 2^-3, 2^-7 of itself; three E5M2 values 2^-9
+#            where rounded up or down by turns along the keys: the share of keys that round up is right to 2^-7 over 2^12
+#            keys (test_cache8_rounding), of a step of 2^-2 P, or of 2^-16 <= P: 2^-7
+#   scores   2^-22 (|s| + 16) in log2 twice, |s| <= 32: 2^-16
+#   out      2^-8
+ALIKE = 2.0 ** -9 + 2.0 ** -7 + 2.0 ** -16 + 2.0 ** -8
+
+
+def alike_case(H, n, ahead, seed):
+    """n keys of score 0 and a value of 1 in 64 columns, of which `ahead` ({position: score}) stand out, with a value of 0;
+    152 rows whose heads scale the scores by 1 to 1.25, all on one sequence.  The shares of the keys alike, 64 bits."""
+    B, size = 152, 64
+    cache, table, _ = base.attend_case(seed, [n], H, 128, 64, size, 16)
+    q = torch.zeros((B, H, 192), dtype=torch.float64)
+    step = torch.arange(B * H, dtype=torch.float64).view(B, H)
+    q[..., 0] = 1 + (step * 37 % 32) / 128          # (BF16, and E4M3 twice, hold them)
+    cache.exps.fill_(127)
+    cache.codes[..., 0] = 0
+    cache.codes[..., 64:128] = code(1.0)
+    pos = torch.tensor(sorted(ahead))
+    page = table[0].long()[pos // size]
+    score = ref.VALUES[ref.nearest(torch.tensor([ahead[i] for i in sorted(ahead)], dtype=torch.float64)).long()]
+    cache.codes[page, pos % size, 0] = ref.nearest(score)
+    cache.codes[page, pos % size, 64:128] = 0
+    alike = float(n - len(ahead))
+    share = alike / (alike + torch.exp2(q[..., :1] * score).sum(-1))
+    return cache, table, q.to(torch.bfloat16), share.to(DEV)
+
+
+def check_alike(H, n, ahead, seed):
+    cache, table, q, share = alike_case(H, n, ahead, seed)
+    out, lse = base.run_attend(cache, table, [n], q, 128, math.log(2), seqs=[0] * q.shape[0])
+    off = ((out[..., 64:].double() - share[..., None]).abs() / share[..., None]).amax(-1)
+    assert off.max() <= ALIKE, f"off by {off.max().item():.4f} of the share, on average {off.mean().item():.4f}"
+    want = math.log(n - len(ahead)) - torch.log(share)
+    assert (lse.double() - want).abs().max() <= 2.0 ** -16 + (n + 16) * 2.0 ** -23 + 2.0 ** -23 * 32
+
+
+@pytest.mark.parametrize("H", [16, 32, 40, 64, 100, 128, 130])
+@pytest.mark.parametrize("at", [0, 200, 6000, 16383])
+def test_many_keys_alike_behind_one(H, at):
+    """One key of 2^16 to 2^20 times the weight of 16383 others, in the first step, in the next, in the middle, at the end."""
+    check_alike(H, 16384, {at: 16.0}, 86)
+
+
+@pytest.mark.parametrize("H", [16, 40, 128])
+@pytest.mark.parametrize("gap", [9.0, 12.0, 18.0])
+def test_many_keys_alike_behind_few(H, gap):
+    """Nine keys that outweigh the rest, in several steps."""
+    check_alike(H, 16000, {i: gap for i in (3, 77, 130, 131, 132, 1000, 5000, 5001, 15999)}, 87)
+
+
+@pytest.mark.parametrize("H", [16, 40, 128])
+@pytest.mark.parametrize("n", [4300, 60000])
+def test_many_keys_alike_behind_uneven_first_ones(H, n):
+    """A first step whose scores differ widely, so that the bound leaves room above its largest, and the rest 2^-13 of that
+    or less."""
+    first = {i: 5.0 + 8.0 * math.sin(1.7 * i) for i in range(128)}
+    check_alike(H, n, first, 88)
