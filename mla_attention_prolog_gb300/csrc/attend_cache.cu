@@ -659,13 +659,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (t > 1) {
                         const int pv = st - 2, f = pv & 1;
                         if (!look(&sh->v_full[f], pv >> 1)) break;
-                        if (t == n + 1 && x.end - x.key0 < n * kKeys) {
-                            // Both CTAs clear the rows behind the end first: the copies into the odd one, which this
-                            // one's barrier has counted, come before its threads' stores.
-                            mbar_acquire_cluster(smem_u32(&sh->v_full[f]), pv >> 1 & 1);
-                            mbar_arrive(smem_u32(&sh->v_seen));
-                            mbar_arrive_cluster(map_shared_rank(smem_u32(&sh->v_seen), 1));
-                        }
+                        if (t == n + 1 && x.end - x.key0 < n * kKeys)  // both CTAs clear the rows behind the end first
+                            copies_seen(smem_u32(&sh->v_full[f]), pv >> 1 & 1, smem_u32(&sh->v_seen));
                         if (!look(&sh->p_full[f], pv >> 1)) break;
                         const uint64_t b = dvals + f * (kMaxValues * kVBytes >> 4);
 #pragma unroll

@@ -451,13 +451,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto values = [&](int u, bool first, int keys) {
                 const int e = u & 1;
                 if (!look(&sh->v_full[e], u >> 1)) return;
-                if (keys < kKeys) {
-                    // Both CTAs clear the rows behind the end first: the copies into the odd one, which this one's barrier
-                    // has counted, come before its threads' stores.
-                    mbar_acquire_cluster(smem_u32(&sh->v_full[e]), u >> 1 & 1);
-                    mbar_arrive(smem_u32(&sh->v_seen));
-                    mbar_arrive_cluster(map_shared_rank(smem_u32(&sh->v_seen), 1));
-                }
+                if (keys < kKeys)  // both CTAs clear the rows behind the end first
+                    copies_seen(smem_u32(&sh->v_full[e]), u >> 1 & 1, smem_u32(&sh->v_seen));
                 if (!look(&sh->p_full, u)) return;
                 // (a piece's first values overwrite O, from which the results of the piece before have been read)
                 if (first && opened++ > 0 && !look(&sh->o_free, opened - 2)) return;

@@ -23,14 +23,16 @@ def test_copies_come_before_the_other_ctas_clears(name):
     """Rows behind a sequence's end are cleared by each CTA of a pair over rows that
     a copy brought, which the even CTA's barrier counted: its arrival at the odd one
     releases, and both looks acquire, at the scope of the cluster."""
+    seen = code("attend_ptx.cuh")
+    a = seen.index("void copies_seen(uint32_t full, uint32_t parity, uint32_t seen) {")
+    assert [x for _, x in statements(seen[seen.index("{", a):seen.index("}", a)])] == [
+        "mbar_acquire_cluster(full, parity)", "mbar_arrive(seen)", "mbar_arrive_cluster(map_shared_rank(seen, 1))"]
     src = code(name)
-    at = [m.start() for m in re.finditer(r"map_shared_rank\(smem_u32\(&sh->v_seen\), 1\)", src)]
+    at = [m.start() for m in re.finditer(r"smem_u32\(&sh->v_seen\)\);", src) if not src[:m.start()].endswith("acquire_cluster(")]
     assert at
     for a in at:
-        assert src[:a].endswith("mbar_arrive_cluster(")
-        before = src[:a]
-        seen = before.rindex("mbar_acquire_cluster(smem_u32(&sh->v_full[")
-        assert seen > before.rindex("look(&sh->v_full[")
+        told = src.rindex("copies_seen(smem_u32(&sh->v_full[", 0, a)
+        assert ";" not in src[told:a] and told > src.rindex("look(&sh->v_full[", 0, a)
     waits = [m.end() for m in re.finditer(r"wait\(&sh->v_seen, tails\)", src)]
     assert waits
     for a in waits:
