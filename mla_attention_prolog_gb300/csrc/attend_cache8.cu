@@ -499,7 +499,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // S of step `step`, chunk by chunk as they arrive
             auto scores = [&]() {
                 const uint32_t d = tmem + kColS + (step & 1) * kStageS;
-                const int done = slot;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
                     if (c >= chunks) break;
@@ -521,8 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 mma_commit(smem_u32(&sh->s_full[step & 1]));
                 if (kThree && rest) mma_commit(smem_u32(&sh->rest_free[step % kRests]));
-                for (int c = blocks; c < chunks; ++c)  // chunks without values have been read
-                    mma_commit(smem_u32(&sh->kv_free[(done + c) % kSlots]));
             };
             // O^T of step u
             auto values = [&](int u, bool first, int keys32) {
@@ -540,8 +537,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             mma_e4m3(tmem + kColO + m * kWidth, a + k * (32 * 128 >> 4), b + k * kNext, kThree ? id_5 : id_4, !first || k > 0);
                             if (!kThree) mma_e4m3(tmem + kColO + m * kWidth, a + k * (32 * 128 >> 4), dp + k * kNext, id_5, 1);
                         }
-                        mma_commit(smem_u32(&sh->kv_free[slot_v]));
                     }
+                    // (Chunks without values too, though their scores are all that reads them: places become free in the
+                    // order of the chunks.  The copying warps, which do not come to every turn of a place, tell its
+                    // phases apart by that.)
+                    mma_commit(smem_u32(&sh->kv_free[slot_v]));
                     if (++slot_v == kSlots) slot_v = 0;
                 }
                 if (!kThree && rest) mma_commit(smem_u32(&sh->rest_free[u % kRests]));

@@ -175,3 +175,29 @@ def test_many_keys_alike_behind_uneven_first_ones(H, n):
     or less."""
     first = {i: 5.0 + 8.0 * math.sin(1.7 * i) for i in range(128)}
     check_alike(H, n, first, 88)
+
+
+# ------------------------------------------------------------ other widths
+
+WIDTHS = [(16, 560), (96, 464), (144, 432), (256, 320), (272, 304), (384, 192), (400, 112), (512, 16), (512, 48),   # > 512 columns
+          (16, 496), (256, 256), (496, 16), (16, 400), (192, 256),                                                  # 4 chunks
+          (16, 368), (128, 256), (256, 128), (320, 0), (16, 240), (144, 112), (16, 112), (48, 0)]                   # fewer
+
+
+@pytest.mark.parametrize("H", [11, 24, 50, 100])
+@pytest.mark.parametrize("Lkv,R", WIDTHS)
+def test_values_of_some_of_the_columns(H, Lkv, R):
+    """Keys of one to five chunks of 128 columns, values in one to four of them, over many steps: one sequence that several
+    units share, and a batch that each unit has many steps and several tiles of."""
+    cache, table, q = base.attend_case(89, [9000, 700, 1300, 5], H, Lkv, R, 64, 16)
+    seqs = [1, 2, 0, 3] + [1, 2] * 150
+    g = base.gen(90)
+    q = torch.randn((len(seqs), H, Lkv + R), generator=g).to(torch.bfloat16)
+    lens = [9000, 700, 1300, 5]
+    for some in ([2], list(range(len(seqs)))):
+        status = base.i32([0])
+        of = [seqs[b] for b in some]
+        out, lse = base.run_attend(cache, table, lens, q[some], Lkv, 0.08, seqs=of, status=status)
+        assert status.item() == 0
+        few = list(range(min(len(some), 6))) + list(range(max(6, len(some) - 4), len(some)))
+        base.check_attend(cache, table, lens, q[some][few], Lkv, 0.08, out[few], lse[few], [of[b] for b in few])

@@ -110,3 +110,54 @@ def test_a_failed_wait_of_the_softmax_warps_stays_failed(name, start, end, least
     known = next(i for i, s in enumerate(code_) if s.startswith("if (failed) break"))
     assert any("named_bar_sync(1, kSoft)" in s for s in code_[told:known])
     assert not [s for s in code_[told:known] if re.search(r"\b(tmem_st\w*|mbar_arrive\w*|arrive_even)\(", s)]
+
+
+def ring(slots, chunks, blocks, early, steps=60):
+    """The ring of attend_cache8.cu: two warps copy chunks of key steps into its places, a step's first two and the others, and
+    wait for a place by the parity of its phase.  The tensor core scores up to two steps ahead of the values; a place is free
+    once its chunk's values, or of a chunk without values its scores (`early`), are multiplied.  Scores come as early as they
+    may, values as late, and the warps run as far as their waits let them: the chunks copied into a place still in use."""
+    phase = [0] * slots
+    lots = [[g for s in range(steps) for g in range(s * chunks + a, s * chunks + min(b, chunks))] for a, b in ((0, 2), (2, 4))]
+    at, wrong, copied = [0, 0], [], set()
+
+    def run():
+        for w in (0, 1):
+            while at[w] < len(lots[w]):
+                g = lots[w][at[w]]
+                turn, place = g // slots, g % slots
+                if turn > 0 and phase[place] % 2 == (turn - 1) % 2:
+                    break
+                if phase[place] < turn:
+                    wrong.append(g)
+                copied.add(g)
+                at[w] += 1
+
+    def free(s, some):
+        for c in some:
+            phase[(s * chunks + c) % slots] += 1
+        run()
+
+    run()
+    values = 0
+    for s in range(steps):
+        if s - values > 1:
+            free(values, range(blocks if early else chunks))
+            values += 1
+        if not all(s * chunks + c in copied for c in range(chunks)):
+            return wrong, s
+        if early:
+            free(s, range(blocks, chunks))
+    return wrong, steps
+
+
+@pytest.mark.parametrize("heads,place", [(64, 0), (32, 1), (16, 2)])
+def test_a_place_of_the_ring_is_free_before_it_is_copied_to(heads, place):
+    src = code("attend_cache8.cu")
+    slots = [int(x) for x in re.search(r"int slots_of\(int heads\) \{ return heads == 64 \? (\d+) : heads == 32 \? (\d+) : (\d+); \}", src).groups()]
+    scores = src[src.index("auto scores = "):src.index("auto values = ")]
+    early = "kv_free" in scores
+    for chunks in (1, 2, 3, 4):
+        for blocks in range(1, chunks + 1):
+            wrong, steps = ring(slots[place], chunks, blocks, early)
+            assert not wrong and steps == 60, (heads, chunks, blocks, wrong[:5], steps)
