@@ -876,7 +876,8 @@ int mla_prolog_cache8_read(const mla_prolog_cache8* cache, const int32_t* page_t
  * keys, so that thousands that are alike add up to their share within 2^-7,
  * however far they lie under the largest (down to 2^-18 of it; FP16 ends at
  * 2^-26).  Sums, softmax statistics and partial results are FP32, and out is
- * rounded once.  A query row with an infinite or NaN element has out = NaN.
+ * rounded once: scores of magnitude m, in log2, are apart by 2^-24 m or taken for
+ * equal.  A query row with an infinite or NaN element has out = NaN.
  * Partial results are joined in a fixed order, so equal inputs give equal bits.
  *
  * Size rules (else MLA_ERR_UNSUPPORTED_DIMS): 0 <= batch <= 2^17, num_heads >= 1,

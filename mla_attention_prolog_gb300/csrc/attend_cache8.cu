@@ -326,9 +326,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // (not by a head that has NaN alone)
                         const float place = last ? kTopAlone : set ? fminf(first_top(top, all, squares), kTopLater) : first_top(top, all, squares);
                         const bool moves = set ? top > place : top > -INFINITY;  // (up, after the first)
-                        top -= place;
-                        sh->by[h] = moves ? ex2(-top) : 1.f;
-                        if (moves) sh->m[h] -= top;
+                        // (By what it moves: of a bound beyond 2^17 FP32 does not hold each fraction of a binade, and beyond
+                        // 2^27 that may be too little by five.)
+                        const float was = sh->m[h];
+                        float now = was - (top - place);
+                        if (top + (now - was) > kMost) now = was - top;
+                        sh->by[h] = moves ? ex2(now - was) : 1.f;
+                        if (moves) sh->m[h] = now;
                     }
                     // (A failed wait stays failed: all the warps learn of it here and leave together.)
                     const uint4 fail0 = *reinterpret_cast<const uint4*>(scratch->failed), fail1 = *reinterpret_cast<const uint4*>(scratch->failed + 4);

@@ -39,6 +39,7 @@ static_assert(kSmem <= 232448, "227 KB");
 static_assert(2 * kQTerm == kPairQBytes, "");
 constexpr uint32_t kColO = 0, kColS = 256, kStages = 4;  // TMEM: O, S of so many steps (64 columns each)
 constexpr int kScales = 3;                            // steps whose scales are found ahead
+constexpr float kFar = 65536.f;                       // a bound whose last bit is 2^-7 of a binade
 
 struct Shared {
     // (of the even CTA for both: k_full, v_full, p_full, q_full, o_free)
@@ -84,6 +85,34 @@ __host__ __device__ constexpr uint32_t turn_at(int i) {
     return static_cast<uint32_t>((i & 1) << 7 | (i & 2) << 5 | (i & 4) << 3 | (i & 8) << 1 | i >> 1 & 8 | 4) ^ 0x80u;
 }
 __host__ __device__ constexpr uint32_t turns_at(int i) { return turn_at(i) | turn_at(i + 1) << 16; }
+
+// The score of a row's largest weight and log2 of its key's scale, the same in all four threads of the row: `up` the scales of
+// this one's 32 keys, `left` its step's keys.  (A call: the hot loop is not to be longer by it.)
+static __device__ __noinline__ float2 far_bound(uint32_t s_at, const float* up, int key_at, int left, Scratch* scratch, int r, int mine,
+                                                float f, float from) {
+    float top = -INFINITY, score = 0.f, scale = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < 32; c += 8) {
+        float w[8];
+        __syncwarp();
+        tmem_ld8(s_at + c, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float y = w[i] * up[c + i], k = static_cast<float>((__float_as_int(up[c + i]) >> 23) - 127), t = fmaf(y - from, f, k);
+            if (key_at + c + i < left && t > top) top = t, score = y, scale = k;  // (NaN is left out)
+        }
+    }
+    scratch->top[mine][r] = top;
+    scratch->all[mine][r] = score;
+    scratch->squares[mine][r] = scale;
+    named_bar_sync(1, kSoft);
+    top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (scratch->top[i][r] > top) top = scratch->top[i][r], score = scratch->all[i][r], scale = scratch->squares[i][r];
+    named_bar_sync(1, kSoft);
+    return make_float2(score, scale);
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     mla_attend_cache8_pair_kernel(const __grid_constant__ CUtensorMap tm_rows, const __grid_constant__ CUtensorMap tm_rest,
@@ -193,7 +222,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (named_bar_or(1, kSoft, !more)) break;
             const float* const f_at = sh->f[turn] + r;
             turn = turn == 2 ? 0 : turn + 1;
-            float m = 0.f, l = 0.f;  // the row's bound; sum of its weights over this thread's keys
+            // The row's bound: its factor times `from`, and m (weights are 2^(factor (score - from) - m)); sum of its weights
+            // over this thread's keys.
+            float from = 0.f, m = 0.f, l = 0.f;
             uint64_t ff = 0;
             for (int j = 0; j < x.n; ++j, ++step) {
                 const int left = x.len - x.key0 - j * kKeys;  // keys from this step on
@@ -218,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int i = 0; i < 32; ++i) w[i] = key_at + i < left ? w[i] : -INFINITY;
                         }
                         const uint32_t turns = turn_of((x.key0 + j * kKeys + key_at) >> 5) * 0x00010001u;
-                        const uint64_t mm = pk2(-m, -m);
+                        const uint64_t mm = pk2(-m, -m), ss = pk2(-from, -from);
                         uint32_t big = 0;
                         sum = 0;
 #pragma unroll
@@ -230,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int h = 0; h < 2; ++h) {
                                 float a, b;
                                 uint32_t pp;
-                                upk2(fma2(mul2(pk2(w[i + 2 * h], w[i + 2 * h + 1]), u[h]), ff, mm), a, b);
+                                upk2(fma2(fma2(pk2(w[i + 2 * h], w[i + 2 * h + 1]), u[h], ss), ff, mm), a, b);
                                 const uint64_t e = pk2(ex2(a), ex2(b));
                                 sum = add2(sum, e);
                                 upk2(mul2(e, u[h]), a, b);
@@ -260,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // the exponents of the scales, as FP32 by way of 2^23 + their bits
                             const uint64_t k = add2(pk2(__uint_as_float(__float_as_uint(a) >> 23 | 0x4b000000u), __uint_as_float(__float_as_uint(b) >> 23 | 0x4b000000u)),
                                                     pk2(-8388735.f, -8388735.f));
-                            const uint64_t t = add2(fma2(mul2(pk2(w[i], w[i + 1]), u), ff, k), pk2(-m, -m));
+                            const uint64_t t = add2(fma2(fma2(pk2(w[i], w[i + 1]), u, pk2(-from, -from)), ff, k), pk2(-m, -m));
                             all = add2(all, t);
                             squares = fma2(t, t, squares);
                             upk2(t, a, b);
@@ -286,12 +317,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // (A failed wait stays failed: all the warps learn of it here and leave together.)
                     const uint4 fail0 = *reinterpret_cast<const uint4*>(scratch->failed), fail1 = *reinterpret_cast<const uint4*>(scratch->failed + 4);
                     failed = (fail0.x | fail0.y | fail0.z | fail0.w | fail1.x | fail1.y | fail1.z | fail1.w) != 0;
-                    named_bar_sync(1, kSoft);
-                    if (failed) break;
                     const float place = last ? kTopAlone : set ? fminf(first_top(top, all, squares), kTopLater) : first_top(top, all, squares);
                     const bool moves = set ? top > place : top > -INFINITY;   // (up, after the first; not a row that has NaN alone)
                     const float by_log = moves ? top - place : 0.f;
                     m += by_log;
+                    // Bounds that FP32 holds to a fraction of a binade only, or not at all: the score of the largest weight
+                    // becomes part of them, whose differences to others it does hold.
+                    const bool far = named_bar_or(1, kSoft, fabsf(m) > kFar);
+                    if (failed) break;
+                    if (far) {
+                        float f, f2;
+                        upk2(ff, f, f2);
+                        const float2 bound = far_bound(s_at, up, key_at, left, scratch, r, mine, f, from);
+                        if (moves) from = bound.x, m = bound.y - place;
+                    }
                     if (set && __any_sync(~0u, moves)) {
                         const float by = ex2(-by_log);
                         l *= by;
@@ -356,7 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int64_t part_row = ((static_cast<int64_t>(unit) * 2 + x.place) * 2 + rank) * kRows;
             const int64_t out_row = static_cast<int64_t>(x.b) * p.H + head0;
             if (mine == 0 && r < nh) {
-                const float lg = log2f(l) + m;
+                float f, f2;
+                upk2(ff, f, f2);  // (its place may have the factors of a later piece by now)
+                const float lg = log2f(l) + fmaf(from, f, m);
                 if (x.place >= 0) p.part_lse[part_row + r] = lg;
                 else if (p.lse) p.lse[out_row + r] = lg * kLn2;
             }

@@ -201,3 +201,39 @@ def test_values_of_some_of_the_columns(H, Lkv, R):
         assert status.item() == 0
         few = list(range(min(len(some), 6))) + list(range(max(6, len(some) - 4), len(some)))
         base.check_attend(cache, table, lens, q[some][few], Lkv, 0.08, out[few], lse[few], [of[b] for b in few])
+
+
+@pytest.mark.parametrize("H", HEADS)
+@pytest.mark.parametrize("power", [6, 12, 18, 24, 30, 40])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_scores_so_large_that_one_value_takes_all(H, power, sign):
+    """Scores of up to 25 * 2^power, each exact in FP32, equal or at least 2^(power - 3) apart: the weight goes to the keys of
+    the largest, wherever the bound of the weights has to move.  Up to 2^12 they share it alike (2^6: e^-8 of it goes to the
+    next).  Beyond that FP32 log-sum-exps of up to 36 * 2^18 in log2, by which the pieces of a sequence are joined, are right
+    to half a binade or worse, and the shares of equals are not: but the result lies between their values."""
+    lens = [1000, 130, 64, 1, 5000]
+    cache, table, q = base.attend_case(91, lens, H, 128, 64, 64, 16, 1.0, 121, 122)
+    cache.codes[..., 0] = ref.nearest(torch.randint(4, 200, cache.codes.shape[:2], generator=base.gen(92)).double() / 8)
+    q[:] = 0
+    q[..., 0] = sign
+    scale = 2.0 ** (power + 6)          # (the rows' scale is 2^-6)
+    out, lse = base.run_attend(cache, table, lens, q, 128, scale)
+    for b, n in enumerate(lens):
+        t = torch.arange(n)
+        rows = cache.rows(table[b].long()[t // 64] * 64 + t % 64)
+        s, values = rows[:, 0] * sign * scale, rows[:, :128]
+        z = torch.logsumexp(s, 0)
+        p = torch.exp(s - z)
+        # weights to 2^-7, theirs and the others' (of 2^-11 and less); 36 * 2^12 in log2 to 2^-24, twice: 2^-5.8
+        room = 2.0 ** -8 + 2.0 ** -6 + 2.0 ** -11
+        if power <= 12:
+            want = p @ values
+            tol = (room + (2.0 ** -5.8 if power == 12 else 0)) * (p @ values.abs()) + 1e-30
+            low, high = want - tol, want + tol
+        else:
+            best = values[s == s.max()]
+            tol = room * best.abs().amax(0) + 1e-30
+            low, high = best.amin(0) - tol, best.amax(0) + tol
+        got = out[b].double().cpu()
+        assert ((got >= low) & (got <= high)).all(), (b, got.isnan().sum().item())
+        assert (lse[b].double() - z.item()).abs().max() <= 2.0 ** -21 * abs(z.item()) + 2.0 ** -8 + (math.log(n) if power > 12 else 0)
