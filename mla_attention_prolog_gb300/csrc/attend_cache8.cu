@@ -38,13 +38,13 @@
 // and another kernel joins them in the order of the cut.  Where it takes no
 // longer, whole tiles are dealt to the units instead.
 //
-// What bounds it.  Many keys of 16 and 32 heads: the reading of the cache, 6.2
-// TB/s (91% of a copy's rate; 152 sequences of 8192, C = 576: 130 and 135 us), of
-// 64 heads shared memory and the ring, that holds two steps (5.0 TB/s; 166 us).
-// A step from L2 takes 1.4, 1.7 and 2.2 us for 16, 32 and 64 heads; the products
-// alone would take 0.7, 0.9 and 1.3.  Few keys: the launches and a cold start
-// (each instruction comes from L2 the first time): 9.6 us for 100 keys of one
-// sequence.  V2-Lite, 64 sequences of 1 to 4096: 29 us, of which the join takes 5.
+// What bounds it.  Many keys of 16 and 32 heads: the reading of the cache, 5.6 and
+// 5.5 TB/s (83 and 81% of a copy's rate; 152 sequences of 8192, C = 576: 129 and
+// 132 us), of 64 heads shared memory and the ring, that holds two steps (4.4 TB/s;
+// 167 us).  A step from L2 takes 1.4, 1.7 and 2.2 us for 16, 32 and 64 heads; the
+// products alone would take 0.7, 0.9 and 1.3.  Few keys: the launches and a cold
+// start (each instruction comes from L2 the first time): 9.5 us for 100 keys of one
+// sequence.  V2-Lite, 64 sequences of 1 to 4096: 30 us, of which the join takes 5.
 #include <cstdint>
 
 #include "attend_cache8.cuh"
@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (threadIdx.x < 64) sh->m[threadIdx.x] = 0.f;
     tc_fence_before();
+    // (The next kernel may come before this CTA has its TMEM: none that takes some fits beside its shared memory.)
     pdl_launch_dependents();
     __syncthreads();
     tc_fence_after();

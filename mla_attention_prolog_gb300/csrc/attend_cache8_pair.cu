@@ -8,18 +8,18 @@
 //   S [heads][keys] = (Qh + Ql) K^T          N = 128, C deep, twice
 //   O [heads][value columns] += (P4 + P5) V   N = 256, 128 keys deep, twice
 //
-// In each CTA that takes 331 KB a step through shared memory (2.6k cycles at 128
-// bytes a cycle), where the arrangement with keys along the lanes takes 433 KB
-// for the same heads and keys, and a key's place is free once its scores are
-// made.  The tensor core spreads the columns of a CTA's 64 rows over both halves
-// of the lanes: a row belongs to four threads, one for each 32 keys of a step
-// and a quarter of the value columns.
+// In each CTA the products' operands are 331 KB of shared memory a step, where
+// with keys along the lanes they would be 433 KB for the same heads and keys, and
+// a key's place is free once its scores are made.  The tensor core spreads the
+// columns of a CTA's 64 rows over both halves of the lanes: a row belongs to four
+// threads, one for each 32 keys of a step and a quarter of the value columns.
 //
-// What bounds it: the products, 2.2k cycles a step (shared memory); a step takes
-// 2.5k (1.25 us) on a few pairs, 1.35 us on all of them from L2 and 1.48 from
-// memory.  V3, 32 sequences of 2000 to 32768 keys: 129 us, of which the partial
-// results and their join take 12; 128 of up to 1024, dealt whole: 39; one of
-// 131072, 14 steps a pair: 39.
+// What bounds it: the products.  Two terms of 64 heads on 128 keys of 576 and 512
+// columns are 17.8 M multiply-adds a step and CTA, 2176 cycles at the tensor
+// core's 8192 a cycle (2213 measured alone); a step takes 2.5k (1.25 us) on a few
+// pairs, 1.35 us on all of them from L2 and 1.48 from memory.  V3, 32 sequences of
+// 2000 to 32768 keys: 132 to 134 us, of which the partial results and their join
+// take 12; 128 of up to 1024, dealt whole: 41; one of 131072, 14 steps a pair: 41.
 #include <cstdint>
 
 #include "attend_cache8.cuh"
@@ -468,6 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!look(&sh->k_full[e], step >> 1)) return;
                 const uint32_t d = tmem + kColS + step % kStages * 64;
                 const uint64_t b = dk + e * (kKeyBytes >> 4), b_rest = dk_rest + e * (kKeyBytes >> 4);
+                // (the most columns there are, and the usual ones, without a loop: long contexts 134 us, by the loop 145)
                 if (C == 576) {
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {

@@ -84,10 +84,11 @@ __device__ __forceinline__ int linked_behind(const uint32_t* bits, int i, int mo
 }
 
 // A CTA writes a window of tokens, a warp kRows of them, which stay in registers between the maximum and the rounding:
-// each row is read once.  (Rows of a run that another window holds are read for their maximum alone; a window is chosen at
-// least as long as a block where there are tokens enough, so that this happens at its two ends only.)  It moves 3 bytes
-// per element: 262144 rows of 576 in 77 us, 5.9 TB/s (87% of a copy's rate); 16384 in 6.8; few tokens by the launch and
-// three dependent reads (slot, scale, row): 2.0 us for one.
+// each row is read once.  (Rows of a run that another window holds are read for their maximum alone, one after another.
+// Windows are 8 to 64 rows, by the dispatch below, so that in blocks of 128 every window reads rows of others: 4096 tokens
+// in blocks of 16, 64 and 128 take 2.9, 4.8 and 7.1 us, 16384 take 6.9, 6.5 and 11.)  It moves 3 bytes per element: 262144
+// rows of 576 in 77 us, 5.9 TB/s (87% of a copy's rate); 16384 in 6.5; few tokens by the launch and three dependent reads
+// (slot, scale, row): 2.0 us for one.
 template <int kWriteWarps, int kRows>
 __global__ void __launch_bounds__(kWriteWarps * 32, kWriteWarps == 8 && kRows < 8 ? 3 : 2)
     mla_cache8_write_kernel(const Cache8 c, const Divide by_page, const Divide by_block, const uint16_t* rows, const int32_t* slots,
